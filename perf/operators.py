@@ -170,8 +170,9 @@ def _prepare_own(s):
             s["ws_bytes"] = max(s["ws_bytes"], qg.ffn_gated_backward_workspace_size(m, k, inter))
     else:
         rows, top = c["rows"], c["top"]
-        for name in ("logp", "entropy", "lse"):
+        for name in ("logp", "entropy"):
             s[name] = torch.empty(rows, **dev)
+        s["stats"] = torch.empty(rows, 2, **dev) if c["train"] else None
         if top:
             s["rank"] = torch.empty(rows, dtype=torch.int32, **dev)
             s["top_ids"] = torch.empty(rows, top, dtype=torch.int32, **dev)
@@ -209,10 +210,10 @@ def _run_own(s):
         return dict(h=h[:, :inter], dx=s["dx"], dw=s["dw"])
     rows, vocab, ld, scale = c["rows"], c["vocab"], s["logits"].stride(0), 1.0 / c["temperature"]
     qg.token_logprobs(s["logits"], s["ltype"], rows, vocab, ld, s["tokens"], scale, c["top"], s["logp"], s["entropy"],
-                      s["lse"], s.get("rank"), s.get("top_ids"), s.get("top_logp"), *ws, stream)
+                      s["stats"], s.get("rank"), s.get("top_ids"), s.get("top_logp"), *ws, stream)
     if not c["train"]:
         return dict(logp=s["logp"], entropy=s["entropy"], rank=s["rank"], top_ids=s["top_ids"], top_logp=s["top_logp"])
-    qg.token_logprobs_backward(s["logits"], s["ltype"], rows, vocab, ld, s["tokens"], scale, s["lse"], s["entropy"],
+    qg.token_logprobs_backward(s["logits"], s["ltype"], rows, vocab, ld, s["tokens"], scale, s["stats"], s["entropy"],
                                s["dlogp"], s["dentropy"], s["dlogits"], ld, stream)
     return dict(logp=s["logp"], entropy=s["entropy"], dlogits=s["dlogits"][:, :vocab])
 
