@@ -39,13 +39,14 @@
  *            bytes).  INT-b codes are two's complement, UINT-b codes are plain,
  *            e2m1 uses bit 3 as its sign, e0m codes bit b-1, e4m3 bit 7.
  *   scales : [N][K/g]: bf16 bit patterns (A16 formats) or e8m0 bytes (MXFP4);
- *            W8A8: fp32 [ceil(N/128)][K/128].
+ *            W8A8: fp32 [ceil(N/128)][K/128]; INT8 x INT8: fp32 [N].
  *   zeros  : [N][K/g] uint8 in 0..2^b-1 for UINT-b formats, NULL otherwise.
  * Activations: x is [rows][ldx] row-major: bf16, e4m3 bytes (MXFP8), or e2m1
  * codes two per byte (MXFP4: element k in the low nibble of byte k/2 when k is
  * even, the high nibble when odd; ldx counts elements), the MX types with
  * x_scales [rows][K/32] e8m0 bytes (row stride K/32), per desc.atype; e4m3
- * bytes with fp32 x_scales [rows] (FP8_TOKEN) or [rows][K/128] (FP8_BLOCK).
+ * bytes with fp32 x_scales [rows] (FP8_TOKEN) or [rows][K/128] (FP8_BLOCK);
+ * int8 with fp32 x_scales [rows] (INT8_TOKEN).
  * y is [rows][ldy] row-major, bf16 or fp32.
  *
  * Numerics (the contract the CPU oracle checks):
@@ -56,6 +57,8 @@
  *   - Per-token FP8: y[r] = s_r * sum_k e4m3(a[r,k]) * Wdq[n,k] (MXFP4 Wdq).
  *   - W8A8: sum over 128-K blocks kb of sa[r][kb] * sw[n/128][kb] * the
  *     block's sum of e4m3 products, each block's partial scaled in fp32.
+ *   - INT8 x INT8: the sum of products is an exact int32; y = its fp32 value
+ *     times the row's scale times the column's scale, two fp32 roundings.
  *   - MXFP4 x MXFP8: e2m1 * 2^(e-127) times e4m3 * 2^(ea-127), exact operands
  *     into gfx950 scaled MFMA; MXFP4 x MXFP4 likewise with e2m1 activations.
  *   - fp32 accumulation; QG_O_BF16 output is the fp32 result rounded to
@@ -107,8 +110,18 @@ typedef enum { QG_S_BF16 = 0, QG_S_E8M0 = 1, QG_S_F32 = 2 } qg_stype;
 /* FP8_TOKEN: e4m3 bytes with one fp32 scale per row (x_scales [rows]).
  * FP8_BLOCK: e4m3 bytes with one fp32 scale per row and 128 K (x_scales
  * [rows][K/128], row stride K/128). */
-typedef enum { QG_A_BF16 = 0, QG_A_MXFP8 = 1, QG_A_MXFP4 = 2, QG_A_FP8_TOKEN = 3, QG_A_FP8_BLOCK = 4 } qg_atype;
+typedef enum {
+  QG_A_BF16 = 0,
+  QG_A_MXFP8 = 1,
+  QG_A_MXFP4 = 2,
+  QG_A_FP8_TOKEN = 3,
+  QG_A_FP8_BLOCK = 4,
+  QG_A_INT8_TOKEN = 6 /* int8 with one fp32 scale per row (x_scales [rows]) */
+} qg_atype;
 typedef enum { QG_O_BF16 = 0, QG_O_F32 = 1 } qg_otype;
+/* Activation of a gated feed-forward block: v / (1 + e^-v), or
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+typedef enum { QG_ACT_SILU = 0, QG_ACT_GELU_TANH = 1 } qg_act;
 
 /* How MoE rows are addressed.  A pair p = t*topk + j is token t's j-th expert
  * choice.  BY_TOKEN: row t of the operand (gate/up input).  BY_PAIR: row p
@@ -147,6 +160,9 @@ typedef enum { QG_ROWS_BY_TOKEN = 0, QG_ROWS_BY_PAIR = 1, QG_ROWS_SORTED = 2 } q
  *   tiled kernels; the skinny kernel (dense below 128 rows, MoE experts with
  *   few rows) widens each activation fragment to e4m3 in registers -- every
  *   e2m1 value is an e4m3 value under the same scale).
+ *   INT8, F32 scales, INT8_TOKEN activations, group = K, K < 2^17, one expert
+ *   (integer products with one scale per output channel and per token; dense
+ *   calls without autotune, and qg_gated_gemm).
  * Other valid combinations return QG_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t abi_version; /* must be QG_ABI_VERSION */
@@ -255,8 +271,13 @@ qg_status qg_gemm_noalloc(const qg_weight *w, const void *x, const void *x_scale
  *   are chosen from (N, K) only, never from m.  Slower than the default at
  *   small m (the large-M kernel serves every m when K % 128 == 0).  An
  *   integer-format layer with m * K * 2 >= 2^31 returns QG_ERR_UNSUPPORTED
- *   rather than switching kernels. */
+ *   rather than switching kernels.  (INT8_TOKEN layers are batch-invariant
+ *   with and without it: their sums are exact.)
+ *   QG_GEMM_QUANTIZE_X (INT8_TOKEN layers; an invalid argument for others): x
+ *   is bf16 [m][ldx] (ldx % 8 == 0) and the call quantizes its rows as
+ *   qg_quantize_int8 does, into ws; x_scales is ignored. */
 #define QG_GEMM_BATCH_INVARIANT 1u
+#define QG_GEMM_QUANTIZE_X 2u
 
 /* qg_gemm_workspace_size for the compute options `flags` (0 = qg_gemm's). */
 qg_status qg_gemm_workspace_size_ex(const qg_weight *w, int64_t m, uint32_t flags, uint64_t *bytes);
@@ -468,6 +489,113 @@ qg_status qg_silu_mul(const void *gu, int32_t gu_type, int64_t rows, int64_t int
 qg_status qg_moe_combine(const void *y, int32_t y_type, int64_t ldy, const float *topk_weights,
                          int64_t num_tokens, int32_t topk, int64_t n, const void *bias, void *out,
                          int32_t out_type, int64_t ldout, hipStream_t stream);
+
+/* bf16 activations -> int8 with one fp32 scale per row, the input of an
+ * INT8_TOKEN layer: scale s = a / 127 in IEEE fp32 with a the row's largest
+ * magnitude (s = 1 for a row of zeros); code = the integer nearest the fp32
+ * quotient v / s (IEEE division), ties to even, in -127 .. 127.
+ *   x        device, bf16 [rows][ldx], 16-B aligned, ldx >= k, ldx % 8 == 0.
+ *   q        device, int8 [rows][ldq], 8-B aligned, ldq >= k, ldq % 8 == 0
+ *            (qg_gemm wants 16-B aligned rows).
+ *   q_scales device, fp32 [rows], 4-B aligned.
+ * k % 8 != 0 or ld too small: QG_ERR_SHAPE.  rows == 0 or k == 0: no-op.  NaN /
+ * Inf inputs give unspecified codes.  Asynchronous on `stream`. */
+qg_status qg_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq,
+                           float *q_scales, hipStream_t stream);
+
+/* The gate / up half of a feed-forward block on an INT8_TOKEN layer in one
+ * kernel: with w the fused layer of n = 2 * inter output channels (gate
+ * 0 .. inter - 1, then up, as in qg_silu_mul),
+ *   h[r][j] = act(y[r][j]) * y[r][inter + j],  y as qg_gemm gives it in fp32,
+ * rounded once to otype.  x, x_scales, ldx, flags, stream as in qg_gemm_ex; h
+ * device [m][ldh], 16-B aligned, ldh >= inter, 4-B aligned rows; ws
+ * qg_gated_gemm_workspace_size bytes, zero-filled once as for qg_gemm.  An odd
+ * n: QG_ERR_SHAPE; layers of other formats: QG_ERR_UNSUPPORTED (qg_gemm and
+ * qg_silu_mul serve them).  m == 0 is a no-op. */
+qg_status qg_gated_gemm_workspace_size(const qg_weight *w, int64_t m, uint32_t flags, uint64_t *bytes);
+qg_status qg_gated_gemm(const qg_weight *w, const void *x, const void *x_scales, int64_t m, int64_t ldx, void *h,
+                        int32_t otype, int64_t ldh, int32_t act, void *ws, uint64_t ws_bytes, uint32_t flags,
+                        hipStream_t stream);
+
+/* The same half of the block in bf16, for models before they are quantized
+ * and for training, in one kernel:
+ *   g = x Wg^T, u = x Wu^T, h = act(g) u   (fp32, rounded once to bf16).
+ *   x   device, bf16 [m][ldx]; w device, bf16 [2 * inter][ldw], the gate rows
+ *       first; both 16-B aligned, ld >= k, ld % 8 == 0, ld <= 2^22, k % 8 == 0.
+ *   h   device, bf16 [m][ldh], 16-B aligned, ldh >= inter.
+ *   gu  device, [m][ldgu] of gu_type, 16-B aligned, ldgu >= 2 * inter, or NULL:
+ *       g in columns 0 .. inter - 1 and u behind it, for the backward pass
+ *       (QG_O_F32 keeps them as computed, QG_O_BF16 takes half the memory and
+ *       rounds them).
+ *   ws  qg_ffn_gated_workspace_size bytes, 256-B aligned, zero-filled once (its
+ *       first 64 KiB suffice); NULL when that size is 0.
+ * No rows, columns or strides beyond these are read or written.  m == 0 is a
+ * no-op.  Asynchronous on `stream`. */
+qg_status qg_ffn_gated_workspace_size(int64_t m, int64_t k, int64_t inter, uint64_t *bytes);
+qg_status qg_ffn_gated(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k, int64_t inter,
+                       int32_t act, void *h, int64_t ldh, void *gu, int32_t gu_type, int64_t ldgu, void *ws,
+                       uint64_t ws_bytes, hipStream_t stream);
+
+/* Backward pass of qg_ffn_gated: with dh the gradient of h,
+ *   du = dh act(g), dg = dh u act'(g)      (fp32, rounded once to bf16)
+ *   dx = dg Wg + du Wu,  dw = [dg du]^T x  (summed in fp32, rounded once).
+ *   x, w  as in the forward pass.  dh device, bf16 [m][lddh], lddh >= inter.
+ *   dx    device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.
+ *   dw    device, [2 * inter][lddw] of dw_type (QG_O_BF16 or QG_O_F32), 16-B
+ *         aligned, lddw >= k, or NULL.  It is overwritten; m == 0 fills it with
+ *         zeros.
+ *   gu    what the forward pass left, or NULL: g and u are computed again.
+ *   ws    qg_ffn_gated_backward_workspace_size bytes (recompute: gu is NULL),
+ *         256-B aligned, zero-filled once as above.
+ * Asynchronous on `stream`. */
+qg_status qg_ffn_gated_backward_workspace_size(int64_t m, int64_t k, int64_t inter, int32_t recompute,
+                                               uint64_t *bytes);
+qg_status qg_ffn_gated_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *dh, int64_t lddh,
+                                int64_t m, int64_t k, int64_t inter, int32_t act, void *dx, int64_t lddx, void *dw,
+                                int32_t dw_type, int64_t lddw, const void *gu, int32_t gu_type, int64_t ldgu,
+                                void *ws, uint64_t ws_bytes, hipStream_t stream);
+
+/* Log probabilities of given tokens, with entropy, rank and the top
+ * alternatives of every row, from logits as a head layer's GEMM writes them:
+ * with z = scale * logits (scale = 1 / temperature),
+ *   logp[r] = z[t_r] - log sum_v exp(z[v]),  entropy[r] = -sum_v p_v log p_v,
+ *   rank[r] = the number of logits greater than the token's,
+ *   top_ids / top_logp [r][top] = the largest logits' ids and log
+ *   probabilities, equal logits in the order of their ids.
+ *   logits  device, [rows][ldl] of ltype (QG_O_BF16 / QG_O_F32), ldl >= vocab;
+ *           any element alignment (rows on 16 bytes are faster).
+ *   tokens  device int32 [rows], or NULL (then logp and rank are NULL).  A
+ *           token outside 0 .. vocab - 1 has logp NaN and rank -1.
+ *   stats   device fp32 [rows][2]: the largest logit and
+ *           log sum_v exp(z[v] - max z), for the backward pass; logp, entropy, stats, rank, top_ids and top_logp
+ *           may each be NULL (top > 0: not both of the last two).
+ *   top     0 .. QG_MAX_ALTERNATIVES.
+ *   ws      qg_token_logprobs_workspace_size bytes, 256-B aligned, zero-filled
+ *           once (its first 64 KiB suffice) and left so; NULL when that is 0.
+ * A logit of -inf is a masked token: probability 0 and never an alternative;
+ * alternatives that do not exist have id -1 and log probability -inf.  A row
+ * with every token masked: logp -inf, entropy 0, rank 0, stats (0, -inf).  NaN
+ * or +inf logits make logp, entropy and top_logp of their row NaN; a NaN is
+ * never an alternative.  vocab <= 2^24.  rows == 0 is a no-op.  Asynchronous. */
+#define QG_MAX_ALTERNATIVES 32
+qg_status qg_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top, uint64_t *bytes);
+qg_status qg_token_logprobs(const void *logits, int32_t ltype, int64_t rows, int64_t vocab, int64_t ldl,
+                            const int32_t *tokens, float scale, int32_t top, float *logp, float *entropy,
+                            float *stats, int32_t *rank, int32_t *top_ids, float *top_logp, void *ws,
+                            uint64_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the logits from those of logp (dlogp, fp32 [rows] or NULL) and of
+ * the entropy (dentropy, fp32 [rows] or NULL; entropy as the forward pass gave
+ * it), with stats of the forward pass on the same logits and scale:
+ *   dlogits[r][v] = scale * (dlogp (1{v = t_r} - p_v) - dentropy p_v (log p_v + entropy)).
+ *   dlogits device, [rows][lddl] of ltype, lddl >= vocab; it may be the logits'
+ *   own buffer (same pointer and stride).
+ * Masked tokens and wholly masked rows get 0 (the token itself its dlogp); a
+ * token outside the vocabulary contributes nothing.  Asynchronous. */
+qg_status qg_token_logprobs_backward(const void *logits, int32_t ltype, int64_t rows, int64_t vocab, int64_t ldl,
+                                     const int32_t *tokens, float scale, const float *stats, const float *entropy,
+                                     const float *dlogp, const float *dentropy, void *dlogits, int64_t lddl,
+                                     hipStream_t stream);
 
 /* Measurement utilities, used for roofline calibration and cold-cache timing.
  * qg_stream_read reads `bytes` (a multiple of 16; src 16-B aligned, device)

@@ -19,7 +19,9 @@ W_INT4, W_UINT4, W_INT3, W_UINT3, W_MXFP4 = 0, 1, 2, 3, 4
 W_INT8, W_UINT8, W_INT2, W_UINT2, W_INT1, W_UINT1, W_E0M3, W_E0M7, W_FP8 = 5, 6, 7, 8, 9, 10, 11, 12, 13
 S_BF16, S_E8M0, S_F32 = 0, 1, 2
 A_BF16, A_MXFP8, A_MXFP4, A_FP8_TOKEN, A_FP8_BLOCK = 0, 1, 2, 3, 4
+A_INT8_TOKEN = 6
 O_BF16, O_F32 = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 ROWS_BY_TOKEN, ROWS_BY_PAIR, ROWS_SORTED = 0, 1, 2
 ABI_VERSION, LAYOUT_VERSION = 1, 2
 
@@ -33,9 +35,13 @@ EXPORTS = (
     "qg_gemm_autotune_workspace_size", "qg_gemm_autotune", "qg_autotune_reset", "qg_quantize_mxfp4",
     "qg_set_override", "qg_clear_overrides", "qg_describe_dispatch_ex", "qg_gemm_noalloc", "qg_quantize_fp8",
     "qg_describe_moe_dispatch", "qg_moe_autotune_workspace_size", "qg_moe_autotune",
+    "qg_quantize_int8", "qg_gated_gemm_workspace_size", "qg_gated_gemm",
+    "qg_ffn_gated_workspace_size", "qg_ffn_gated", "qg_ffn_gated_backward_workspace_size", "qg_ffn_gated_backward",
+    "qg_token_logprobs_workspace_size", "qg_token_logprobs", "qg_token_logprobs_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
-GEMM_BATCH_INVARIANT = 1
+GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X = 1, 2
+MAX_ALTERNATIVES = 32
 
 
 class QGError(RuntimeError):
@@ -106,6 +112,17 @@ def _load():
         "qg_moe_autotune_workspace_size": (I32, [W, I64, I32, ctypes.POINTER(U64)]),
         "qg_moe_autotune": (I32, [W, P, P, I32, P, P, I64, I32, P, I32, I32, P, U64, P, U64, I32, P,
                                   ctypes.c_char_p, U64, ctypes.POINTER(ctypes.c_float)]),
+        "qg_quantize_int8": (I32, [P, I64, I64, I64, P, I64, P, P]),
+        "qg_gated_gemm_workspace_size": (I32, [W, I64, ctypes.c_uint32, ctypes.POINTER(U64)]),
+        "qg_gated_gemm": (I32, [W, P, P, I64, I64, P, I32, I64, I32, P, U64, ctypes.c_uint32, P]),
+        "qg_ffn_gated_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
+        "qg_ffn_gated": (I32, [P, I64, P, I64, I64, I64, I64, I32, P, I64, P, I32, I64, P, U64, P]),
+        "qg_ffn_gated_backward_workspace_size": (I32, [I64, I64, I64, I32, ctypes.POINTER(U64)]),
+        "qg_ffn_gated_backward": (I32, [P, I64, P, I64, P, I64, I64, I64, I64, I32, P, I64, P, I32, I64, P, I32, I64, P,
+                                        U64, P]),
+        "qg_token_logprobs_workspace_size": (I32, [I64, I64, I32, ctypes.POINTER(U64)]),
+        "qg_token_logprobs": (I32, [P, I32, I64, I64, I64, P, ctypes.c_float, I32, P, P, P, P, P, P, P, U64, P]),
+        "qg_token_logprobs_backward": (I32, [P, I32, I64, I64, I64, P, ctypes.c_float, P, P, P, P, P, I64, P]),
         "qg_autotune_reset": (None, []),
         "qg_set_override": (I32, [ctypes.c_char_p, ctypes.c_char_p]),
         "qg_clear_overrides": (None, []),
@@ -161,7 +178,7 @@ def layer_desc(wtype: int, n: int, k: int, group_size: int, atype: int | None = 
     mx = wtype == W_MXFP4
     atype = (A_MXFP8 if mx else A_BF16) if atype is None else atype
     if stype is None:
-        stype = S_E8M0 if mx else S_F32 if atype == A_FP8_BLOCK else S_BF16
+        stype = S_E8M0 if mx else S_F32 if atype in (A_FP8_BLOCK, A_INT8_TOKEN) else S_BF16
     return LayerDesc(ABI_VERSION, wtype, stype, group_size, atype, num_experts, n, k)
 
 
@@ -217,7 +234,7 @@ def gemm_workspace_size_ex(w: Weight, m: int, flags: int) -> int:
 
 def gemm_ex(w: Weight, x, x_scales, m: int, ldx: int, y, otype: int, ldy: int, ws, ws_bytes: int,
             flags: int, stream=None) -> None:
-    """qg_gemm with compute options (GEMM_BATCH_INVARIANT)."""
+    """qg_gemm with compute options (GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X)."""
     _check(_lib.qg_gemm_ex(ctypes.byref(w), _ptr(x), _ptr(x_scales), m, ldx, _ptr(y), otype, ldy,
                            _ptr(ws), ws_bytes, flags, _stream(stream)), "qg_gemm_ex")
 
@@ -292,6 +309,77 @@ def quantize_mxfp4(x, rows: int, k: int, ldx: int, q, ldq: int, q_scales, stream
     """bf16 x [rows][ldx] -> e2m1 q [rows][ldq elements, two per byte] + e8m0 q_scales [rows][k/32]."""
     _check(_lib.qg_quantize_mxfp4(_ptr(x), rows, k, ldx, _ptr(q), ldq, _ptr(q_scales), _stream(stream)),
            "qg_quantize_mxfp4")
+
+
+def quantize_int8(x, rows: int, k: int, ldx: int, q, ldq: int, q_scales, stream=None) -> None:
+    """bf16 x [rows][ldx] -> int8 q [rows][ldq] + fp32 q_scales [rows]."""
+    _check(_lib.qg_quantize_int8(_ptr(x), rows, k, ldx, _ptr(q), ldq, _ptr(q_scales), _stream(stream)),
+           "qg_quantize_int8")
+
+
+def _size(fn, where: str, *args) -> int:
+    out = ctypes.c_uint64()
+    _check(fn(*args, ctypes.byref(out)), where)
+    return out.value
+
+
+def gated_gemm_workspace_size(w: Weight, m: int, flags: int = 0) -> int:
+    return _size(_lib.qg_gated_gemm_workspace_size, "qg_gated_gemm_workspace_size", ctypes.byref(w), m, flags)
+
+
+def gated_gemm(w: Weight, x, x_scales, m: int, ldx: int, h, otype: int, ldh: int, act: int, ws=None, ws_bytes: int = 0,
+               flags: int = 0, stream=None) -> None:
+    """h = act(gate) * up of an INT8_TOKEN layer of n = 2 * inter output channels, in one kernel."""
+    _check(_lib.qg_gated_gemm(ctypes.byref(w), _ptr(x), _ptr(x_scales), m, ldx, _ptr(h), otype, ldh, act, _ptr(ws),
+                              ws_bytes, flags, _stream(stream)), "qg_gated_gemm")
+
+
+def ffn_gated_workspace_size(m: int, k: int, inter: int) -> int:
+    return _size(_lib.qg_ffn_gated_workspace_size, "qg_ffn_gated_workspace_size", m, k, inter)
+
+
+def ffn_gated(x, ldx: int, w, ldw: int, m: int, k: int, inter: int, act: int, h, ldh: int, ws=None, ws_bytes: int = 0,
+              gu=None, gu_type: int = O_F32, ldgu: int = 0, stream=None) -> None:
+    """bf16 h = act(x Wg^T) * (x Wu^T), w [2 * inter][ldw] with the gate rows first; gu keeps the
+    pre-activations for the backward pass."""
+    _check(_lib.qg_ffn_gated(_ptr(x), ldx, _ptr(w), ldw, m, k, inter, act, _ptr(h), ldh, _ptr(gu), gu_type, ldgu,
+                             _ptr(ws), ws_bytes, _stream(stream)), "qg_ffn_gated")
+
+
+def ffn_gated_backward_workspace_size(m: int, k: int, inter: int, recompute: bool = False) -> int:
+    return _size(_lib.qg_ffn_gated_backward_workspace_size, "qg_ffn_gated_backward_workspace_size", m, k, inter,
+                 int(recompute))
+
+
+def ffn_gated_backward(x, ldx: int, w, ldw: int, dh, lddh: int, m: int, k: int, inter: int, act: int, dx, lddx: int, dw,
+                       dw_type: int, lddw: int, ws, ws_bytes: int, gu=None, gu_type: int = O_F32, ldgu: int = 0,
+                       stream=None) -> None:
+    """dx and dw (each may be None) of ffn_gated from dh; gu None computes the pre-activations again
+    (workspace size with recompute=True)."""
+    _check(_lib.qg_ffn_gated_backward(_ptr(x), ldx, _ptr(w), ldw, _ptr(dh), lddh, m, k, inter, act, _ptr(dx), lddx,
+                                      _ptr(dw), dw_type, lddw, _ptr(gu), gu_type, ldgu, _ptr(ws), ws_bytes,
+                                      _stream(stream)), "qg_ffn_gated_backward")
+
+
+def token_logprobs_workspace_size(rows: int, vocab: int, top: int) -> int:
+    return _size(_lib.qg_token_logprobs_workspace_size, "qg_token_logprobs_workspace_size", rows, vocab, top)
+
+
+def token_logprobs(logits, ltype: int, rows: int, vocab: int, ldl: int, tokens, scale: float, top: int, logp, entropy,
+                   stats=None, rank=None, top_ids=None, top_logp=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """Log probabilities of int32 tokens [rows] under softmax(scale * logits), with entropy, rank, the
+    backward pass's stats [rows][2] and the top alternatives (outputs may be None)."""
+    _check(_lib.qg_token_logprobs(_ptr(logits), ltype, rows, vocab, ldl, _ptr(tokens), scale, top, _ptr(logp),
+                                  _ptr(entropy), _ptr(stats), _ptr(rank), _ptr(top_ids), _ptr(top_logp), _ptr(ws),
+                                  ws_bytes, _stream(stream)), "qg_token_logprobs")
+
+
+def token_logprobs_backward(logits, ltype: int, rows: int, vocab: int, ldl: int, tokens, scale: float, stats, entropy,
+                            dlogp, dentropy, dlogits, lddl: int, stream=None) -> None:
+    """dlogits from the gradients of logp and of the entropy (either may be None); dlogits may be logits."""
+    _check(_lib.qg_token_logprobs_backward(_ptr(logits), ltype, rows, vocab, ldl, _ptr(tokens), scale, _ptr(stats),
+                                           _ptr(entropy), _ptr(dlogp), _ptr(dentropy), _ptr(dlogits), lddl,
+                                           _stream(stream)), "qg_token_logprobs_backward")
 
 
 def silu_mul(gu, gu_type: int, rows: int, inter: int, ldgu: int, h, h_type: int, ldh: int,

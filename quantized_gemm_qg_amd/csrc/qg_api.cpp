@@ -23,12 +23,6 @@ static thread_local int32_t g_last_hip_error = 0;
 constexpr int kNumCUs = 256;  // MI355X compute units (8 XCDs x 32)
 void set_last_hip_error(int32_t e) { g_last_hip_error = e; }
 
-static qg_status hip_status(hipError_t e) {
-  if (e == hipSuccess) return QG_OK;
-  set_last_hip_error((int32_t)e);
-  return QG_ERR_HIP;
-}
-
 static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // ---------------------------------------------------------------------------
@@ -974,7 +968,7 @@ static uint64_t moe_ws_bytes(const qg_weight &w, int64_t pairs, int64_t x_rows_c
   return b;
 }
 
-static qg_status check_weight(const qg_weight *w, Layout *L) {
+qg_status check_weight(const qg_weight *w, Layout *L) {
   if (!w || !w->data) return QG_ERR_INVALID_ARGUMENT;
   qg_status st = make_layout(&w->desc, L);
   if (st != QG_OK) return st;
@@ -1169,7 +1163,12 @@ extern "C" qg_status qg_gemm_workspace_size_ex(const qg_weight *w, int64_t m, ui
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
-  if (!bytes || m < 0 || (flags & ~(uint32_t)QG_GEMM_BATCH_INVARIANT) != 0) return QG_ERR_INVALID_ARGUMENT;
+  if (!bytes || m < 0 || (flags & ~(L.i8 ? kI8Flags : (uint32_t)QG_GEMM_BATCH_INVARIANT)) != 0)
+    return QG_ERR_INVALID_ARGUMENT;
+  if (L.i8) {
+    *bytes = i8_ws_bytes(*w, false, m, flags);
+    return QG_OK;
+  }
   *bytes = dense_ws_bytes(*w, dense_variant(*w, m, flags), m);
   return QG_OK;
 }
@@ -1190,6 +1189,8 @@ extern "C" qg_status qg_gemm_ex(const qg_weight *w, const void *x, const void *x
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8)
+    return i8_product(w, L, false, x, x_scales, m, ldx, y, otype, ldy, QG_ACT_SILU, ws, ws_bytes, flags, stream);
   const qg_layer_desc &d = w->desc;
   if (d.num_experts != 1) return QG_ERR_INVALID_ARGUMENT;
   if (m < 0 || (otype != QG_O_BF16 && otype != QG_O_F32)) return QG_ERR_INVALID_ARGUMENT;
@@ -1266,7 +1267,8 @@ extern "C" qg_status qg_gemm_noalloc(const qg_weight *w, const void *x, const vo
   if (st != QG_OK) return st;
   if (m < 0) return QG_ERR_INVALID_ARGUMENT;
   // the scratch this call needs must fit the static array
-  if (m > 0 && dense_ws_bytes(*w, dense_variant(*w, m, 0), m) > QG_NOALLOC_SCRATCH_BYTES)
+  if (m > 0 && (L.i8 ? i8_ws_bytes(*w, false, m, 0) : dense_ws_bytes(*w, dense_variant(*w, m, 0), m)) >
+                   QG_NOALLOC_SCRATCH_BYTES)
     return QG_ERR_BUFFER_TOO_SMALL;
   if (m == 0) return qg_gemm_ex(w, x, x_scales, m, ldx, y, otype, ldy, nullptr, 0, 0, stream);
   void *ws = nullptr;
@@ -1289,6 +1291,7 @@ extern "C" qg_status qg_moe_workspace_size(const qg_weight *w, int64_t num_token
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   if (!bytes || num_tokens < 0 || topk <= 0) return QG_ERR_INVALID_ARGUMENT;
   const int64_t pairs = num_tokens * topk;
   // the sort's need, or the grouped GEMM's with X indexed by pair (the larger
@@ -1422,6 +1425,7 @@ extern "C" qg_status qg_moe_gemm(const qg_weight *w, const void *x, const void *
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   const qg_weight wk = mx_kernel_weight(*w, L);
   if (num_tokens < 0 || topk <= 0 || (otype != QG_O_BF16 && otype != QG_O_F32))
     return QG_ERR_INVALID_ARGUMENT;
@@ -1478,6 +1482,7 @@ extern "C" qg_status qg_moe_autotune_workspace_size(const qg_weight *w, int64_t 
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   if (!bytes || num_tokens < 0 || topk <= 0) return QG_ERR_INVALID_ARGUMENT;
   const qg_weight wk = mx_kernel_weight(*w, L);
   const int64_t pairs = num_tokens * topk;
@@ -1498,6 +1503,7 @@ extern "C" qg_status qg_moe_autotune(const qg_weight *w, const void *x, const vo
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   const qg_weight wk = mx_kernel_weight(*w, L);
   if (num_tokens < 1 || topk <= 0 || reps < 1 || reps > kTuneMaxReps) return QG_ERR_INVALID_ARGUMENT;
   if (otype != QG_O_BF16 && otype != QG_O_F32) return QG_ERR_INVALID_ARGUMENT;
@@ -1600,6 +1606,7 @@ extern "C" qg_status qg_describe_moe_dispatch(const qg_weight *w, int64_t num_to
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   if (!buf || buf_bytes == 0 || num_tokens < 0 || topk <= 0) return QG_ERR_INVALID_ARGUMENT;
   const qg_weight wk = mx_kernel_weight(*w, L);
   const int64_t pairs = num_tokens * topk;
@@ -1778,6 +1785,7 @@ extern "C" qg_status qg_gemm_autotune_workspace_size(const qg_weight *w, int64_t
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   if (!bytes || m < 0 || w->desc.num_experts != 1) return QG_ERR_INVALID_ARGUMENT;
   if (m == 0) {
     *bytes = 0;
@@ -1796,6 +1804,7 @@ extern "C" qg_status qg_gemm_autotune(const qg_weight *w, const void *x, const v
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
+  if (L.i8) return QG_ERR_UNSUPPORTED;
   const qg_layer_desc &d = w->desc;
   if (d.num_experts != 1 || m < 1 || reps < 1 || reps > kTuneMaxReps) return QG_ERR_INVALID_ARGUMENT;
   if (otype != QG_O_BF16 && otype != QG_O_F32) return QG_ERR_INVALID_ARGUMENT;
@@ -1892,8 +1901,12 @@ extern "C" qg_status qg_describe_dispatch_ex(const qg_weight *w, int64_t m, uint
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
-  if (!buf || buf_bytes == 0 || m < 0 || (flags & ~(uint32_t)QG_GEMM_BATCH_INVARIANT) != 0)
+  if (!buf || buf_bytes == 0 || m < 0 || (flags & ~(L.i8 ? kI8Flags : (uint32_t)QG_GEMM_BATCH_INVARIANT)) != 0)
     return QG_ERR_INVALID_ARGUMENT;
+  if (L.i8) {
+    i8_describe(*w, m, buf, buf_bytes);
+    return QG_OK;
+  }
   if (flags && w->desc.num_experts > 1) return QG_ERR_INVALID_ARGUMENT;
   const Variant v = w->desc.num_experts > 1 ? select_moe(*w, m) : dense_variant(*w, m, flags);
   describe_variant(v, L, w->k_blocks, buf, buf_bytes);

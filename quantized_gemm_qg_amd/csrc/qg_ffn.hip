@@ -1,0 +1,130 @@
+// Gated feed-forward block in bf16, forward and backward:
+//   g = x Wg^T, u = x Wu^T, h = act(g) u
+//   du = dh act(g), dg = dh u act'(g), dx = dg Wg + du Wu, dW = [dg du]^T x
+// The forward is one launch (both projections, the activation and the
+// product, the pre-activations saved on request); the backward is one
+// elementwise pass that leaves [dg du] in bf16 and one product per gradient.
+// [dg du] is rounded to bf16 once because the matrix cores take bf16 operands
+// (fp32 ones run at 1/16 of the rate): the rounding errors of its elements are
+// independent, so each gradient's relative error grows from the output
+// rounding's 1.7e-3 (2-norm) to sqrt(2) times that.
+#include <hip/hip_runtime.h>
+
+#include "qg_device.h"
+#include "qg_internal.h"
+#include "qg_mm.h"
+
+namespace qg {
+
+// [dg du] ([rows_pad][ldd] bf16, ldd >= 2 inter, zeros from 2 inter to ldd and
+// from row m to rows_pad) from the pre-activations and dh; one unit = 4
+// consecutive elements of one half.
+__global__ __launch_bounds__(256) void ffn_dgu_kernel(const void *gu, int gu_f32, int64_t ldgu, const uint16_t *dh,
+                                                      int64_t lddh, int64_t m, int64_t inter, int act, uint16_t *dgu,
+                                                      int64_t ldd) {
+  const int64_t row = blockIdx.y;
+  for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < ldd - inter; c += (int64_t)gridDim.x * 256) {
+    uint16_t *d = dgu + row * ldd;
+    if (c >= inter) {  // padding columns
+      d[inter + c] = 0;
+      continue;
+    }
+    float g, u;
+    if (gu_f32) {
+      const float *p = (const float *)gu + row * ldgu + c;
+      g = p[0];
+      u = p[inter];
+    } else {
+      const uint16_t *p = (const uint16_t *)gu + row * ldgu + c;
+      g = bf16_bits_to_f32(p[0]);
+      u = bf16_bits_to_f32(p[inter]);
+    }
+    const float t = bf16_bits_to_f32(dh[row * lddh + c]);
+    float v, dv;
+    act_both(g, act, &v, &dv);
+    d[c] = (uint16_t)bf16_rne(t * u * dv);
+    d[inter + c] = (uint16_t)bf16_rne(t * v);
+  }
+}
+
+__global__ __launch_bounds__(256) void ffn_zero_kernel(uint8_t *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = 2 * (int64_t)threadIdx.x; c < row_bytes; c += 512) *(uint16_t *)(p + r * ld_bytes + c) = 0;
+}
+
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s) {
+  MmArgs a = {};
+  a.a = (const uint8_t *)c.x;
+  a.lda = c.ldx * 2;
+  a.b = (const uint8_t *)c.w;
+  a.ldb = c.ldw * 2;
+  a.m = (int32_t)c.m;
+  a.n = (int32_t)c.inter;
+  a.kd = (int32_t)c.k;
+  a.y = c.h;
+  a.ldy = c.ldh;
+  a.otype = QG_O_BF16;
+  a.gu = c.gu;
+  a.ldgu = c.ldgu;
+  a.gu_type = c.gu_type;
+  a.act = c.act;
+  a.group_m = 4;
+  return launch_mm<MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 64, 4>>(a, s);
+}
+
+hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
+  const unsigned gx = (unsigned)std::min<int64_t>((ldd - c.inter + 255) / 256, 64);
+  for (int64_t r0 = 0; r0 < c.m; r0 += 65535) {
+    const int64_t rows = std::min<int64_t>(c.m - r0, 65535);
+    const int gel = c.gu_type == QG_O_F32 ? 4 : 2;
+    hipLaunchKernelGGL(ffn_dgu_kernel, dim3(gx, (unsigned)rows), dim3(256), 0, s,
+                       (const void *)((const uint8_t *)c.gu + r0 * c.ldgu * gel), c.gu_type == QG_O_F32, c.ldgu,
+                       (const uint16_t *)dh + r0 * lddh, lddh, rows, c.inter, c.act, (uint16_t *)dgu + r0 * ldd, ldd);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// dx = [dg du] W: contraction over the 2 inter rows of W
+hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s) {
+  MmArgs a = {};
+  a.a = (const uint8_t *)dgu;
+  a.lda = ldd * 2;
+  a.b = (const uint8_t *)c.w;
+  a.ldb = c.ldw * 2;
+  a.m = (int32_t)c.m;
+  a.n = (int32_t)c.k;
+  a.kd = (int32_t)(2 * c.inter);
+  a.y = dx;
+  a.ldy = lddx;
+  a.otype = QG_O_BF16;
+  a.group_m = 4;
+  return launch_mm<MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
+}
+
+// dW = [dg du]^T x: contraction over the tokens
+hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
+                         hipStream_t s) {
+  MmArgs a = {};
+  a.a = (const uint8_t *)dgu;
+  a.lda = ldd * 2;
+  a.b = (const uint8_t *)c.x;
+  a.ldb = c.ldx * 2;
+  a.m = (int32_t)(2 * c.inter);
+  a.n = (int32_t)c.k;
+  a.kd = (int32_t)c.m;
+  a.y = dw;
+  a.ldy = lddw;
+  a.otype = dw_type;
+  a.group_m = 4;
+  return launch_mm<MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
+}
+
+hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s) {
+  hipLaunchKernelGGL(ffn_zero_kernel, dim3((unsigned)std::min<int64_t>(rows, 4096)), dim3(256), 0, s, (uint8_t *)p,
+                     ld_bytes, row_bytes, rows);
+  return hipGetLastError();
+}
+
+}  // namespace qg

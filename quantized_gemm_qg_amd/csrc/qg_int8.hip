@@ -1,0 +1,95 @@
+// int8 x int8 products with one fp32 scale per token and per output channel,
+// and the quantization of bf16 rows that feeds them:
+//   s_r = max_k |x_rk| / 127 (1 for a row of zeros),  q_rk = rint(x_rk / s_r)
+//   y_rn = (float)(sum_k q_rk c_nk) * s_r * t_n
+// The sum is exact in 32 bits (K < 2^17), so a row's result does not depend
+// on the kernel, the tile or the split that computed it.
+#include <hip/hip_runtime.h>
+
+#include "qg_device.h"
+#include "qg_internal.h"
+#include "qg_mm.h"
+
+namespace qg {
+
+// One row per workgroup (grid-stride): the row maximum, then the codes, the
+// row read a second time from L2.  The scale and the quotient are IEEE fp32
+// divisions, the code the nearest integer, ties to even.
+__global__ __launch_bounds__(256) void quantize_int8_kernel(const uint16_t *x, int64_t ldx, int64_t k, uint8_t *q,
+                                                            int64_t ldq, float *qs, int64_t rows) {
+  __shared__ float wave_max[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto load8 = [](const uint16_t *p, float (&v)[8]) {
+    const u32x4 w = *(const u32x4 *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  };
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const uint16_t *xr = x + row * ldx;
+    float m = 0.f;
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < k; c += 2048) {
+      float v[8];
+      load8(xr + c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+    if (lane == 0) wave_max[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+    __syncthreads();  // wave_max is rewritten for the next row
+    const float s = m > 0.f ? m / 127.f : 1.f;
+    for (int64_t c = 8 * (int64_t)threadIdx.x; c < k; c += 2048) {
+      float v[8];
+      load8(xr + c, v);
+      uint32_t w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[h] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[h] |= ((uint32_t)(int)rintf(v[4 * h + i] / s) & 255u) << (8 * i);
+      }
+      *(uint2 *)(q + row * ldq + c) = uint2{w[0], w[1]};
+    }
+    if (threadIdx.x == 0) qs[row] = s;
+  }
+}
+
+hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq, float *qs,
+                                hipStream_t s) {
+  if (rows == 0 || k == 0) return hipSuccess;
+  hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)std::min<int64_t>(rows, 256 * 8)), dim3(256), 0, s,
+                     (const uint16_t *)x, ldx, k, (uint8_t *)q, ldq, qs, rows);
+  return hipGetLastError();
+}
+
+static MmArgs i8_args(const I8Call &c) {
+  MmArgs a = {};
+  a.a = (const uint8_t *)c.x;
+  a.lda = c.ldx;
+  a.b = c.codes;
+  a.ldb = (int64_t)c.k_blocks * 2048;
+  a.m = (int32_t)c.m;
+  a.n = c.n;
+  a.kd = c.k;
+  a.y = c.y;
+  a.ldy = c.ldy;
+  a.otype = c.otype;
+  a.sa = c.x_scales;
+  a.sb = c.scales;
+  a.act = c.act;
+  a.group_m = 4;
+  return a;
+}
+
+hipError_t launch_i8(const I8Call &c, hipStream_t s) {
+  const MmArgs a = i8_args(c);
+  if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 128, 128, 2, 2, 64, 4>>(a, s);
+  return launch_mm<MmCfg<true, kRows, kPacked, false, 128, 128, 2, 2, 64, 4>>(a, s);
+}
+
+}  // namespace qg

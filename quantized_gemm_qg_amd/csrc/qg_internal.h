@@ -30,6 +30,10 @@
 //     * W8A8 e4m3 (block 2048 B, 32 B per lane): the lane's bytes are K 16 q
 //       .. 16 q + 15 and 64 + 16 q .. 64 + 16 q + 15 of the block for column
 //       n = 16 t + l % 16 (the scaled MFMA's 8-bit operand).
+//     * int8 with per-token int8 activations (block 2048 B): two 1-KB halves
+//       of 64 k, in each the lane's 16 bytes are k 128 kb + 64 half + 16 q ..
+//       + 15 of column n = 16 t + l % 16 (the operand of one 16x16x64 int8
+//       MFMA), two's complement.
 //     * e2m1 (block 1024 B, 16 B per lane): the lane's 32 codes k = 128 kb +
 //       32 q + e in standard order (two per byte, low nibble first), i.e. the
 //       16-B chunk of the standard row that one 16x16x128 scaled MFMA lane reads.
@@ -48,6 +52,7 @@
 //           (a whole n-tile) as 256 contiguous bytes.
 //           W8A8: fp32 [n_tile][kb_pad], the scale of the 128 x 128 block
 //           holding n-tile n_tile and k-block kb.
+//           int8 with per-token int8 activations: fp32 [n_pad].
 //   zeros   UINT formats: [n_pad][groups_padded / 8] uint32, group g in nibble
 //           g % 8 of word g / 8; UINT8: [n_pad][groups_padded / 4] uint32,
 //           group g in byte g % 4 of word g / 4.
@@ -78,6 +83,8 @@ inline bool mx_a4(const qg_layer_desc &d) { return d.wtype == QG_W_MXFP4 && d.at
 inline bool mx_tok(const qg_layer_desc &d) { return d.wtype == QG_W_MXFP4 && d.atype == QG_A_FP8_TOKEN; }
 // W8A8 FP8 with block scales (e4m3 x e4m3, fp32 scales)
 inline bool w8a8(const qg_layer_desc &d) { return d.wtype == QG_W_FP8 && d.atype == QG_A_FP8_BLOCK; }
+// int8 weights with one scale per output channel, per-token int8 activations
+inline bool i8_tok(const qg_layer_desc &d) { return d.wtype == QG_W_INT8 && d.atype == QG_A_INT8_TOKEN; }
 // Layers of the MX tiled kernel (MXFP4 weights with MXFP8, MXFP4 or per-token
 // FP8 activations; W8A8)
 inline bool mx_tiled_fmt(const qg_layer_desc &d) { return mx_a8(d) || mx_a4(d) || mx_tok(d) || w8a8(d); }
@@ -137,6 +144,7 @@ struct Layout {
   bool a4 = false;        // MXFP4 activations (two e2m1 codes per byte)
   bool fp4 = false;       // MXFP4 weights x bf16 activations (integer-format layout, bf16 scales)
   bool f8 = false;        // W8A8: e4m3 codes in the 8-bit MFMA operand layout, fp32 block scales
+  bool i8 = false;        // int8 x int8 (per-token and per-channel fp32 scales)
   bool x8 = false;        // one byte per activation element (e4m3)
   int xs_kind = 0;        // activation scales: 0 none, 1 e8m0 per 32, 2 fp32 per row, 3 fp32 per row and 128 K
   uint64_t block_bytes = 0;
@@ -172,8 +180,25 @@ void std_sizes(const qg_layer_desc &d, const Layout &L, uint64_t *codes, uint64_
 void repack_expert(const qg_layer_desc &d, const Layout &L, const uint8_t *codes,
                    const uint8_t *scales, const uint8_t *zeros, uint8_t *dst);
 
-// Thread-local record of the last HIP error.
+// Thread-local record of the last HIP error, and the status of a HIP call.
 void set_last_hip_error(int32_t e);
+inline qg_status hip_status(hipError_t e) {
+  if (e == hipSuccess) return QG_OK;
+  set_last_hip_error((int32_t)e);
+  return QG_ERR_HIP;
+}
+
+// Checks a bound weight against its descriptor; fills the layout.
+qg_status check_weight(const qg_weight *w, Layout *L);
+
+// Products of an int8 layer (qg_ops.cpp): qg_gemm's (gated false) and
+// qg_gated_gemm's, all argument checks included; the workspace both need.
+constexpr uint32_t kI8Flags = QG_GEMM_BATCH_INVARIANT | QG_GEMM_QUANTIZE_X;
+qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void *x, const void *x_scales, int64_t m,
+                     int64_t ldx, void *y, int32_t otype, int64_t ldy, int32_t act, void *ws, uint64_t ws_bytes,
+                     uint32_t flags, hipStream_t stream);
+uint64_t i8_ws_bytes(const qg_weight &w, bool gated, int64_t m, uint32_t flags);
+void i8_describe(const qg_weight &w, int64_t m, char *buf, uint64_t buf_bytes);
 
 // ---------------------------------------------------------------------------
 // kernel launch parameters
@@ -318,6 +343,64 @@ hipError_t launch_silu_mul(const void *gu, bool gu_f32, int64_t rows, int64_t in
                            void *h, int64_t ldh, void *hs, hipStream_t s);
 hipError_t launch_moe_combine(const void *y, bool y_f32, int64_t ldy, const float *wts, int64_t tokens, int topk,
                               int64_t n, const void *bias, void *out, bool out_f32, int64_t ldo, hipStream_t s);
+// int8 products (qg_int8.hip): quantized rows (x int8 [m][ldx], x_scales [m])
+// times the packed codes; gated: n outputs from 2 n weight columns.
+struct I8Call {
+  const uint8_t *codes;
+  const float *scales;
+  int32_t n, k, k_blocks;
+  bool gated;
+  int32_t act;
+  const void *x;
+  int64_t ldx;
+  const float *x_scales;
+  int64_t m;
+  void *y;
+  int32_t otype;
+  int64_t ldy;
+};
+hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq, float *qs,
+                                hipStream_t s);
+hipError_t launch_i8(const I8Call &c, hipStream_t s);
+// bf16 gated feed-forward block (qg_ffn.hip); strides in elements
+struct FfnCall {
+  const void *x;
+  int64_t ldx;
+  const void *w;
+  int64_t ldw;
+  int64_t m, k, inter;
+  int32_t act;
+  void *h;
+  int64_t ldh;
+  void *gu;
+  int64_t ldgu;
+  int32_t gu_type;
+};
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s);
+hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s);
+hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s);
+hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
+                         hipStream_t s);
+hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s);
+// token log probabilities (qg_logprobs.hip)
+struct LogprobArgs {
+  const void *logits;
+  bool f32;
+  int64_t rows, vocab, ldl;
+  const int32_t *tokens;
+  float scale;
+  int32_t top;
+  float *logp, *entropy, *stats;
+  int32_t *rank, *top_ids;
+  float *top_logp;
+  // backward
+  const float *dlogp, *dentropy;
+  void *dlogits;
+  int64_t lddl;
+};
+uint64_t logprobs_ws_bytes(int64_t rows, int64_t vocab, int top);
+hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s);
+hipError_t launch_logprobs_backward(const LogprobArgs &a, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

@@ -1,0 +1,406 @@
+// Tiled matrix product of the int8 layers and the bf16 gated feed-forward
+// block: Y[r][c] = sum_k A(r, k) B(c, k), int8 x int8 into int32 or bf16 x bf16
+// into fp32, with three operand forms:
+//
+//   kRows    the operand's rows run along k ([row][pitch], k contiguous):
+//            activations, bf16 weights, the gradient of the pre-activations
+//   kPacked  int8 weights in the packed layout (1-KB pieces of 16 columns x 64 k)
+//   kCols    k runs along the rows of the stored matrix ([k][pitch], the
+//            operand's own index contiguous): the backward products contract
+//            over tokens or over the feed-forward index, which no stored
+//            matrix has contiguous, so the fragments are transposed on their
+//            way out of LDS (ds_read_b64_tr_b16) instead of in memory
+//
+// A workgroup computes a BM x BN tile with WM x WN waves as blocks of 16 x 16
+// (v_mfma_i32_16x16x64_i8 / v_mfma_f32_16x16x32_bf16: both take 64 bytes of k
+// per row, 16 per lane).  The operands go through a ring of ST stages of KB
+// bytes of k, filled by global_load_lds_dwordx4 (1 KB per wave and copy, no
+// register staging): stage s + ST - 1 is issued right after the barrier that
+// publishes stage s, so ST - 2 whole stages stay in flight behind the one that
+// lands.  Bank conflicts: row chunks of 16 bytes sit at slot chunk ^ f(row), the
+// 32-byte column units of kCols at unit ^ f(k); packed pieces are read in the
+// order they are stored.  Past the last k both operands read a line of zeros
+// (nothing is multiplied by what lies behind a row), past the last row or
+// column the last valid one (never stored).
+//
+// The weights are the MFMA's first operand, so a lane holds four consecutive
+// columns of one row: the epilogue packs them with one LDS write per block and
+// stores 16 bytes per lane along the rows.
+//
+// Gated: the tile's B columns are half gate and half up columns of the same
+// BN / 2 outputs, and every wave owns both halves of its outputs, so
+// act(g) u is computed on the accumulators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "qg_device.h"
+#include "qg_internal.h"
+
+namespace qg {
+
+enum { kRows = 0, kPacked = 1, kCols = 2 };
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at any element
+
+// bf16 bits, nearest-even (a NaN stays a NaN)
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+// act(g) and its derivative
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == QG_ACT_SILU) return g / (1.f + __expf(-g));
+  const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
+  return 0.5f * g * (1.f + t);
+}
+__device__ __forceinline__ void act_both(float g, int act, float *v, float *dv) {
+  if (act == QG_ACT_SILU) {
+    const float p = 1.f / (1.f + __expf(-g));
+    *v = g * p;
+    *dv = p * (1.f + g * (1.f - p));
+  } else {
+    const float c = 0.7978845608028654f;
+    const float t = tanhf(c * (g + 0.044715f * g * g * g));
+    *v = 0.5f * g * (1.f + t);
+    *dv = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * c * (1.f + 0.134145f * g * g);
+  }
+}
+
+struct MmArgs {
+  const uint8_t *a;  // kRows: [m][lda]; kCols: [kd][lda]
+  int64_t lda;       // bytes
+  const uint8_t *b;  // kRows: [columns][ldb]; kCols: [kd][ldb]; kPacked: the codes
+  int64_t ldb;       // bytes; kPacked: bytes of one 16-column strip
+  int32_t m, n;      // output rows and columns (gated: n = inter, B has 2 n columns)
+  int32_t kd;        // contraction length
+  void *y;
+  int64_t ldy;       // elements
+  int32_t otype;
+  const float *sa;   // int8: scale of each row, of each B column
+  const float *sb;
+  void *gu;          // gated: the pre-activations, or NULL
+  int64_t ldgu;
+  int32_t gu_type;
+  int32_t act;
+  int32_t group_m;
+};
+
+// 16 zero bytes that copies past the last k read
+static __device__ const uint32_t mm_zeros[4] = {0u, 0u, 0u, 0u};
+
+template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, int WN_, int KB_, int ST_>
+struct MmCfg {
+  static constexpr bool I8 = I8_, GATED = GATED_;
+  static constexpr int AF = AF_, BF = BF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, ST = ST_;
+  static constexpr int EL = I8 ? 1 : 2;
+  static constexpr int KE = KB / EL;             // k per stage
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
+  static constexpr int SUB = KB / 64;            // MFMA steps per stage
+  static constexpr int A = BM * KB, B = BN * KB, STAGE = A + B;
+  static constexpr int A_COPIES = A / 1024, B_COPIES = B / 1024;
+  static constexpr int A_LOADS = (A_COPIES + WAVES - 1) / WAVES, B_LOADS = (B_COPIES + WAVES - 1) / WAVES;
+  static constexpr int LOADS = A_LOADS + B_LOADS;
+  static constexpr int OUT_NB = GATED ? NB / 2 : NB;                  // 16-column blocks of a wave's output
+  static constexpr int PITCH = 16 * OUT_NB * 4 + 16;                  // bytes of a slab row (fp32)
+  static constexpr int SLAB = 16 * PITCH;
+  static constexpr int LDS = STAGE * ST > WAVES * SLAB ? STAGE * ST : WAVES * SLAB;
+  static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && (!GATED || NB % 2 == 0), "blocks");
+  static_assert(KB == 64 || KB == 128, "stage depth");
+  static_assert(!I8 || AF == kRows, "int8 activations are rows");
+  static_assert(AF != kCols || BM >= 128, "column units for the swizzle");
+  static_assert(BF != kCols || BN >= 128, "column units for the swizzle");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+// chunk order of a row's 16-byte chunks
+template <int KB>
+__device__ __forceinline__ int row_swz(int row) { return KB == 128 ? (row & 7) : ((row >> 1) & 3); }
+// unit order of a k row's 32-byte column units
+__device__ __forceinline__ int col_swz(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  typedef typename std::conditional<C::I8, i32x4, f32x4>::type Acc;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int q = lane >> 4, r16 = lane & 15;
+  constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;  // output columns per tile
+
+  int tm, tn;
+  if (!tile_of(blockIdx.x, (a.m + C::BM - 1) / C::BM, (a.n + OUT_BN - 1) / OUT_BN, a.group_m, &tm, &tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * OUT_BN;
+  const int rows = min(C::BM, a.m - m0);
+
+  // B column of block jb of the tile (the up half of a gated tile starts at
+  // column n), not clamped; and the last valid one of its half
+  auto b_col = [&](int jb, int r, bool *up) {
+    if constexpr (C::GATED) {
+      const int w = jb / C::NB, j = jb % C::NB;
+      *up = j >= C::NB / 2;
+      return n0 + (w * (C::NB / 2) + (j % (C::NB / 2))) * 16 + r;
+    } else {
+      *up = false;
+      return n0 + jb * 16 + r;
+    }
+  };
+
+  // source offset of each copy of this wave (from a 64-bit base per operand),
+  // and the k, inside a stage, of the 16 bytes
+  uint32_t a_off[C::A_LOADS], b_off[C::B_LOADS];
+  int a_k[C::A_LOADS], b_k[C::B_LOADS];
+  bool b_up[C::B_LOADS];
+  auto a_copy = [&](int i) { return min(wave * C::A_LOADS + i, C::A_COPIES - 1); };
+  auto b_copy = [&](int i) { return min(wave * C::B_LOADS + i, C::B_COPIES - 1); };
+  constexpr int CPR = C::KB / 16;  // chunks per row
+#pragma unroll
+  for (int i = 0; i < C::A_LOADS; ++i) {
+    if constexpr (C::AF == kRows) {
+      const int row = a_copy(i) * (64 / CPR) + lane / CPR;
+      const int c = (lane % CPR) ^ row_swz<C::KB>(row);
+      a_off[i] = (uint32_t)((int64_t)min(row, rows - 1) * a.lda + 16 * c);
+      a_k[i] = 16 * c / C::EL;
+    } else {
+      const int k = a_copy(i) * (512 / C::BM) + lane / (C::BM / 8), s = lane % (C::BM / 8);
+      const int col = 16 * ((s >> 1) ^ col_swz(k)) + 8 * (s & 1);
+      a_off[i] = (uint32_t)(k * a.lda + 2 * min(col, ((a.m + 7) & ~7) - 8 - m0));
+      a_k[i] = k;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_LOADS; ++i) {
+    if constexpr (C::BF == kRows) {
+      const int row = b_copy(i) * (64 / CPR) + lane / CPR;
+      const int c = (lane % CPR) ^ row_swz<C::KB>(row);
+      const int col = b_col(row / 16, row % 16, &b_up[i]);
+      b_off[i] = (uint32_t)((int64_t)(min(col, a.n - 1) - n0) * a.ldb + 16 * c);
+      b_k[i] = 16 * c / C::EL;
+    } else if constexpr (C::BF == kPacked) {
+      const int jb = b_copy(i) / C::SUB, half = b_copy(i) % C::SUB;
+      int col = min(b_col(jb, r16, &b_up[i]), a.n - 1);
+      const int first = b_up[i] ? (a.n + n0) / 16 : n0 / 16;  // strip of the base below
+      if (b_up[i]) col += a.n;
+      b_off[i] = (uint32_t)((int64_t)(col / 16 - first) * a.ldb + half * 1024 + q * 256 + (col % 16) * 16);
+      b_k[i] = 0;  // padded with zeros to whole 128-k blocks
+    } else {
+      const int k = b_copy(i) * (512 / C::BN) + lane / (C::BN / 8), s = lane % (C::BN / 8);
+      const int col = 16 * ((s >> 1) ^ col_swz(k)) + 8 * (s & 1);
+      b_off[i] = (uint32_t)(k * a.ldb + 2 * min(col, ((a.n + 7) & ~7) - 8 - n0));
+      b_k[i] = k;
+      b_up[i] = false;
+    }
+  }
+  const uint8_t *a_base = a.a + (C::AF == kRows ? (int64_t)m0 * a.lda : (int64_t)m0 * 2);
+  const uint8_t *b_base, *b_base_up;
+  if constexpr (C::BF == kRows) {
+    b_base = a.b + (int64_t)n0 * a.ldb;
+    b_base_up = b_base + (int64_t)a.n * a.ldb;
+  } else if constexpr (C::BF == kPacked) {
+    b_base = a.b + (int64_t)(n0 / 16) * a.ldb;
+    b_base_up = a.b + (int64_t)((a.n + n0) / 16) * a.ldb;
+  } else {
+    b_base = b_base_up = a.b + (int64_t)n0 * 2;
+  }
+  // bytes from one stage to the next
+  const int64_t a_step = C::AF == kRows ? C::KB : (int64_t)C::KE * a.lda;
+  const int64_t b_step = C::BF == kRows ? C::KB : C::BF == kPacked ? 1024 * C::SUB : (int64_t)C::KE * a.ldb;
+  const int steps = (a.kd + C::KE - 1) / C::KE;
+  const bool ragged = a.kd % C::KE != 0;
+
+  auto issue = [&](int s) {
+    uint8_t *st = smem + (s % C::ST) * C::STAGE;
+    const uint8_t *as = a_base + s * a_step;
+    if (!ragged || s + 1 < steps) {
+#pragma unroll
+      for (int i = 0; i < C::A_LOADS; ++i) lds_dma16(as + a_off[i], st + a_copy(i) * 1024);
+#pragma unroll
+      for (int i = 0; i < C::B_LOADS; ++i)
+        lds_dma16((b_up[i] ? b_base_up : b_base) + s * b_step + b_off[i], st + C::A + b_copy(i) * 1024);
+    } else {
+      const int left = a.kd - s * C::KE;
+#pragma unroll
+      for (int i = 0; i < C::A_LOADS; ++i)
+        lds_dma16(a_k[i] < left ? as + a_off[i] : (const uint8_t *)mm_zeros, st + a_copy(i) * 1024);
+#pragma unroll
+      for (int i = 0; i < C::B_LOADS; ++i)
+        lds_dma16(b_k[i] < left ? (b_up[i] ? b_base_up : b_base) + s * b_step + b_off[i] : (const uint8_t *)mm_zeros,
+                  st + C::A + b_copy(i) * 1024);
+    }
+  };
+
+  // fragment of 16 rows (or columns) `blk` of an operand, MFMA step u
+  auto rows_frag = [&](const uint8_t *op, int blk, int u) {
+    const int row = blk * 16 + r16;
+    return *(const u32x4 *)(op + row * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(row)));
+  };
+  auto cols_frag = [&](const uint8_t *op, int width, int blk, int u) {
+    // k 32 u + 8 q + 0..3 and + 4..7 of column 16 blk + r16: within 16 lanes,
+    // lane i names k row i / 4 and columns 4 (i % 4) .. + 3 and receives column i
+    u32x4 v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = 32 * u + 8 * q + 4 * h + (r16 >> 2);
+      const uint8_t *p = op + k * (2 * width) + 32 * (blk ^ col_swz(k)) + 8 * (r16 & 3);
+      const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
+      const uint2 w = __builtin_bit_cast(uint2, t);
+      v[2 * h] = w.x;
+      v[2 * h + 1] = w.y;
+    }
+    return v;
+  };
+  auto a_frag = [&](const uint8_t *st, int i, int u) {
+    if constexpr (C::AF == kRows) return rows_frag(st, wm * C::MB + i, u);
+    else return cols_frag(st, C::BM, wm * C::MB + i, u);
+  };
+  auto b_frag = [&](const uint8_t *st, int j, int u) {
+    const int blk = wn * C::NB + j;
+    if constexpr (C::BF == kRows) return rows_frag(st + C::A, blk, u);
+    else if constexpr (C::BF == kPacked) return *(const u32x4 *)(st + C::A + (blk * C::SUB + u) * 1024 + 16 * lane);
+    else return cols_frag(st + C::A, C::BN, blk, u);
+  };
+
+  Acc acc[C::MB][C::NB];
+#pragma unroll
+  for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+
+#pragma unroll
+  for (int s = 0; s < C::ST - 1; ++s)
+    if (s < steps) issue(s);
+  for (int s = 0; s < steps; ++s) {
+    // stage s has landed when only the loads of the stages behind it are out
+    const int behind = min(C::ST - 2, steps - 1 - s);
+    if (behind >= 3) {
+      QG_WAIT_VMCNT(3 * C::LOADS);
+    } else if (behind == 2) {
+      QG_WAIT_VMCNT(2 * C::LOADS);
+    } else if (behind == 1) {
+      QG_WAIT_VMCNT(C::LOADS);
+    } else {
+      QG_WAIT_VMCNT(0);
+    }
+    __builtin_amdgcn_s_barrier();  // stage s is in LDS for every wave, stage s - 1 is free
+    if (s + C::ST - 1 < steps) issue(s + C::ST - 1);
+    const uint8_t *st = smem + (s % C::ST) * C::STAGE;
+#pragma unroll
+    for (int u = 0; u < C::SUB; ++u) {
+      u32x4 bf[C::NB];
+#pragma unroll
+      for (int j = 0; j < C::NB; ++j) bf[j] = b_frag(st, j, u);
+#pragma unroll
+      for (int i = 0; i < C::MB; ++i) {
+        const u32x4 af = a_frag(st, i, u);
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j) {
+          if constexpr (C::I8)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, bf[j]),
+                                                              __builtin_bit_cast(i32x4, af), acc[i][j], 0, 0, 0);
+          else
+            acc[i][j] = mfma_bf16(bf[j], af, acc[i][j]);
+        }
+      }
+    }
+  }
+  static_assert(C::ST <= 5 && 3 * C::LOADS < 64, "outstanding loads");
+
+  // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  uint8_t *slab = smem + wave * C::SLAB;
+  const int row_w = m0 + wm * C::MB * 16;           // first row of the wave
+  const int col_w = n0 + wn * C::OUT_NB * 16;       // first output column of the wave
+  // fp32 values of block (i, j), scales applied
+  auto value = [&](int i, int j) {
+    f32x4 v;
+    if constexpr (C::I8) {
+      bool up;
+      int col = b_col(wn * C::NB + j, 4 * q, &up);
+      const float s = a.sa[min(row_w + 16 * i + r16, a.m - 1)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = (float)acc[i][j][e] * s * a.sb[min(col + e, a.n - 1) + (up ? a.n : 0)];
+    } else {
+      v = acc[i][j];
+    }
+    return v;
+  };
+  // writes slab i of `at(j)` to out columns col_w .. of a matrix whose column
+  // 0 is at element `shift` of its rows
+  auto store = [&](int i, auto &&at, void *out, int64_t ld, int otype, int64_t shift) {
+    const int el = otype == QG_O_F32 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < C::OUT_NB; ++j) {
+      const f32x4 v = at(j);
+      uint8_t *p = slab + r16 * C::PITCH + (16 * j + 4 * q) * el;
+      if (otype == QG_O_F32)
+        *(f32x4 *)p = v;
+      else
+        *(uint2 *)p = uint2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, before its reads
+    const int cpr = 16 * C::OUT_NB * el / 16, per = 16 / el;
+    for (int t = lane; t < 16 * cpr; t += 64) {
+      const int rr = t / cpr, c = (t % cpr) * per;
+      const int row = row_w + 16 * i + rr, col = col_w + c;
+      if (row >= a.m || col >= a.n) continue;
+      const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * el);
+      uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * el;
+      if (col + per <= a.n) {
+        *(u32x4_any *)dst = v;
+      } else {
+        for (int b = 0; b < a.n - col; ++b) {
+          const uint32_t w = el == 4 ? v[b] : v[b >> 1] >> (16 * (b & 1));
+          if (el == 4)
+            ((uint32_t *)dst)[b] = w;
+          else
+            ((uint16_t *)dst)[b] = (uint16_t)w;
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the reads, before the slab's next writes
+  };
+#pragma unroll
+  for (int i = 0; i < C::MB; ++i) {
+    if constexpr (C::GATED) {
+      constexpr int H = C::NB / 2;
+      if (a.gu) {
+        store(i, [&](int j) { return value(i, j); }, a.gu, a.ldgu, a.gu_type, 0);
+        store(i, [&](int j) { return value(i, H + j); }, a.gu, a.ldgu, a.gu_type, a.n);
+      }
+      if (a.y)
+        store(i,
+              [&](int j) {
+                const f32x4 g = value(i, j), u = value(i, H + j);
+                f32x4 h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = act_value(g[e], a.act) * u[e];
+                return h;
+              },
+              a.y, a.ldy, a.otype, 0);
+    } else {
+      store(i, [&](int j) { return value(i, j); }, a.y, a.ldy, a.otype, 0);
+    }
+  }
+}
+
+template <class C>
+static hipError_t launch_mm(const MmArgs &a, hipStream_t s) {
+  constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  const int64_t total = (int64_t)((a.m + C::BM - 1) / C::BM) * ((a.n + OUT_BN - 1) / OUT_BN);
+  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
+  auto kern = mm_kernel<C>;
+  hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(C::THREADS), C::LDS, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace qg

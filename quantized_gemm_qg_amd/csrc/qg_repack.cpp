@@ -32,7 +32,8 @@ qg_status make_layout(const qg_layer_desc *d, Layout *out) {
   if (d->abi_version != QG_ABI_VERSION) return QG_ERR_INVALID_ARGUMENT;
   if (d->wtype < QG_W_INT4 || d->wtype > QG_W_FP8) return QG_ERR_INVALID_ARGUMENT;
   if (d->stype < QG_S_BF16 || d->stype > QG_S_F32) return QG_ERR_INVALID_ARGUMENT;
-  if (d->atype < QG_A_BF16 || d->atype > QG_A_FP8_BLOCK) return QG_ERR_INVALID_ARGUMENT;
+  if ((d->atype < QG_A_BF16 || d->atype > QG_A_FP8_BLOCK) && d->atype != QG_A_INT8_TOKEN)
+    return QG_ERR_INVALID_ARGUMENT;
   if (d->n <= 0 || d->k <= 0 || d->num_experts <= 0 || d->group_size <= 0) return QG_ERR_SHAPE;
   if (d->n > (1 << 24) || d->k > (1 << 24) || d->num_experts > 4096) return QG_ERR_UNSUPPORTED;
   if (d->k % 32 != 0 || d->k % d->group_size != 0) return QG_ERR_SHAPE;
@@ -44,6 +45,15 @@ qg_status make_layout(const qg_layer_desc *d, Layout *out) {
     L.f8 = true;
     L.x8 = true;
     L.xs_kind = 3;
+  } else if (i8_tok(*d)) {
+    // int8 x int8: one fp32 scale per output channel; the int32 sums hold
+    // K (-128)^2 < 2^31
+    if (d->stype != QG_S_F32 || d->group_size != d->k || d->k >= (1 << 17) || d->num_experts != 1)
+      return QG_ERR_UNSUPPORTED;
+    L.bits = 8;
+    L.i8 = true;
+    L.x8 = true;
+    L.xs_kind = 2;
   } else if (a16_bits(d->wtype) != 0) {
     if (d->stype != QG_S_BF16 || d->atype != QG_A_BF16) return QG_ERR_UNSUPPORTED;
     if (d->group_size != 32 && d->group_size != 64 && d->group_size != 128) return QG_ERR_UNSUPPORTED;
@@ -56,7 +66,7 @@ qg_status make_layout(const qg_layer_desc *d, Layout *out) {
     // the MX tiled kernel's K step); bf16 activations: the 4-bit integer
     // layout with each e8m0 scale stored as its (exact) bf16 power of two
     if (d->atype == QG_A_MXFP4 && d->k % kBlockK != 0) return QG_ERR_UNSUPPORTED;
-    if (d->atype == QG_A_FP8_BLOCK) return QG_ERR_UNSUPPORTED;
+    if (d->atype == QG_A_FP8_BLOCK || d->atype == QG_A_INT8_TOKEN) return QG_ERR_UNSUPPORTED;
     L.is_mx = d->atype == QG_A_MXFP8 || d->atype == QG_A_MXFP4;
     L.mx_pack = L.is_mx || d->atype == QG_A_FP8_TOKEN;
     L.a4 = d->atype == QG_A_MXFP4;
@@ -67,7 +77,7 @@ qg_status make_layout(const qg_layer_desc *d, Layout *out) {
   L.n_tiles = (int)((d->n + kTileN - 1) / kTileN);
   L.k_blocks = (int)((d->k + kBlockK - 1) / kBlockK);
   L.groups = (int)(d->k / d->group_size);
-  const int groups_in_padded_k = L.k_blocks * kBlockK / d->group_size;
+  const int groups_in_padded_k = L.i8 ? 1 : L.k_blocks * kBlockK / d->group_size;
   L.groups_padded = (int)align_up((uint64_t)groups_in_padded_k, 32);
   L.kb_pad = (int)align_up((uint64_t)L.k_blocks, 4);
   L.block_bytes = 256 * (uint64_t)L.bits;  // 64 lanes x 4 * bits bytes (MX: 16 B per lane)
@@ -76,6 +86,7 @@ qg_status make_layout(const qg_layer_desc *d, Layout *out) {
   L.scales_offset = align_up(L.codes_bytes, 256);
   L.scales_bytes = L.mx_pack ? n_pad * 4 * (uint64_t)L.kb_pad
                    : L.f8    ? (uint64_t)L.n_tiles * L.kb_pad * 4
+                   : L.i8    ? n_pad * 4
                              : n_pad * (uint64_t)L.groups_padded * 2;
   uint64_t end = L.scales_offset + L.scales_bytes;
   if (L.has_zp) {
@@ -259,9 +270,42 @@ static void repack_codes_f8(const qg_layer_desc &d, const Layout &L, const uint8
   }
 }
 
+// int8 for int8 activations: 16 consecutive k of a column per lane of a
+// 1-KB half block (n-tiles t0 .. t1 - 1).
+static void repack_codes_i8(const qg_layer_desc &d, const Layout &L, const uint8_t *codes, uint8_t *dst, int t0,
+                            int t1) {
+  const int64_t n_end = std::min<int64_t>(d.n, (int64_t)t1 * kTileN);
+  for (int64_t n = (int64_t)t0 * kTileN; n < n_end; ++n) {
+    const uint8_t *row = codes + n * d.k;
+    uint8_t *strip = dst + (uint64_t)(n / kTileN) * L.k_blocks * L.block_bytes + (n % kTileN) * 16;
+    // (chunk c of 16 k: block c / 8, half and q c % 8, so consecutive chunks are 256 bytes apart)
+    for (int64_t c = 0; c < d.k / 16; ++c) memcpy(strip + c * 256, row + c * 16, 16);
+  }
+}
+
 void repack_expert(const qg_layer_desc &d, const Layout &L, const uint8_t *codes,
                    const uint8_t *scales, const uint8_t *zeros, uint8_t *dst) {
   memset(dst, 0, L.expert_stride);
+  if (L.i8) {
+    memcpy(dst + L.scales_offset, scales, (uint64_t)d.n * 4);
+    // large layers in parallel; a thread that cannot start leaves its strips
+    // to this one
+    const int parts = d.n * d.k >= (1 << 22) ? (int)std::min(8u, std::max(1u, std::thread::hardware_concurrency())) : 1;
+    const int per = (L.n_tiles + parts - 1) / parts;
+    std::vector<std::thread> pool;
+    int begun = 1;
+    try {
+      for (; begun < parts; ++begun) {
+        const int t0 = std::min(begun * per, L.n_tiles), t1 = std::min(t0 + per, L.n_tiles);
+        pool.emplace_back([&, t0, t1] { repack_codes_i8(d, L, codes, dst, t0, t1); });
+      }
+    } catch (...) {
+    }
+    repack_codes_i8(d, L, codes, dst, 0, std::min(per, L.n_tiles));
+    if (begun < parts) repack_codes_i8(d, L, codes, dst, std::min(begun * per, L.n_tiles), L.n_tiles);
+    for (auto &th : pool) th.join();
+    return;
+  }
   if (L.f8) {
     repack_codes_f8(d, L, codes, dst);
     // block (n / 128, kb) scale -> every n-tile of the block
@@ -327,6 +371,8 @@ void std_sizes(const qg_layer_desc &d, const Layout &L, uint64_t *codes, uint64_
   *codes = (uint64_t)d.n * d.k * L.bits / 8;
   if (L.f8)
     *scales = (uint64_t)((d.n + 127) / 128) * (d.k / 128) * 4;
+  else if (L.i8)
+    *scales = (uint64_t)d.n * 4;
   else
     *scales = (uint64_t)d.n * (d.k / d.group_size) * ((L.mx_pack || L.fp4) ? 1 : 2);
   *zeros = L.has_zp ? (uint64_t)d.n * (d.k / d.group_size) : 0;

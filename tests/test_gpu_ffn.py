@@ -1,0 +1,247 @@
+"""GPU tests of the bf16 gated feed-forward block, forward and backward,
+against the formulas in 64 bits and, for the gradients, against differences.
+
+Tolerances: fp32 sums of K products are within K 2^-23 of the sum of the
+products' magnitudes (one rounding per product and one per addition), outputs
+and the gradient of the pre-activations are rounded once to bf16 (2^-8)."""
+import math
+
+import pytest
+import torch
+
+import quantized_gemm_qg_amd as qg
+from gpu_harness import require_gpu
+
+pytestmark = pytest.mark.gpu
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+D = torch.float64
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def act64(g, act):
+    """act(g), act'(g)"""
+    if act == qg.ACT_SILU:
+        p = torch.sigmoid(g)
+        return g * p, p * (1 + g * (1 - p))
+    c = math.sqrt(2 / math.pi)
+    t = torch.tanh(c * (g + 0.044715 * g ** 3))
+    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+
+
+class Case:
+    def __init__(self, m, k, inter, act, seed=0, pad=8):
+        gen = torch.Generator().manual_seed(seed)
+        bf = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16)  # noqa: E731
+        self.m, self.k, self.inter, self.act = m, k, inter, act
+        self.x, self.dh = bf(m, k), bf(m, inter)
+        self.w = (torch.randn(2 * inter, k, generator=gen) * (1.5 / math.sqrt(k))).to(torch.bfloat16)
+        self.ldx = self.ldw = k + pad
+        self.lddh = inter + 3
+        self.xd = self._pad(self.x, self.ldx)
+        self.wd = self._pad(self.w, self.ldw)
+        self.dhd = self._pad(self.dh, self.lddh)
+        x, w = self.x.to(D), self.w.to(D)
+        gu = x @ w.T
+        self.e_gu = k * 2 * U32 * (x.abs() @ w.abs().T)   # bound on the error of the fp32 sums
+        self.g, self.u = gu[:, :inter], gu[:, inter:]
+        self.a, self.da = act64(self.g, act)
+        self.h = self.a * self.u
+        dh = self.dh.to(D)
+        self.dgu = torch.cat((dh * self.u * self.da, dh * self.a), 1)
+        self.dx, self.dw = self.dgu @ w, self.dgu.T @ x
+
+    @staticmethod
+    def _pad(t, ld):
+        """Rows with a longer pitch, NaN behind them."""
+        d = torch.full((t.shape[0], ld), float("nan"), dtype=t.dtype, device="cuda")
+        d[:, :t.shape[1]] = t.cuda()
+        return d
+
+    def e_h(self):
+        eg, eu = self.e_gu[:, :self.inter], self.e_gu[:, self.inter:]
+        # |act'| <= 1.13, |act''| <= 0.8, |act(g)| <= |g|; the activation itself in fp32
+        act = 2.0 ** -20 * (1 + self.g.abs())
+        return 1.13 * eg * (self.u.abs() + eu) + self.a.abs() * eu + act * self.u.abs()
+
+    def e_dgu(self):
+        eg, eu = self.e_gu[:, :self.inter], self.e_gu[:, self.inter:]
+        dh, act = self.dh.to(D).abs(), 2.0 ** -20 * (1 + self.g.abs())
+        e_dg = dh * (0.8 * eg * (self.u.abs() + eu) + 1.13 * eu + act * self.u.abs())
+        e_du = dh * (1.13 * eg + act)
+        return torch.cat((e_dg, e_du), 1) + U16 * self.dgu.abs()
+
+    def forward(self, gu_type=None):
+        m, i = self.m, self.inter
+        ldh = i + 5
+        h = torch.full((m + 1, ldh), 7.0, dtype=torch.bfloat16, device="cuda")
+        gu, ldgu = None, 0
+        if gu_type is not None:
+            ldgu = 2 * i + 3
+            gu = torch.full((m + 1, ldgu), 7.0, dtype=torch.float32 if gu_type == qg.O_F32 else torch.bfloat16, device="cuda")
+        wsb = qg.ffn_gated_workspace_size(m, self.k, i)
+        self.fws = torch.zeros(max(wsb, 1), dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            qg.ffn_gated(self.xd, self.ldx, self.wd, self.ldw, m, self.k, i, self.act, h, ldh, self.fws, wsb, gu=gu,
+                         gu_type=gu_type or 0, ldgu=ldgu)
+        assert (h[m:] == 7).all() and (h[:m, i:] == 7).all()
+        if gu is not None:
+            assert (gu[m:] == 7).all() and (gu[:m, 2 * i:] == 7).all()
+        return h[:m, :i].cpu().to(D), gu, ldgu
+
+    def backward(self, gu=None, gu_type=0, ldgu=0, want_dx=True, dw_type=qg.O_F32, want_dw=True):
+        m, k, i = self.m, self.k, self.inter
+        dx = torch.full((m + 1, k + 8), 7.0, dtype=torch.bfloat16, device="cuda") if want_dx else None
+        dwt = torch.float32 if dw_type == qg.O_F32 else torch.bfloat16
+        dw = torch.full((2 * i + 1, k + 4), 7.0, dtype=dwt, device="cuda") if want_dw else None
+        wsb = qg.ffn_gated_backward_workspace_size(m, k, i, recompute=gu is None)
+        ws = torch.zeros(max(wsb, 1), dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            qg.ffn_gated_backward(self.xd, self.ldx, self.wd, self.ldw, self.dhd, self.lddh, m, k, i, self.act, dx, k + 8, dw,
+                                  dw_type, k + 4, ws, wsb, gu=gu, gu_type=gu_type, ldgu=ldgu)
+        if want_dx:
+            assert (dx[m:] == 7).all() and (dx[:m, k:] == 7).all()
+            dx = dx[:m, :k].cpu().to(D)
+        if want_dw:
+            assert (dw[2 * i:] == 7).all() and (dw[:2 * i, k:] == 7).all()
+            dw = dw[:2 * i, :k].cpu().to(D)
+        return dx, dw
+
+
+def within(got, ref, bound):
+    off = (got - ref).abs() - bound
+    assert (off <= 0).all(), f"{off.max().item():.3g} over the bound"
+
+
+FORWARD = [(1, 8, 1), (1, 4096, 300), (1, 1032, 2048), (2, 264, 17), (5, 512, 130), (16, 2048, 96), (17, 72, 33), (40, 1000, 64),
+           (64, 256, 200), (100, 136, 257), (128, 64, 128), (257, 1032, 281), (600, 40, 90), (1100, 128, 70)]
+
+
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+@pytest.mark.parametrize("m,k,inter", FORWARD)
+def test_forward(m, k, inter, act):
+    print(f"ffn forward m={m} k={k} inter={inter} act={act}", flush=True)
+    c = Case(m, k, inter, act, seed=m + k)
+    h, _, _ = c.forward()
+    within(h, c.h, c.e_h() * (1 + U16) + U16 * c.h.abs() + 1e-37)
+    for t, u in ((qg.O_F32, 0.0), (qg.O_BF16, U16)):
+        h2, gu, _ = c.forward(t)
+        assert torch.equal(h, h2)
+        ref = torch.cat((c.g, c.u), 1)
+        within(gu[:m, :2 * inter].cpu().to(D), ref, c.e_gu * (1 + u) + u * ref.abs() + 1e-37)
+
+
+BACKWARD = [(1, 8, 1), (1, 512, 100), (3, 264, 17), (16, 128, 64), (31, 1000, 130), (65, 72, 33), (128, 256, 192), (257, 1032, 281),
+            (600, 40, 90), (1100, 128, 70)]
+
+
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+@pytest.mark.parametrize("m,k,inter", BACKWARD)
+def test_backward(m, k, inter, act):
+    print(f"ffn backward m={m} k={k} inter={inter} act={act}", flush=True)
+    c = Case(m, k, inter, act, seed=m * 3 + k)
+    e = c.e_dgu()
+    x, w = c.x.to(D).abs(), c.w.to(D).abs()
+    grown = c.dgu.abs() + e
+    b_dx = e @ w + 2 * inter * 2 * U32 * (grown @ w)
+    b_dw = e.T @ x + m * 2 * U32 * (grown.T @ x)
+    _, gu, ldgu = c.forward(qg.O_F32)
+    for saved in (dict(gu=gu, gu_type=qg.O_F32, ldgu=ldgu), {}):
+        dx, dw = c.backward(**saved)
+        within(dx, c.dx, b_dx * (1 + U16) + U16 * c.dx.abs() + 1e-37)
+        within(dw, c.dw, b_dw + 1e-37)
+        # the roundings of the pre-activations' gradient are independent: far nearer in the 2-norm
+        if c.dgu.numel() > 1000:
+            assert (dw - c.dw).norm() <= U16 * c.dw.norm()
+            assert (dx - c.dx).norm() <= 2 * U16 * c.dx.norm()
+    only_dx, none = c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu, want_dw=False)
+    none2, dw16 = c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu, want_dx=False, dw_type=qg.O_BF16)
+    assert none is None and none2 is None
+    again, dw = c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu)
+    assert torch.equal(only_dx, again)
+    assert torch.equal(dw16, dw.to(torch.bfloat16).to(D))
+
+
+def test_backward_from_pre_activations_saved_in_bf16():
+    c = Case(130, 256, 96, qg.ACT_SILU, seed=5)
+    _, gu, ldgu = c.forward(qg.O_BF16)
+    dx, dw = c.backward(gu=gu, gu_type=qg.O_BF16, ldgu=ldgu)
+    # g and u each off by 2^-8 of themselves, then the gradient's own rounding
+    assert (dx - c.dx).norm() <= 5 * U16 * c.dx.norm()
+    assert (dw - c.dw).norm() <= 5 * U16 * c.dw.norm()
+
+
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+def test_gradient_against_differences(act):
+    c = Case(70, 136, 45, act, seed=11)
+    dx, dw = c.backward()
+    gen = torch.Generator().manual_seed(1)
+
+    def loss(x, w):
+        gu = x @ w.T
+        return (c.dh.to(D) * act64(gu[:, :c.inter], act)[0] * gu[:, c.inter:]).sum()
+
+    x, w = c.x.to(D), c.w.to(D)
+    for _ in range(4):
+        vx, vw = torch.randn(x.shape, generator=gen, dtype=D), torch.randn(w.shape, generator=gen, dtype=D)
+        eps = 1e-5
+        slope = (loss(x + eps * vx, w + eps * vw) - loss(x - eps * vx, w - eps * vw)) / (2 * eps)
+        got = (dx * vx).sum() + (dw * vw).sum()
+        # both gradients are within 2^-7 of their norm, the direction is random
+        assert abs(got - slope) <= 2 * U16 * (dx.norm() * vx.norm() + dw.norm() * vw.norm())
+
+
+def test_inf_and_nan_stay_in_their_rows_and_columns():
+    c = Case(40, 72, 33, qg.ACT_SILU, seed=2)   # k ends inside a stage of the ring
+    c.xd[7, 71] = float("nan")
+    c.xd[9, 0] = float("inf")
+    h, _, _ = c.forward()
+    bad = ~torch.isfinite(h)
+    assert bad[7].all() and bad[9].any()
+    bad[7] = bad[9] = False
+    assert not bad.any()
+    clean = [r for r in range(40) if r not in (7, 9)]
+    within(h[clean], c.h[clean], (c.e_h() * (1 + U16) + U16 * c.h.abs())[clean] + 1e-37)
+
+
+def test_no_tokens():
+    c = Case(1, 64, 16, qg.ACT_SILU)
+    dw = torch.full((33, 64), 7.0, device="cuda")
+    qg.ffn_gated(c.xd, c.ldx, c.wd, c.ldw, 0, 64, 16, qg.ACT_SILU, None, 16)
+    qg.ffn_gated_backward(c.xd, c.ldx, c.wd, c.ldw, None, 16, 0, 64, 16, qg.ACT_SILU, None, 64, dw, qg.O_F32, 64, None, 0)
+    assert (dw[:32] == 0).all() and (dw[32] == 7).all()
+
+
+def test_graph_replays():
+    for m in (1, 40):
+        c = Case(m, 256, 64, qg.ACT_SILU, seed=m)
+        h = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda")
+        gu = torch.zeros(m, 128, device="cuda")
+        dx = torch.zeros(m, 256, dtype=torch.bfloat16, device="cuda")
+        dw = torch.zeros(128, 256, device="cuda")
+        wsb = max(qg.ffn_gated_workspace_size(m, 256, 64), qg.ffn_gated_backward_workspace_size(m, 256, 64))
+        ws = torch.zeros(wsb, dtype=torch.uint8, device="cuda")
+
+        def run():
+            qg.ffn_gated(c.xd, c.ldx, c.wd, c.ldw, m, 256, 64, c.act, h, 64, ws, wsb, gu=gu, gu_type=qg.O_F32, ldgu=128)
+            qg.ffn_gated_backward(c.xd, c.ldx, c.wd, c.ldw, c.dhd, c.lddh, m, 256, 64, c.act, dx, 256, dw, qg.O_F32, 256, ws, wsb,
+                                  gu=gu, gu_type=qg.O_F32, ldgu=128)
+
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for rep in range(3):
+            c.dhd[:, :64] = torch.randn(m, 64, device="cuda").to(torch.bfloat16)
+            run()
+            eager = [t.clone() for t in (h, dx, dw)]
+            for t in (h, gu, dx, dw):
+                t.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(eager, (h, dx, dw)))
