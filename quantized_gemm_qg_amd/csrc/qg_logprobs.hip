@@ -7,6 +7,24 @@
 // overflow in c l, and a row of them would lose its maximum.)
 // A logit of -inf is a masked token: probability 0, never an alternative.  A
 // row of nothing else has logp -inf, entropy 0 and gradient 0.
+//
+// One pass over the logits.  A workgroup walks its part of a row in chunks
+// that its threads hold in registers (32 or 128 bytes each), so the
+// maximum, the sums under it and the search for alternatives read memory once.
+// Every thread keeps its own running maximum and sums (no barrier between the
+// maximum and the exponentials); they meet once per workgroup.
+//
+// Alternatives: a bound b that at least `top` logits reach turns the search
+// into a collection of the few logits >= b.  For the first chunk b is the
+// top-th largest of 64 group maxima (4 threads each); afterwards it is the
+// last alternative of the list so far (later ids lose ties, so > b).  The
+// candidates meet the list in LDS and each finds its place by counting the
+// larger keys; keys (value, id) are distinct, so the order of arrival does not
+// matter.  Where ties or an order against the walk give more candidates than
+// the buffer holds, the chunk's alternatives are found one by one.
+//
+// With few rows, several workgroups share a row (arrival counters, the last
+// one joins the parts in their order, so the sums do not depend on timing).
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"
@@ -17,126 +35,478 @@ namespace qg {
 
 namespace {
 
-__device__ __forceinline__ float logit_at(const void *row, bool f32, int64_t i) {
-  return f32 ? ((const float *)row)[i] : bf16_bits_to_f32(((const uint16_t *)row)[i]);
-}
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kCap = 1024;       // candidates of one chunk
+constexpr int kMaxParts = 64;    // workgroups per row
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // Order of alternatives as one key: larger logits first, equal ones by lower
-// id (-0 equals +0); 0 for masked and NaN logits.
+// id (-0 equals +0).
 __device__ __forceinline__ uint64_t alt_key(float l, uint32_t id) {
-  if (!(l > -__builtin_inff())) return 0;
   uint32_t u = __float_as_uint(l + 0.f);
-  if (u == 0x80000000u) u = 0;
   u = (u & 0x80000000u) ? ~u : u | 0x80000000u;
   return ((uint64_t)u << 32) | (0xFFFFFFFFu - id);
 }
-
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, T *lds, F &&op) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) v = op(v, __shfl_xor(v, off));
-  if (lane == 0) lds[wave] = v;
-  __syncthreads();
-  v = lds[0];
-  for (int w = 1; w < waves; ++w) v = op(v, lds[w]);
-  __syncthreads();
-  return v;
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
 }
+__device__ __forceinline__ int key_id(uint64_t k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
+
+// The value of rank `place` (0 = largest) among the 64 lanes' v.
+__device__ __forceinline__ float wave_rank_value(float v, int place) {
+  const int lane = threadIdx.x & 63;
+  int above = 0;
+#pragma unroll 8
+  for (int g = 0; g < 64; ++g) {
+    const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), g));
+    above += (o > v || (o == v && g < lane)) ? 1 : 0;
+  }
+  const int at = __ffsll((unsigned long long)__ballot(above == place)) - 1;
+  return __shfl(v, at);
+}
+
+// Running maximum and sums (log2 scale: the exponent is c2 (l - m))
+struct Sums {
+  float m, s, t;
+};
+// b after a: the sums move under the larger maximum.  t is in units of the
+// exponent (base 2).
+__device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float c2) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == neg_inf()) return Sums{m, a.s + b.s, a.t + b.t};
+  const float da = fmaxf((a.m - m) * c2, -200.f), db = fmaxf((b.m - m) * c2, -200.f);
+  const float fa = exp2f(da), fb = exp2f(db);
+  return Sums{m, a.s * fa + b.s * fb, fa * (a.t + da * a.s) + fb * (b.t + db * b.s)};
+}
+
+struct Shared {
+  uint64_t cand[kCap + QG_MAX_ALTERNATIVES];
+  uint64_t list[QG_MAX_ALTERNATIVES];
+  float group[64];
+  Sums sums[kWaves];
+  uint64_t best[kWaves];
+  int above[kWaves];
+  int count;
+  int flag;
+};
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void logprobs_kernel(LogprobArgs a) {
-  __shared__ uint64_t lds[4];
-  float *ldf = (float *)lds;
-  const float ninf = -__builtin_inff();
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const uint8_t *l = (const uint8_t *)a.logits + row * a.ldl * (a.f32 ? 4 : 2);
-    float m = ninf;
-    for (int64_t i = threadIdx.x; i < a.vocab; i += blockDim.x) m = fmaxf(m, logit_at(l, a.f32, i));
-    m = block_reduce(m, ldf, [](float x, float y) { return fmaxf(x, y); });
-    const bool empty = m == ninf;
-    const float zm = empty ? 0.f : m;
-    const int tok = a.tokens ? a.tokens[row] : -1;
-    const bool in = tok >= 0 && tok < a.vocab;
-    const float lt = in ? logit_at(l, a.f32, tok) : 0.f;
-    float s = 0.f, t = 0.f;
-    int above = 0;
-    for (int64_t i = threadIdx.x; i < a.vocab; i += blockDim.x) {
-      const float x = logit_at(l, a.f32, i);
-      const float d = (x - zm) * a.scale, e = __expf(d);
-      s += e;
-      t += e != 0.f ? e * d : 0.f;
-      above += x > lt;
+template <bool F32, int VEC>
+struct Chunk {
+  static constexpr int EPV = F32 ? 4 : 8;            // logits per 16 bytes
+  static constexpr int SIZE = kThreads * VEC * EPV;  // logits per chunk
+  u32x4 d[VEC];
+
+  // chunk at logit `first` of a row of `vocab`; masked tokens behind its end
+  __device__ __forceinline__ void load(const uint8_t *row, int first, int vocab) {
+    constexpr int EL = F32 ? 4 : 2;
+    constexpr uint32_t none = F32 ? 0xFF800000u : 0xFF80FF80u;
+    if (first + SIZE <= vocab) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+        d[v] = *(const u32x4_any *)(row + (int64_t)(first + (v * kThreads + (int)threadIdx.x) * EPV) * EL);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int i = first + (v * kThreads + (int)threadIdx.x) * EPV;
+        const uint8_t *p = row + (int64_t)i * EL;
+        d[v] = u32x4{none, none, none, none};
+        if (i + EPV <= vocab) {
+          d[v] = *(const u32x4_any *)p;
+        } else if (i < vocab) {
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) {
+            if (i + e >= vocab) continue;
+            if constexpr (F32)
+              d[v][e] = ((const uint32_t *)p)[e];
+            else
+              d[v][e / 2] = (e & 1) ? (d[v][e / 2] & 0xFFFFu) | ((uint32_t)((const uint16_t *)p)[e] << 16)
+                                    : (d[v][e / 2] & 0xFFFF0000u) | ((const uint16_t *)p)[e];
+          }
+        }
+      }
     }
-    auto add = [](float x, float y) { return x + y; };
-    s = block_reduce(s, ldf, add);
-    t = block_reduce(t, ldf, add);
-    above = block_reduce(above, (int *)lds, [](int x, int y) { return x + y; });
-    const float log_s = empty ? ninf : logf(s);
+  }
+  __device__ __forceinline__ float at(int v, int e) const {
+    if constexpr (F32)
+      return __uint_as_float(d[v][e]);
+    else
+      return __uint_as_float((e & 1) ? d[v][e / 2] & 0xFFFF0000u : d[v][e / 2] << 16);
+  }
+  // Forgets what was unpacked: each pass over the chunk unpacks it again (one
+  // instruction per logit) instead of holding it in a register per logit.
+  __device__ __forceinline__ void repack() {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) asm volatile("" : "+v"(d[v]));
+  }
+  __device__ __forceinline__ int id(int first, int v, int e) const {
+    return first + (v * kThreads + (int)threadIdx.x) * EPV + e;
+  }
+};
+
+// Merges sh.cand[0 .. n) and sh.list[0 .. have) into sh.list; returns its
+// length.  All threads call; the candidates are visible before the call.
+__device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) {
+  for (int i = threadIdx.x; i < have; i += kThreads) sh.cand[n + i] = sh.list[i];
+  __syncthreads();
+  const int all = n + have;
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    const uint64_t k = sh.cand[i];
+    int r = 0;
+    for (int j = 0; j < all; ++j) r += sh.cand[j] > k;
+    if (r < top) sh.list[r] = k;
+  }
+  __syncthreads();
+  return min(all, top);
+}
+
+// The chunk's part in the list of alternatives; most: the thread's largest
+// logit of the chunk.  Uniform over the workgroup; returns the list's length.
+template <bool F32, int VEC>
+__device__ __forceinline__ int take_alternatives(Shared &sh, Chunk<F32, VEC> &ch, int first, float most, int have,
+                                                 int top) {
+  using C = Chunk<F32, VEC>;
+  const float last = have == top ? key_value(sh.list[top - 1]) : neg_inf();
+  if (!__syncthreads_or(most > last)) return have;
+  // candidates: l > bound (or >= bound where it is one of the chunk's own)
+  float bound = last;
+  bool own = false;
+  for (int attempt = have == top ? 0 : 1; attempt < 2; ++attempt) {
+    if (attempt == 1) {
+      // the top-th largest of the 64 group maxima
+      float g = fmaxf(most, __shfl_xor(most, 1));
+      g = fmaxf(g, __shfl_xor(g, 2));
+      if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = g;
+      __syncthreads();
+      const float b = wave_rank_value(sh.group[threadIdx.x & 63], top - 1);
+      own = b > bound;
+      bound = own ? b : bound;
+    }
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    ch.repack();
+    if (own ? most >= bound : most > bound) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+#pragma unroll
+        for (int e = 0; e < C::EPV; ++e) {
+          const float l = ch.at(v, e);
+          if (own ? l >= bound : l > bound) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)ch.id(first, v, e));
+          }
+        }
+    }
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kCap) return merge_list(sh, n, have, top);
+    __syncthreads();  // (count is cleared for the next attempt)
+  }
+  // one by one: the largest key below the one before it
+  int n = 0;
+  for (uint64_t below = ~0ull; n < top; ++n) {
+    uint64_t best = 0;
+    ch.repack();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+#pragma unroll
+      for (int e = 0; e < C::EPV; ++e) {
+        const float l = ch.at(v, e);
+        const uint64_t k = alt_key(l, (uint32_t)ch.id(first, v, e));
+        if (l > last && k < below && k > best) best = k;
+      }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)best, off);
+      best = o > best ? o : best;
+    }
+    if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+    __syncthreads();
+    if (best == 0) break;  // uniform
+    if (threadIdx.x == 0) sh.cand[n] = best;
+    below = best;
+  }
+  __syncthreads();
+  return merge_list(sh, n, have, top);
+}
+
+// The record of one part of a row: sums, count and the sorted alternatives.
+__host__ __device__ constexpr int64_t record_bytes(int top) { return 16 + 8 * (int64_t)((top + 1) & ~1); }
+
+template <bool F32, int VEC>
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int parts, uint32_t *counters,
+                                                            uint8_t *records) {
+  using C = Chunk<F32, VEC>;
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int vocab = (int)a.vocab, chunks = (vocab + C::SIZE - 1) / C::SIZE;
+  const float c2 = a.scale * kLog2e;
+  for (int64_t unit = blockIdx.x; unit < a.rows * parts; unit += gridDim.x) {
+    const int64_t row = parts == 1 ? unit : unit / parts;
+    const int part = (int)(unit - row * parts);
+    const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
+    const int tok = a.tokens ? a.tokens[row] : -1;
+    const bool in = tok >= 0 && tok < vocab;
+    const float lt = !in ? __builtin_inff()
+                     : F32 ? ((const float *)lp)[tok] : bf16_bits_to_f32(((const uint16_t *)lp)[tok]);
+    Sums st = {neg_inf(), 0.f, 0.f};
+    int above = 0, have = 0;
+    const int c_end = (int)((int64_t)(part + 1) * chunks / parts);
+    for (int c = (int)((int64_t)part * chunks / parts); c < c_end; ++c) {
+      C ch;
+      ch.load(lp, c * C::SIZE, vocab);
+      float most = neg_inf();
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+#pragma unroll
+        for (int e = 0; e < C::EPV; ++e) most = fmaxf(most, ch.at(v, e));
+      ch.repack();
+      // the running sums under the new maximum
+      const float m = fmaxf(st.m, most);
+      const float base = m == neg_inf() ? 0.f : m;
+      const float back = fmaxf((st.m - base) * c2, -200.f), f = __builtin_amdgcn_exp2f(back);
+      float s = st.s * f, t = f * (st.t + back * st.s);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+        for (int e = 0; e < C::EPV; ++e) {
+          const float l = ch.at(v, e);
+          const float d = (l - base) * c2, x = __builtin_amdgcn_exp2f(d);
+          s += x;
+          t = __builtin_fmaf(x, fmaxf(d, -200.f), t);  // (0 * -inf for masked tokens; a NaN comes in through x)
+          above += __popcll(__ballot(l > lt));         // wave-uniform
+        }
+        __builtin_amdgcn_sched_barrier(0);  // (bounds the masks held at once)
+      }
+      st = Sums{m, s, t};
+      if (a.top > 0) have = take_alternatives(sh, ch, c * C::SIZE, most, have, a.top);
+    }
+    // join the threads, then the waves
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+      st = join(st, Sums{__shfl_xor(st.m, off), __shfl_xor(st.s, off), __shfl_xor(st.t, off)}, c2);
+    if (lane == 0) {
+      sh.sums[wave] = st;
+      sh.above[wave] = above;
+    }
+    __syncthreads();
+    st = sh.sums[0];
+    above = sh.above[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      st = join(st, sh.sums[w], c2);
+      above += sh.above[w];
+    }
+    if (parts > 1) {
+      // publish this part, and let the last workgroup of the row join them:
+      // agent-scope stores, complete before the counter moves
+      const int64_t rb = record_bytes(a.top);
+      uint8_t *rec = records + row * parts * rb;
+      float *rf = (float *)(rec + part * rb);
+      if (threadIdx.x < 4) {
+        const float v = threadIdx.x == 0 ? st.m : threadIdx.x == 1 ? st.s : threadIdx.x == 2 ? st.t : __int_as_float(above);
+        __hip_atomic_store(rf + threadIdx.x, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      if ((int)threadIdx.x < a.top)
+        __hip_atomic_store((uint64_t *)(rf + 4) + threadIdx.x, (int)threadIdx.x < have ? sh.list[threadIdx.x] : 0ull,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (threadIdx.x == 0)
+        sh.flag = __hip_atomic_fetch_add(counters + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                  (uint32_t)(parts - 1);
+      __syncthreads();
+      if (!sh.flag) {  // uniform over the workgroup
+        __syncthreads();
+        continue;
+      }
+      auto word = [&](int p, int i) {
+        return __hip_atomic_load((const float *)(rec + p * rb) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      };
+      auto key = [&](int p, int i) {
+        return __hip_atomic_load((const uint64_t *)(rec + p * rb + 16) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      };
+      st = Sums{neg_inf(), 0.f, 0.f};
+      above = 0;
+      if (lane < parts) {
+        st = Sums{word(lane, 0), word(lane, 1), word(lane, 2)};
+        above = __float_as_int(word(lane, 3));
+      }
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        st = join(st, Sums{__shfl_xor(st.m, off), __shfl_xor(st.s, off), __shfl_xor(st.t, off)}, c2);
+        above += __shfl_xor(above, off);
+      }
+      if (a.top > 0) {
+        // the first `deep` keys of each list hold at least `top` keys: their
+        // top-th largest is a bound that at most max(top^2, parts top) keys of
+        // the sorted lists reach, within the buffer
+        const int deep = (a.top + parts - 1) / parts;
+        const uint64_t mine = lane < parts * deep ? key(lane % parts, lane / parts) : 0;
+        int larger = 0;
+#pragma unroll 8
+        for (int g = 0; g < 64; ++g) {
+          const uint64_t o = ((uint64_t)__builtin_amdgcn_readlane((uint32_t)(mine >> 32), g) << 32) |
+                             (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine, g);
+          larger += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+        }
+        const int at = __ffsll((unsigned long long)__ballot(larger == a.top - 1)) - 1;
+        const uint64_t bound = __shfl((unsigned long long)mine, at);
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < parts * a.top; i += kThreads) {
+          const uint64_t k = key(i / a.top, i % a.top);
+          if (k != 0 && k >= bound) sh.cand[atomicAdd(&sh.count, 1)] = k;
+        }
+        __syncthreads();
+        have = merge_list(sh, sh.count, 0, a.top);
+      }
+      if (threadIdx.x == 0) __hip_atomic_store(counters + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const bool empty = st.m == neg_inf() && st.s == 0.f;
+    const float most = st.m == neg_inf() ? 0.f : st.m;
+    const float log_s = empty ? neg_inf() : logf(st.s);
     if (threadIdx.x == 0) {
-      if (a.logp) a.logp[row] = in ? (empty ? ninf : (lt - zm) * a.scale - log_s) : __builtin_nanf("");
+      if (a.logp) a.logp[row] = !in ? __builtin_nanf("") : empty ? neg_inf() : (lt - most) * a.scale - log_s;
       if (a.rank) a.rank[row] = in ? above : -1;
-      if (a.entropy) a.entropy[row] = empty ? 0.f : log_s - t / s;
+      if (a.entropy) a.entropy[row] = empty ? 0.f : log_s - st.t / st.s * kLn2;
       if (a.stats) {
-        a.stats[2 * row] = zm;
+        a.stats[2 * row] = most;
         a.stats[2 * row + 1] = log_s;
       }
     }
-    uint64_t last = ~0ull;
-    for (int j = 0; j < a.top; ++j) {
-      uint64_t best = 0;
-      for (int64_t i = threadIdx.x; i < a.vocab; i += blockDim.x) {
-        const uint64_t k = alt_key(logit_at(l, a.f32, i), (uint32_t)i);
-        if (k < last && k > best) best = k;
-      }
-      best = block_reduce(best, lds, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
-      if (threadIdx.x == 0) {
-        const int id = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : -1;
-        if (a.top_ids) a.top_ids[row * a.top + j] = id;
-        if (a.top_logp) a.top_logp[row * a.top + j] = best ? (logit_at(l, a.f32, id) - zm) * a.scale - log_s : ninf;
-      }
-      last = best;
+    if ((int)threadIdx.x < a.top) {
+      const bool there = (int)threadIdx.x < have;
+      const uint64_t k = there ? sh.list[threadIdx.x] : 0;
+      if (a.top_ids) a.top_ids[row * a.top + threadIdx.x] = there ? key_id(k) : -1;
+      if (a.top_logp)
+        a.top_logp[row * a.top + threadIdx.x] = there ? (key_value(k) - most) * a.scale - log_s : neg_inf();
     }
+    __syncthreads();  // sh is used again for the next row
   }
 }
 
-__global__ __launch_bounds__(256) void logprobs_backward_kernel(LogprobArgs a) {
-  const float ninf = -__builtin_inff();
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const uint8_t *l = (const uint8_t *)a.logits + row * a.ldl * (a.f32 ? 4 : 2);
-    uint8_t *dl = (uint8_t *)a.dlogits + row * a.lddl * (a.f32 ? 4 : 2);
-    const float zm = a.stats[2 * row], log_s = a.stats[2 * row + 1];
-    const bool empty = log_s == ninf;
+// dl in one pass: 16 bytes per thread and step, VEC steps of a row in flight.
+// Reads and writes of one 16 bytes are the same thread's, so dl may be l.
+template <bool F32, int VEC>
+__global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a, int parts) {
+  using C = Chunk<F32, VEC>;
+  constexpr int EL = F32 ? 4 : 2;
+  const int vocab = (int)a.vocab;
+  const float c2 = a.scale * kLog2e;
+  for (int64_t unit = blockIdx.x; unit < a.rows * parts; unit += gridDim.x) {
+    const int64_t row = parts == 1 ? unit : unit / parts;
+    const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * EL;
+    uint8_t *dp = (uint8_t *)a.dlogits + row * a.lddl * EL;
+    const float most = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+    const bool empty = log_s == neg_inf();
     const int tok = a.tokens ? a.tokens[row] : -1;
-    const bool in = tok >= 0 && tok < a.vocab;
-    const float g = a.dlogp && in ? a.dlogp[row] : 0.f;
-    const float e = a.dentropy ? a.dentropy[row] : 0.f;
-    const float h = a.dentropy ? a.entropy[row] : 0.f;
-    for (int64_t i = threadIdx.x; i < a.vocab; i += blockDim.x) {
-      const float lq = (logit_at(l, a.f32, i) - zm) * a.scale - log_s;
-      const float p = __expf(lq);
-      float v = -g * p;
-      if (p != 0.f) v -= e * p * (lq + h);
-      if (i == tok) v += g;
-      v = empty ? 0.f : v * a.scale;
-      if (a.f32)
-        ((float *)dl)[i] = v;
-      else
-        ((uint16_t *)dl)[i] = (uint16_t)bf16_rne(v);
+    const float g = a.dlogp && tok >= 0 && tok < vocab && !empty ? a.dlogp[row] * a.scale : 0.f;
+    const float e = a.dentropy && !empty ? a.dentropy[row] * a.scale : 0.f;
+    // -p (g + e (log p + H)) = p (w0 - e ln2 q) with q = log2 p
+    const float w0 = -g - (e != 0.f ? e * a.entropy[row] : 0.f), w1 = -e * kLn2, q0 = empty ? 0.f : -log_s * kLog2e;
+    for (int first = (int)(unit - row * parts) * C::SIZE; first < vocab; first += parts * C::SIZE) {
+      C ch;
+      ch.load(lp, first, vocab);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int i = ch.id(first, v, 0);
+        float o[C::EPV];
+#pragma unroll
+        for (int k = 0; k < C::EPV; ++k) {
+          const float q = __builtin_fmaf(ch.at(v, k) - most, c2, q0);
+          o[k] = __builtin_amdgcn_exp2f(q) * __builtin_fmaf(w1, fmaxf(q, -300.f), w0);
+          if (i + k == tok) o[k] += g;
+        }
+        u32x4 w;
+        if constexpr (F32) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(o[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = bf16_rne(o[2 * k]) | (bf16_rne(o[2 * k + 1]) << 16);
+        }
+        if (empty) w = u32x4{0u, 0u, 0u, 0u};
+        uint8_t *p = dp + (int64_t)i * EL;
+        if (i + C::EPV <= vocab) {
+          *(u32x4_any *)p = w;
+        } else {
+          for (int k = 0; k < vocab - i; ++k) {
+            if constexpr (F32)
+              ((uint32_t *)p)[k] = w[k];
+            else
+              ((uint16_t *)p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      }
     }
   }
 }
 
-uint64_t logprobs_ws_bytes(int64_t, int64_t, int) { return 0; }
+namespace {
+// Chunks of 2 x 16 bytes per thread while 8 x 16 would leave CUs without a
+// workgroup; then rows are shared by so many workgroups that each CU gets
+// about four (at most one chunk each, kMaxParts).
+struct Split {
+  bool small;
+  int parts;
+};
+Split logprobs_split(int64_t rows, int64_t vocab, bool f32) {
+  const int64_t big = (f32 ? 4 : 8) * kThreads * 8;
+  const bool small = rows * ((vocab + big - 1) / big) < 256;
+  const int64_t size = small ? big / 4 : big, chunks = (vocab + size - 1) / size;
+  const int64_t want = (1024 + rows - 1) / rows;
+  return Split{small, (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, chunks), kMaxParts))};
+}
+}  // namespace
 
-hipError_t launch_logprobs(const LogprobArgs &a, void *, hipStream_t s) {
-  hipLaunchKernelGGL(logprobs_kernel, dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(256), 0, s, a);
+uint64_t logprobs_ws_bytes(int64_t rows, int64_t vocab, int top) {
+  if (rows <= 0 || vocab <= 0) return 0;
+  uint64_t b = 0;
+  for (bool f32 : {false, true}) {
+    const Split s = logprobs_split(rows, vocab, f32);
+    if (s.parts > 1) b = std::max<uint64_t>(b, kSplitCounterBytes + align_up((uint64_t)(rows * s.parts * record_bytes(top)), 256));
+  }
+  return b;
+}
+
+hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s) {
+  const Split sp = logprobs_split(a.rows, a.vocab, a.f32);
+  const dim3 grid((unsigned)std::min<int64_t>(a.rows * sp.parts, 1 << 20));
+  uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 1024
+  uint8_t *records = (uint8_t *)ws + kSplitCounterBytes;
+  if (a.f32) {
+    if (sp.small)
+      hipLaunchKernelGGL((logprobs_kernel<true, 2>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+    else
+      hipLaunchKernelGGL((logprobs_kernel<true, 8>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+  } else {
+    if (sp.small)
+      hipLaunchKernelGGL((logprobs_kernel<false, 2>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+    else
+      hipLaunchKernelGGL((logprobs_kernel<false, 8>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_logprobs_backward(const LogprobArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(logprobs_backward_kernel, dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(256), 0, s, a);
+  const int64_t size = (a.f32 ? 4 : 8) * kThreads * 4;
+  const int64_t chunks = (a.vocab + size - 1) / size;
+  // one workgroup per chunk up to about eight per CU, then more chunks each
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (2048 + a.rows - 1) / a.rows));
+  const dim3 grid((unsigned)std::min<int64_t>(a.rows * parts, 1 << 20));
+  if (a.f32)
+    hipLaunchKernelGGL((logprobs_backward_kernel<true, 4>), grid, dim3(kThreads), 0, s, a, parts);
+  else
+    hipLaunchKernelGGL((logprobs_backward_kernel<false, 4>), grid, dim3(kThreads), 0, s, a, parts);
   return hipGetLastError();
 }
 
