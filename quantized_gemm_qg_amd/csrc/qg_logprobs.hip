@@ -56,6 +56,20 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ int key_id(uint64_t k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
 
+// The largest of three (a NaN loses against a number).  Written out because
+// fmaxf first quiets every operand of unknown origin, an instruction each.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// The next number above l (the most negative one above -inf); l is no NaN.
+__device__ __forceinline__ float next_above(float l) {
+  const uint32_t u = __float_as_uint(l + 0.f);
+  return u == 0x7F800000u ? l : __uint_as_float((u & 0x80000000u) ? u - 1 : u + 1);
+}
+
 // The value of rank `place` (0 = largest) among the 64 lanes' v.
 __device__ __forceinline__ float wave_rank_value(float v, int place) {
   const int lane = threadIdx.x & 63;
@@ -99,37 +113,47 @@ struct Shared {
 template <bool F32, int VEC>
 struct Chunk {
   static constexpr int EPV = F32 ? 4 : 8;            // logits per 16 bytes
+  static constexpr int EL = F32 ? 4 : 2;
+  static constexpr uint32_t NONE = F32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
   static constexpr int SIZE = kThreads * VEC * EPV;  // logits per chunk
   u32x4 d[VEC];
 
-  // chunk at logit `first` of a row of `vocab`; masked tokens behind its end
-  __device__ __forceinline__ void load(const uint8_t *row, int first, int vocab) {
-    constexpr int EL = F32 ? 4 : 2;
-    constexpr uint32_t none = F32 ? 0xFF800000u : 0xFF80FF80u;
+  // Chunk at logit `first` of a row of `vocab`.  16 bytes that the row's end
+  // cuts are read whole, ending with the row, and what is the neighbour's of
+  // them is masked; so is everything behind the end.
+  __device__ __forceinline__ void load(const uint8_t *row, int first, int base, int vocab) {
     if (first + SIZE <= vocab) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v)
-        d[v] = *(const u32x4_any *)(row + (int64_t)(first + (v * kThreads + (int)threadIdx.x) * EPV) * EL);
-    } else {
+      for (int v = 0; v < VEC; ++v) d[v] = *(const u32x4_any *)(row + (int64_t)place(base, v) * EL);
+      return;
+    }
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const int i = first + (v * kThreads + (int)threadIdx.x) * EPV;
-        const uint8_t *p = row + (int64_t)i * EL;
-        d[v] = u32x4{none, none, none, none};
-        if (i + EPV <= vocab) {
-          d[v] = *(const u32x4_any *)p;
-        } else if (i < vocab) {
+    for (int v = 0; v < VEC; ++v) load16(v, row, place(base, v), vocab);
+  }
+  // the 16 bytes of logits i ..
+  __device__ __forceinline__ void load16(int v, const uint8_t *row, int i, int vocab) {
+    d[v] = u32x4{NONE, NONE, NONE, NONE};
+    if (i >= vocab) return;
+    if (vocab < EPV) {  // (a row of less than 16 bytes: i is 0)
+      for (int e = 0; e < vocab; ++e) set(v, e, F32 ? ((const uint32_t *)row)[e] : ((const uint16_t *)row)[e]);
+      return;
+    }
+    const int at = min(i, vocab - EPV);
+    d[v] = *(const u32x4_any *)(row + (int64_t)at * EL);
+    if (at < i) {
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            if (i + e >= vocab) continue;
-            if constexpr (F32)
-              d[v][e] = ((const uint32_t *)p)[e];
-            else
-              d[v][e / 2] = (e & 1) ? (d[v][e / 2] & 0xFFFFu) | ((uint32_t)((const uint16_t *)p)[e] << 16)
-                                    : (d[v][e / 2] & 0xFFFF0000u) | ((const uint16_t *)p)[e];
-          }
-        }
-      }
+      for (int e = 0; e < EPV - 1; ++e)
+        if (at + e < i) set(v, e, NONE);
+    }
+  }
+  // replaces one logit by its bits (the low ones of `bits`)
+  __device__ __forceinline__ void set(int v, int e, uint32_t bits) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if constexpr (F32)
+        d[v][w] = w == e ? bits : d[v][w];
+      else if (w == e >> 1)
+        d[v][w] = (e & 1) ? (d[v][w] & 0xFFFFu) | (bits << 16) : (d[v][w] & 0xFFFF0000u) | (bits & 0xFFFFu);
     }
   }
   __device__ __forceinline__ float at(int v, int e) const {
@@ -138,14 +162,18 @@ struct Chunk {
     else
       return __uint_as_float((e & 1) ? d[v][e / 2] & 0xFFFF0000u : d[v][e / 2] << 16);
   }
-  // Forgets what was unpacked: each pass over the chunk unpacks it again (one
-  // instruction per logit) instead of holding it in a register per logit.
-  __device__ __forceinline__ void repack() {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) asm volatile("" : "+v"(d[v]));
+  // The thread's place in a chunk at `first` (a wave's 16 bytes x VEC are
+  // contiguous: one address, small offsets), opaque to the compiler: it would
+  // keep everything that follows from it for every v, in a register each.
+  __device__ __forceinline__ static int base_of(int first) {
+    int base = first + (((int)threadIdx.x >> 6) * VEC * 64 + ((int)threadIdx.x & 63)) * EPV;
+    asm volatile("" : "+v"(base));
+    return base;
   }
-  __device__ __forceinline__ int id(int first, int v, int e) const {
-    return first + (v * kThreads + (int)threadIdx.x) * EPV + e;
+  // first logit of its v-th 16 bytes: their place, and where they were read
+  __device__ __forceinline__ static int place(int base, int v) { return base + v * 64 * EPV; }
+  __device__ __forceinline__ static int id(int base, int v, int vocab) {
+    return max(min(place(base, v), vocab - EPV), 0);
   }
 };
 
@@ -165,17 +193,16 @@ __device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) 
   return min(all, top);
 }
 
-// The chunk's part in the list of alternatives; most: the thread's largest
-// logit of the chunk.  Uniform over the workgroup; returns the list's length.
+// The chunk's part in the list of alternatives; vmax: the largest logit of
+// each of the thread's 16 bytes, most: of all.  Uniform over the workgroup;
+// returns the list's length.
 template <bool F32, int VEC>
-__device__ __forceinline__ int take_alternatives(Shared &sh, Chunk<F32, VEC> &ch, int first, float most, int have,
+__device__ __forceinline__ int take_alternatives(Shared &sh, const float (&vmax)[VEC], const uint8_t *row, int vocab, int first, float most, int have,
                                                  int top) {
   using C = Chunk<F32, VEC>;
   const float last = have == top ? key_value(sh.list[top - 1]) : neg_inf();
   if (!__syncthreads_or(most > last)) return have;
-  // candidates: l > bound (or >= bound where it is one of the chunk's own)
-  float bound = last;
-  bool own = false;
+  float bound = next_above(last);  // candidates: l >= bound
   for (int attempt = have == top ? 0 : 1; attempt < 2; ++attempt) {
     if (attempt == 1) {
       // the top-th largest of the 64 group maxima
@@ -183,24 +210,32 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, Chunk<F32, VEC> &ch
       g = fmaxf(g, __shfl_xor(g, 2));
       if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = g;
       __syncthreads();
-      const float b = wave_rank_value(sh.group[threadIdx.x & 63], top - 1);
-      own = b > bound;
-      bound = own ? b : bound;
+      bound = fmaxf(bound, wave_rank_value(sh.group[threadIdx.x & 63], top - 1));
     }
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    ch.repack();
-    if (own ? most >= bound : most > bound) {
+    // the few 16 bytes that hold candidates are read again (they are in the
+    // caches): unrolled over the registers instead, this search would cost the
+    // kernel half its occupancy
+    uint32_t hit = 0;
+    const int base = C::base_of(first);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v)
+    for (int v = 0; v < VEC; ++v) hit |= vmax[v] >= bound ? 1u << v : 0u;
+    while (hit != 0) {
+      const int v = __ffs(hit) - 1;
+      hit &= hit - 1;
+      const int i = C::place(base, v);
+      Chunk<F32, 1> one;
+      one.load16(0, row, i, vocab);
+      const int at0 = C::id(base, v, vocab);
 #pragma unroll
-        for (int e = 0; e < C::EPV; ++e) {
-          const float l = ch.at(v, e);
-          if (own ? l >= bound : l > bound) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)ch.id(first, v, e));
-          }
+      for (int e = 0; e < C::EPV; ++e) {
+        const float l = one.at(0, e);
+        if (l >= bound) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)(at0 + e));
         }
+      }
     }
     __syncthreads();
     const int n = sh.count;
@@ -211,15 +246,11 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, Chunk<F32, VEC> &ch
   int n = 0;
   for (uint64_t below = ~0ull; n < top; ++n) {
     uint64_t best = 0;
-    ch.repack();
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-#pragma unroll
-      for (int e = 0; e < C::EPV; ++e) {
-        const float l = ch.at(v, e);
-        const uint64_t k = alt_key(l, (uint32_t)ch.id(first, v, e));
-        if (l > last && k < below && k > best) best = k;
-      }
+    for (int i = first + (int)threadIdx.x; i < min(first + C::SIZE, vocab); i += kThreads) {  // (read again: rare)
+      const float l = F32 ? ((const float *)row)[i] : bf16_bits_to_f32(((const uint16_t *)row)[i]);
+      const uint64_t k = alt_key(l, (uint32_t)i);
+      if (l > last && k < below && k > best) best = k;
+    }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const uint64_t o = __shfl_xor((unsigned long long)best, off);
@@ -242,16 +273,14 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, Chunk<F32, VEC> &ch
 __host__ __device__ constexpr int64_t record_bytes(int top) { return 16 + 8 * (int64_t)((top + 1) & ~1); }
 
 template <bool F32, int VEC>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int parts, uint32_t *counters,
-                                                            uint8_t *records) {
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
   using C = Chunk<F32, VEC>;
   __shared__ Shared sh;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int vocab = (int)a.vocab, chunks = (vocab + C::SIZE - 1) / C::SIZE;
   const float c2 = a.scale * kLog2e;
-  for (int64_t unit = blockIdx.x; unit < a.rows * parts; unit += gridDim.x) {
-    const int64_t row = parts == 1 ? unit : unit / parts;
-    const int part = (int)(unit - row * parts);
+  const int parts = gridDim.x, part = blockIdx.x;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
     const int tok = a.tokens ? a.tokens[row] : -1;
     const bool in = tok >= 0 && tok < vocab;
@@ -259,35 +288,42 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int p
                      : F32 ? ((const float *)lp)[tok] : bf16_bits_to_f32(((const uint16_t *)lp)[tok]);
     Sums st = {neg_inf(), 0.f, 0.f};
     int above = 0, have = 0;
-    const int c_end = (int)((int64_t)(part + 1) * chunks / parts);
-    for (int c = (int)((int64_t)part * chunks / parts); c < c_end; ++c) {
+    const int c_end = (part + 1) * chunks / parts;
+    for (int c = part * chunks / parts; c < c_end; ++c) {
       C ch;
-      ch.load(lp, c * C::SIZE, vocab);
-      float most = neg_inf();
+      ch.load(lp, c * C::SIZE, C::base_of(c * C::SIZE), vocab);
+      float most = neg_inf(), vmax[VEC];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v)
+      for (int v = 0; v < VEC; ++v) {
+        vmax[v] = neg_inf();
 #pragma unroll
-        for (int e = 0; e < C::EPV; ++e) most = fmaxf(most, ch.at(v, e));
-      ch.repack();
+        for (int e = 0; e < C::EPV; e += 2) vmax[v] = max3(vmax[v], ch.at(v, e), ch.at(v, e + 1));
+        most = fmaxf(most, vmax[v]);
+      }
       // the running sums under the new maximum
       const float m = fmaxf(st.m, most);
       const float base = m == neg_inf() ? 0.f : m;
       const float back = fmaxf((st.m - base) * c2, -200.f), f = __builtin_amdgcn_exp2f(back);
       float s = st.s * f, t = f * (st.t + back * st.s);
+      int hits = 0;
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
+        // one 16 bytes after the other: unpacked again (an instruction per
+        // logit) instead of held in a register per logit, their masks counted
+        // before the next ones are made
+        asm volatile("" : "+v"(ch.d[v]), "+v"(s), "+v"(t), "+s"(hits));
 #pragma unroll
         for (int e = 0; e < C::EPV; ++e) {
           const float l = ch.at(v, e);
           const float d = (l - base) * c2, x = __builtin_amdgcn_exp2f(d);
           s += x;
           t = __builtin_fmaf(x, fmaxf(d, -200.f), t);  // (0 * -inf for masked tokens; a NaN comes in through x)
-          above += __popcll(__ballot(l > lt));         // wave-uniform
+          hits += __popcll(__ballot(l > lt));          // wave-uniform
         }
-        __builtin_amdgcn_sched_barrier(0);  // (bounds the masks held at once)
       }
       st = Sums{m, s, t};
-      if (a.top > 0) have = take_alternatives(sh, ch, c * C::SIZE, most, have, a.top);
+      above += hits;
+      if (a.top > 0) have = take_alternatives<F32, VEC>(sh, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
     }
     // join the threads, then the waves
 #pragma unroll
@@ -397,13 +433,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, int p
 // dl in one pass: 16 bytes per thread and step, VEC steps of a row in flight.
 // Reads and writes of one 16 bytes are the same thread's, so dl may be l.
 template <bool F32, int VEC>
-__global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a, int parts) {
+__global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
   using C = Chunk<F32, VEC>;
   constexpr int EL = F32 ? 4 : 2;
   const int vocab = (int)a.vocab;
   const float c2 = a.scale * kLog2e;
-  for (int64_t unit = blockIdx.x; unit < a.rows * parts; unit += gridDim.x) {
-    const int64_t row = parts == 1 ? unit : unit / parts;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * EL;
     uint8_t *dp = (uint8_t *)a.dlogits + row * a.lddl * EL;
     const float most = a.stats[2 * row], log_s = a.stats[2 * row + 1];
@@ -413,18 +448,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     const float e = a.dentropy && !empty ? a.dentropy[row] * a.scale : 0.f;
     // -p (g + e (log p + H)) = p (w0 - e ln2 q) with q = log2 p
     const float w0 = -g - (e != 0.f ? e * a.entropy[row] : 0.f), w1 = -e * kLn2, q0 = empty ? 0.f : -log_s * kLog2e;
-    for (int first = (int)(unit - row * parts) * C::SIZE; first < vocab; first += parts * C::SIZE) {
+    for (int first = (int)blockIdx.x * C::SIZE; first < vocab; first += (int)gridDim.x * C::SIZE) {
       C ch;
-      ch.load(lp, first, vocab);
+      const int base = C::base_of(first);
+      ch.load(lp, first, base, vocab);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const int i = ch.id(first, v, 0);
+        const int i = C::place(base, v), at = C::id(base, v, vocab);
         float o[C::EPV];
 #pragma unroll
         for (int k = 0; k < C::EPV; ++k) {
           const float q = __builtin_fmaf(ch.at(v, k) - most, c2, q0);
           o[k] = __builtin_amdgcn_exp2f(q) * __builtin_fmaf(w1, fmaxf(q, -300.f), w0);
-          if (i + k == tok) o[k] += g;
+          if (at + k == tok) o[k] += g;
         }
         u32x4 w;
         if constexpr (F32) {
@@ -435,11 +471,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
           for (int k = 0; k < 4; ++k) w[k] = bf16_rne(o[2 * k]) | (bf16_rne(o[2 * k + 1]) << 16);
         }
         if (empty) w = u32x4{0u, 0u, 0u, 0u};
-        uint8_t *p = dp + (int64_t)i * EL;
         if (i + C::EPV <= vocab) {
-          *(u32x4_any *)p = w;
+          *(u32x4_any *)(dp + (int64_t)i * EL) = w;
         } else {
-          for (int k = 0; k < vocab - i; ++k) {
+          uint8_t *p = dp + (int64_t)at * EL;
+#pragma unroll
+          for (int k = 0; k < C::EPV; ++k) {
+            if (at + k < i || at + k >= vocab) continue;
             if constexpr (F32)
               ((uint32_t *)p)[k] = w[k];
             else
@@ -480,19 +518,19 @@ uint64_t logprobs_ws_bytes(int64_t rows, int64_t vocab, int top) {
 
 hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s) {
   const Split sp = logprobs_split(a.rows, a.vocab, a.f32);
-  const dim3 grid((unsigned)std::min<int64_t>(a.rows * sp.parts, 1 << 20));
+  const dim3 grid((unsigned)sp.parts, (unsigned)std::min<int64_t>(a.rows, 65535));
   uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 1024
   uint8_t *records = (uint8_t *)ws + kSplitCounterBytes;
   if (a.f32) {
     if (sp.small)
-      hipLaunchKernelGGL((logprobs_kernel<true, 2>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+      hipLaunchKernelGGL((logprobs_kernel<true, 2>), grid, dim3(kThreads), 0, s, a, counters, records);
     else
-      hipLaunchKernelGGL((logprobs_kernel<true, 8>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+      hipLaunchKernelGGL((logprobs_kernel<true, 8>), grid, dim3(kThreads), 0, s, a, counters, records);
   } else {
     if (sp.small)
-      hipLaunchKernelGGL((logprobs_kernel<false, 2>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+      hipLaunchKernelGGL((logprobs_kernel<false, 2>), grid, dim3(kThreads), 0, s, a, counters, records);
     else
-      hipLaunchKernelGGL((logprobs_kernel<false, 8>), grid, dim3(kThreads), 0, s, a, sp.parts, counters, records);
+      hipLaunchKernelGGL((logprobs_kernel<false, 8>), grid, dim3(kThreads), 0, s, a, counters, records);
   }
   return hipGetLastError();
 }
@@ -502,11 +540,11 @@ hipError_t launch_logprobs_backward(const LogprobArgs &a, hipStream_t s) {
   const int64_t chunks = (a.vocab + size - 1) / size;
   // one workgroup per chunk up to about eight per CU, then more chunks each
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (2048 + a.rows - 1) / a.rows));
-  const dim3 grid((unsigned)std::min<int64_t>(a.rows * parts, 1 << 20));
+  const dim3 grid((unsigned)parts, (unsigned)std::min<int64_t>(a.rows, 65535));
   if (a.f32)
-    hipLaunchKernelGGL((logprobs_backward_kernel<true, 4>), grid, dim3(kThreads), 0, s, a, parts);
+    hipLaunchKernelGGL((logprobs_backward_kernel<true, 4>), grid, dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((logprobs_backward_kernel<false, 4>), grid, dim3(kThreads), 0, s, a, parts);
+    hipLaunchKernelGGL((logprobs_backward_kernel<false, 4>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
