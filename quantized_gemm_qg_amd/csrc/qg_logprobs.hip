@@ -39,6 +39,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCap = 1024;       // candidates of one chunk
 constexpr int kMaxParts = 64;    // workgroups per row
+constexpr int kRecordKeys = kMaxParts * QG_MAX_ALTERNATIVES / kThreads;  // keys of a row's parts, per thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -186,6 +187,7 @@ __device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) 
   for (int i = threadIdx.x; i < all; i += kThreads) {
     const uint64_t k = sh.cand[i];
     int r = 0;
+#pragma unroll 16
     for (int j = 0; j < all; ++j) r += sh.cand[j] > k;
     if (r < top) sh.list[r] = k;
   }
@@ -272,14 +274,15 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const float (&vmax)
 // The record of one part of a row: sums, count and the sorted alternatives.
 __host__ __device__ constexpr int64_t record_bytes(int top) { return 16 + 8 * (int64_t)((top + 1) & ~1); }
 
-template <bool F32, int VEC>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
+// SHARED: gridDim.x workgroups share a row.
+template <bool F32, int VEC, bool SHARED>
+__global__ __launch_bounds__(kThreads, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
   using C = Chunk<F32, VEC>;
   __shared__ Shared sh;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int vocab = (int)a.vocab, chunks = (vocab + C::SIZE - 1) / C::SIZE;
   const float c2 = a.scale * kLog2e;
-  const int parts = gridDim.x, part = blockIdx.x;
+  const int parts = SHARED ? gridDim.x : 1, part = SHARED ? blockIdx.x : 0;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
     const int tok = a.tokens ? a.tokens[row] : -1;
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, uint3
       st = join(st, sh.sums[w], c2);
       above += sh.above[w];
     }
-    if (parts > 1) {
+    if constexpr (SHARED) {
       // publish this part, and let the last workgroup of the row join them:
       // agent-scope stores, complete before the counter moves
       const int64_t rb = record_bytes(a.top);
@@ -370,6 +373,16 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, uint3
       auto key = [&](int p, int i) {
         return __hip_atomic_load((const uint64_t *)(rec + p * rb + 16) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       };
+      // every load of the records goes out at once: this thread's keys (one
+      // position of a list each), this lane's sums
+      uint64_t all[kRecordKeys];
+      if (a.top > 0) {
+#pragma unroll
+        for (int j = 0; j < kRecordKeys; ++j) {
+          const int i = j * kThreads + (int)threadIdx.x, pos = i / kMaxParts, p = i % kMaxParts;
+          all[j] = pos < a.top && p < parts ? key(p, pos) : 0;
+        }
+      }
       st = Sums{neg_inf(), 0.f, 0.f};
       above = 0;
       if (lane < parts) {
@@ -398,10 +411,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a, uint3
         const uint64_t bound = __shfl((unsigned long long)mine, at);
         if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < parts * a.top; i += kThreads) {
-          const uint64_t k = key(i / a.top, i % a.top);
-          if (k != 0 && k >= bound) sh.cand[atomicAdd(&sh.count, 1)] = k;
-        }
+#pragma unroll
+        for (int j = 0; j < kRecordKeys; ++j)
+          if (all[j] != 0 && all[j] >= bound) sh.cand[atomicAdd(&sh.count, 1)] = all[j];
         __syncthreads();
         have = merge_list(sh, sh.count, 0, a.top);
       }
@@ -521,17 +533,14 @@ hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s) {
   const dim3 grid((unsigned)sp.parts, (unsigned)std::min<int64_t>(a.rows, 65535));
   uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 1024
   uint8_t *records = (uint8_t *)ws + kSplitCounterBytes;
-  if (a.f32) {
-    if (sp.small)
-      hipLaunchKernelGGL((logprobs_kernel<true, 2>), grid, dim3(kThreads), 0, s, a, counters, records);
-    else
-      hipLaunchKernelGGL((logprobs_kernel<true, 8>), grid, dim3(kThreads), 0, s, a, counters, records);
-  } else {
-    if (sp.small)
-      hipLaunchKernelGGL((logprobs_kernel<false, 2>), grid, dim3(kThreads), 0, s, a, counters, records);
-    else
-      hipLaunchKernelGGL((logprobs_kernel<false, 8>), grid, dim3(kThreads), 0, s, a, counters, records);
-  }
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, s, a, counters, records); };
+  // (small chunks of a row that is not shared: a vocabulary of one chunk)
+  if (a.f32)
+    sp.parts > 1 ? (sp.small ? go(logprobs_kernel<true, 2, true>) : go(logprobs_kernel<true, 8, true>))
+                 : (sp.small ? go(logprobs_kernel<true, 2, false>) : go(logprobs_kernel<true, 8, false>));
+  else
+    sp.parts > 1 ? (sp.small ? go(logprobs_kernel<false, 2, true>) : go(logprobs_kernel<false, 8, true>))
+                 : (sp.small ? go(logprobs_kernel<false, 2, false>) : go(logprobs_kernel<false, 8, false>));
   return hipGetLastError();
 }
 
