@@ -13,6 +13,7 @@
 #include "qg_device.h"
 #include "qg_internal.h"
 #include "qg_mm.h"
+#include "qg_rows.h"
 
 namespace qg {
 
@@ -69,6 +70,10 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s) {
   a.gu_type = c.gu_type;
   a.act = c.act;
   a.group_m = 4;
+  if (c.m <= 16) return launch_rows<false, true, 1, 2, 4, false>(a, s);
+  if (c.m <= 32) return launch_rows<false, true, 2, 2, 4, false>(a, s);
+  if (c.m <= 64) return launch_rows<false, true, 4, 2, 2, false>(a, s);
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 64, 4>>(a, s);
   return launch_mm<MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 64, 4>>(a, s);
 }
 
@@ -100,6 +105,7 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddx;
   a.otype = QG_O_BF16;
   a.group_m = 4;
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 64, 4>>(a, s);
   return launch_mm<MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
 }
 
@@ -118,6 +124,7 @@ hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddw;
   a.otype = dw_type;
   a.group_m = 4;
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 64, 4>>(a, s);
   return launch_mm<MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
 }
 

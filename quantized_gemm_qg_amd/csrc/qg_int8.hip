@@ -9,6 +9,7 @@
 #include "qg_device.h"
 #include "qg_internal.h"
 #include "qg_mm.h"
+#include "qg_rows.h"
 
 namespace qg {
 
@@ -19,20 +20,12 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const uint16_t *x, i
                                                             int64_t ldq, float *qs, int64_t rows) {
   __shared__ float wave_max[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto load8 = [](const uint16_t *p, float (&v)[8]) {
-    const u32x4 w = *(const u32x4 *)p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  };
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const uint16_t *xr = x + row * ldx;
     float m = 0.f;
     for (int64_t c = 8 * (int64_t)threadIdx.x; c < k; c += 2048) {
       float v[8];
-      load8(xr + c, v);
+      unpack8(*(const u32x4 *)(xr + c), v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
     }
@@ -42,18 +35,11 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const uint16_t *x, i
     __syncthreads();
     m = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
     __syncthreads();  // wave_max is rewritten for the next row
-    const float s = m > 0.f ? m / 127.f : 1.f;
+    const float s = i8_scale(m);
     for (int64_t c = 8 * (int64_t)threadIdx.x; c < k; c += 2048) {
       float v[8];
-      load8(xr + c, v);
-      uint32_t w[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        w[h] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[h] |= ((uint32_t)(int)rintf(v[4 * h + i] / s) & 255u) << (8 * i);
-      }
-      *(uint2 *)(q + row * ldq + c) = uint2{w[0], w[1]};
+      unpack8(*(const u32x4 *)(xr + c), v);
+      *(uint2 *)(q + row * ldq + c) = uint2{i8_codes4(v, s), i8_codes4(v + 4, s)};
     }
     if (threadIdx.x == 0) qs[row] = s;
   }
@@ -86,8 +72,23 @@ static MmArgs i8_args(const I8Call &c) {
   return a;
 }
 
+// Rows whose codes the few-rows kernel holds in LDS (one workgroup then
+// leaves room for another on its CU).
+bool i8_quantizes_in_kernel(int64_t m, int64_t k) { return m <= 4 && m * rows_pitch((int)k) <= 64 * 1024; }
+
 hipError_t launch_i8(const I8Call &c, hipStream_t s) {
-  const MmArgs a = i8_args(c);
+  MmArgs a = i8_args(c);
+  if (c.quantize) {
+    a.lda = c.ldx * 2;
+    return c.gated ? launch_rows<true, true, 1, 2, 4, true>(a, s) : launch_rows<true, false, 1, 1, 8, true>(a, s);
+  }
+  if (c.m <= 16) return c.gated ? launch_rows<true, true, 1, 2, 4, false>(a, s) : launch_rows<true, false, 1, 1, 4, false>(a, s);
+  if (c.m <= 32) return c.gated ? launch_rows<true, true, 2, 2, 4, false>(a, s) : launch_rows<true, false, 2, 2, 4, false>(a, s);
+  if (c.m <= 64) return c.gated ? launch_rows<true, true, 4, 2, 2, false>(a, s) : launch_rows<true, false, 4, 2, 2, false>(a, s);
+  if (c.m >= 1000) {
+    if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 256, 256, 4, 2, 64, 4>>(a, s);
+    return launch_mm<MmCfg<true, kRows, kPacked, false, 256, 256, 4, 2, 64, 4>>(a, s);
+  }
   if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 128, 128, 2, 2, 64, 4>>(a, s);
   return launch_mm<MmCfg<true, kRows, kPacked, false, 128, 128, 2, 2, 64, 4>>(a, s);
 }

@@ -344,12 +344,13 @@ hipError_t launch_silu_mul(const void *gu, bool gu_f32, int64_t rows, int64_t in
 hipError_t launch_moe_combine(const void *y, bool y_f32, int64_t ldy, const float *wts, int64_t tokens, int topk,
                               int64_t n, const void *bias, void *out, bool out_f32, int64_t ldo, hipStream_t s);
 // int8 products (qg_int8.hip): quantized rows (x int8 [m][ldx], x_scales [m])
-// times the packed codes; gated: n outputs from 2 n weight columns.
+// times the packed codes; gated: n outputs from 2 n weight columns; quantize:
+// x is bf16 (where i8_quantizes_in_kernel).
 struct I8Call {
   const uint8_t *codes;
   const float *scales;
   int32_t n, k, k_blocks;
-  bool gated;
+  bool gated, quantize;
   int32_t act;
   const void *x;
   int64_t ldx;
@@ -361,6 +362,7 @@ struct I8Call {
 };
 hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq, float *qs,
                                 hipStream_t s);
+bool i8_quantizes_in_kernel(int64_t m, int64_t k);
 hipError_t launch_i8(const I8Call &c, hipStream_t s);
 // bf16 gated feed-forward block (qg_ffn.hip); strides in elements
 struct FfnCall {

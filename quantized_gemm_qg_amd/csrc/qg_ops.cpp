@@ -21,8 +21,8 @@ constexpr int64_t kMaxPitchBytes = 1 << 23;
 static bool tiles_fit(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 31) / 32) < (1ll << 31) - 8; }
 
 // Int8 workspace: [split-K counters][codes of the quantized rows][their scales]
-uint64_t i8_ws_bytes(const qg_weight &w, bool, int64_t m, uint32_t flags) {
-  if (m <= 0 || !(flags & QG_GEMM_QUANTIZE_X)) return 0;
+uint64_t i8_ws_bytes(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
+  if (m <= 0 || !(flags & QG_GEMM_QUANTIZE_X) || i8_quantizes_in_kernel(m, w.desc.k)) return 0;
   return kSplitCounterBytes + align_up((uint64_t)m * w.desc.k, 256) + align_up((uint64_t)m * 4, 256);
 }
 
@@ -66,7 +66,8 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
   c.y = y;
   c.otype = otype;
   c.ldy = ldy;
-  if (quantize) {
+  c.quantize = quantize && i8_quantizes_in_kernel(m, d.k);
+  if (quantize && !c.quantize) {
     uint8_t *q = (uint8_t *)ws + kSplitCounterBytes;
     float *qs = (float *)(q + align_up((uint64_t)m * d.k, 256));
     const hipError_t e = launch_quantize_int8(x, m, d.k, ldx, q, d.k, qs, stream);
