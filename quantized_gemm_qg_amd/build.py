@@ -40,10 +40,11 @@ def _flags():
     ]
 
 
-# Per-source extra flags.  The integer-format tiled kernel keeps its MFMA
-# results in VGPRs (they feed fp32 FMAs right away); left to its heuristics the
-# compiler puts them in AGPRs and copies every one back.
-EXTRA = {"qg_tiled_a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# Per-source extra flags.  These tiled kernels keep their MFMA results in VGPRs
+# (the integer formats' feed fp32 FMAs right away); left to its heuristics the
+# compiler puts them in AGPRs and copies them back.
+VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"qg_tiled_a16.hip": VGPR_MFMA, "qg_int8.hip": VGPR_MFMA, "qg_ffn.hip": VGPR_MFMA}
 
 
 def _compile(src: str, verbose: bool) -> str:

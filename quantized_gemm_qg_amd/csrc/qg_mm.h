@@ -15,9 +15,8 @@
 // (v_mfma_i32_16x16x64_i8 / v_mfma_f32_16x16x32_bf16: both take 64 bytes of k
 // per row, 16 per lane).  The operands go through a ring of ST stages of KB
 // bytes of k, filled by global_load_lds_dwordx4 (1 KB per wave and copy, no
-// register staging): stage s + ST - 1 is issued right after the barrier that
-// publishes stage s, so ST - 2 whole stages stay in flight behind the one that
-// lands.  Bank conflicts: row chunks of 16 bytes sit at slot chunk ^ f(row), the
+// register staging), and from LDS into a second set of operand registers while
+// the first one multiplies.  Bank conflicts: row chunks of 16 bytes sit at slot chunk ^ f(row), the
 // 32-byte column units of kCols at unit ^ f(k); packed pieces are read in the
 // order they are stored.  Past the last k both operands read a line of zeros
 // (nothing is multiplied by what lies behind a row), past the last row or
@@ -117,6 +116,23 @@ struct MmCfg {
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
+// Waits until at most `stages` (0 .. 4) stages of LOADS loads each are out.
+template <int LOADS>
+__device__ __forceinline__ void wait_loads(int stages) {
+  static_assert(4 * LOADS < 64, "outstanding loads");
+  if (stages >= 4) {
+    QG_WAIT_VMCNT(4 * LOADS);
+  } else if (stages == 3) {
+    QG_WAIT_VMCNT(3 * LOADS);
+  } else if (stages == 2) {
+    QG_WAIT_VMCNT(2 * LOADS);
+  } else if (stages == 1) {
+    QG_WAIT_VMCNT(LOADS);
+  } else {
+    QG_WAIT_VMCNT(0);
+  }
+}
+
 // chunk order of a row's 16-byte chunks
 template <int KB>
 __device__ __forceinline__ int row_swz(int row) { return KB == 128 ? (row & 7) : ((row >> 1) & 3); }
@@ -210,13 +226,14 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   // bytes from one stage to the next
   const int64_t a_step = C::AF == kRows ? C::KB : (int64_t)C::KE * a.lda;
   const int64_t b_step = C::BF == kRows ? C::KB : C::BF == kPacked ? 1024 * C::SUB : (int64_t)C::KE * a.ldb;
-  const int steps = (a.kd + C::KE - 1) / C::KE;
-  const bool ragged = a.kd % C::KE != 0;
+  // an even number of stages (the loop below handles two at a time); what lies
+  // behind the last k is zeros
+  const int steps = ((a.kd + C::KE - 1) / C::KE + 1) & ~1;
 
   auto issue = [&](int s) {
     uint8_t *st = smem + (s % C::ST) * C::STAGE;
     const uint8_t *as = a_base + s * a_step;
-    if (!ragged || s + 1 < steps) {
+    if ((s + 1) * C::KE <= a.kd) {
 #pragma unroll
       for (int i = 0; i < C::A_LOADS; ++i) lds_dma16(as + a_off[i], st + a_copy(i) * 1024);
 #pragma unroll
@@ -234,35 +251,67 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     }
   };
 
-  // fragment of 16 rows (or columns) `blk` of an operand, MFMA step u
-  auto rows_frag = [&](const uint8_t *op, int blk, int u) {
-    const int row = blk * 16 + r16;
-    return *(const u32x4 *)(op + row * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(row)));
-  };
-  auto cols_frag = [&](const uint8_t *op, int width, int blk, int u) {
-    // k 32 u + 8 q + 0..3 and + 4..7 of column 16 blk + r16: within 16 lanes,
-    // lane i names k row i / 4 and columns 4 (i % 4) .. + 3 and receives column i
+  // Fragments of one stage in registers.  kRows: row 16 blk + r16, its swizzle
+  // depends on r16 alone.  kCols: k 32 u + 8 q + 0..3 and + 4..7 of column
+  // 16 blk + r16; within 16 lanes, lane i names k row i / 4 and columns 4 (i % 4)
+  // .. + 3 and receives column i; the unit swizzle depends on i / 4 and q alone.
+  // So every address is a lane offset per operand (kCols: per block) plus
+  // constants.
+  uint32_t a_at[C::AF == kCols ? C::MB : C::SUB], b_at[C::BF == kCols ? C::NB : C::SUB];
+  const int ksw = (r16 >> 2) | ((q & 1) << 2);
+  if constexpr (C::AF == kCols) {
+#pragma unroll
+    for (int i = 0; i < C::MB; ++i)
+      a_at[i] = (8 * q + (r16 >> 2)) * (2 * C::BM) + 32 * ((wm * C::MB + i) ^ ksw) + 8 * (r16 & 3);
+  } else {
+#pragma unroll
+    for (int u = 0; u < C::SUB; ++u)
+      a_at[u] = (wm * C::MB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(r16));
+  }
+  if constexpr (C::BF == kCols) {
+#pragma unroll
+    for (int j = 0; j < C::NB; ++j)
+      b_at[j] = C::A + (8 * q + (r16 >> 2)) * (2 * C::BN) + 32 * ((wn * C::NB + j) ^ ksw) + 8 * (r16 & 3);
+  } else {
+#pragma unroll
+    for (int u = 0; u < C::SUB; ++u)
+      b_at[u] = C::A + (C::BF == kRows ? (wn * C::NB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(r16))
+                                       : (wn * C::NB * C::SUB + u) * 1024 + 16 * lane);
+  }
+  auto cols_frag = [&](const uint8_t *p, int width, int u) {
     u32x4 v;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = 32 * u + 8 * q + 4 * h + (r16 >> 2);
-      const uint8_t *p = op + k * (2 * width) + 32 * (blk ^ col_swz(k)) + 8 * (r16 & 3);
-      const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
+      const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4 *)(p + (32 * u + 4 * h) * (2 * width)));
       const uint2 w = __builtin_bit_cast(uint2, t);
       v[2 * h] = w.x;
       v[2 * h + 1] = w.y;
     }
     return v;
   };
-  auto a_frag = [&](const uint8_t *st, int i, int u) {
-    if constexpr (C::AF == kRows) return rows_frag(st, wm * C::MB + i, u);
-    else return cols_frag(st, C::BM, wm * C::MB + i, u);
+  struct Frags {
+    u32x4 a[C::SUB][C::MB], b[C::SUB][C::NB];
   };
-  auto b_frag = [&](const uint8_t *st, int j, int u) {
-    const int blk = wn * C::NB + j;
-    if constexpr (C::BF == kRows) return rows_frag(st + C::A, blk, u);
-    else if constexpr (C::BF == kPacked) return *(const u32x4 *)(st + C::A + (blk * C::SUB + u) * 1024 + 16 * lane);
-    else return cols_frag(st + C::A, C::BN, blk, u);
+  auto read = [&](int s, Frags &f) {
+    const uint8_t *st = smem + (s % C::ST) * C::STAGE;
+#pragma unroll
+    for (int u = 0; u < C::SUB; ++u) {
+#pragma unroll
+      for (int j = 0; j < C::NB; ++j) {
+        if constexpr (C::BF == kCols)
+          f.b[u][j] = cols_frag(st + b_at[j], C::BN, u);
+        else
+          f.b[u][j] = *(const u32x4 *)(st + b_at[u] + j * (C::BF == kRows ? 16 * C::KB : 1024 * C::SUB));
+      }
+#pragma unroll
+      for (int i = 0; i < C::MB; ++i) {
+        if constexpr (C::AF == kCols)
+          f.a[u][i] = cols_frag(st + a_at[i], C::BM, u);
+        else
+          f.a[u][i] = *(const u32x4 *)(st + a_at[u] + i * 16 * C::KB);
+      }
+    }
   };
 
   Acc acc[C::MB][C::NB];
@@ -270,45 +319,55 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   for (int i = 0; i < C::MB; ++i)
 #pragma unroll
     for (int j = 0; j < C::NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-
+  auto multiply = [&](const Frags &f) {
 #pragma unroll
-  for (int s = 0; s < C::ST - 1; ++s)
-    if (s < steps) issue(s);
-  for (int s = 0; s < steps; ++s) {
-    // stage s has landed when only the loads of the stages behind it are out
-    const int behind = min(C::ST - 2, steps - 1 - s);
-    if (behind >= 3) {
-      QG_WAIT_VMCNT(3 * C::LOADS);
-    } else if (behind == 2) {
-      QG_WAIT_VMCNT(2 * C::LOADS);
-    } else if (behind == 1) {
-      QG_WAIT_VMCNT(C::LOADS);
-    } else {
-      QG_WAIT_VMCNT(0);
-    }
-    __builtin_amdgcn_s_barrier();  // stage s is in LDS for every wave, stage s - 1 is free
-    if (s + C::ST - 1 < steps) issue(s + C::ST - 1);
-    const uint8_t *st = smem + (s % C::ST) * C::STAGE;
+    for (int u = 0; u < C::SUB; ++u)
 #pragma unroll
-    for (int u = 0; u < C::SUB; ++u) {
-      u32x4 bf[C::NB];
-#pragma unroll
-      for (int j = 0; j < C::NB; ++j) bf[j] = b_frag(st, j, u);
-#pragma unroll
-      for (int i = 0; i < C::MB; ++i) {
-        const u32x4 af = a_frag(st, i, u);
+      for (int i = 0; i < C::MB; ++i)
 #pragma unroll
         for (int j = 0; j < C::NB; ++j) {
           if constexpr (C::I8)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, bf[j]),
-                                                              __builtin_bit_cast(i32x4, af), acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, f.b[u][j]),
+                                                              __builtin_bit_cast(i32x4, f.a[u][i]), acc[i][j], 0, 0, 0);
           else
-            acc[i][j] = mfma_bf16(bf[j], af, acc[i][j]);
+            acc[i][j] = mfma_bf16(f.b[u][j], f.a[u][i], acc[i][j]);
         }
-      }
+  };
+
+  // The fragments of stage s + 1 are read while those of stage s multiply, so
+  // no product waits for LDS; a stage's buffer is free once its fragments are
+  // in registers, and stage s + ST follows into it.
+#pragma unroll
+  for (int s = 0; s < C::ST; ++s)
+    if (s < steps) issue(s);
+  Frags f[2];
+  wait_loads<C::LOADS>(min(C::ST - 1, steps - 1));
+  __builtin_amdgcn_s_barrier();  // stage 0 is in LDS for every wave
+  read(0, f[0]);
+  auto step = [&](int s, Frags &cur, Frags &nxt) {  // s + 1 < steps
+    // stages s + 2 .. s + ST - 1 may still be out; this wave's reads of stage s are done
+    wait_loads<C::LOADS>(min(C::ST - 2, steps - 2 - s));
+    QG_WAIT_LGKMCNT0();
+    __builtin_amdgcn_s_barrier();  // stage s + 1 is in LDS; every wave holds stage s in registers
+    if (s + C::ST < steps) issue(s + C::ST);
+    read(s + 1, nxt);
+    multiply(cur);
+    constexpr int READS = C::SUB * (C::NB * (C::BF == kCols ? 2 : 1) + C::MB * (C::AF == kCols ? 2 : 1));
+    constexpr int MULS = C::SUB * C::NB * C::MB, PER = MULS / READS > 0 ? MULS / READS : 1;
+#pragma unroll
+    for (int r = 0; r < READS; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // one LDS read,
+      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);  // then its share of the products
     }
+    if constexpr (MULS > READS * PER) __builtin_amdgcn_sched_group_barrier(0x008, MULS - READS * PER, 0);
+  };
+  int s = 0;
+  for (; s + 2 < steps; s += 2) {
+    step(s, f[0], f[1]);
+    step(s + 1, f[1], f[0]);
   }
-  static_assert(C::ST <= 5 && 3 * C::LOADS < 64, "outstanding loads");
+  step(s, f[0], f[1]);
+  multiply(f[1]);
 
   // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
   asm volatile("" ::: "memory");
