@@ -73,8 +73,8 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s) {
   if (c.m <= 16) return launch_rows<false, true, 1, 2, 4, false>(a, s);
   if (c.m <= 32) return launch_rows<false, true, 2, 2, 4, false>(a, s);
   if (c.m <= 64) return launch_rows<false, true, 4, 2, 2, false>(a, s);
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 64, 4>>(a, s);
-  return launch_mm<MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 64, 4>>(a, s);
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 128, 2>>(a, s);
+  return launch_mm<MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 128, 2>>(a, s);
 }
 
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
@@ -105,8 +105,8 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddx;
   a.otype = QG_O_BF16;
   a.group_m = 4;
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 64, 4>>(a, s);
-  return launch_mm<MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 128, 2>>(a, s);
+  return launch_mm<MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 128, 2>>(a, s);
 }
 
 // dW = [dg du]^T x: contraction over the tokens
@@ -124,8 +124,8 @@ hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddw;
   a.otype = dw_type;
   a.group_m = 4;
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 64, 4>>(a, s);
-  return launch_mm<MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 64, 4>>(a, s);
+  if (c.m >= 1000) return launch_mm<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 128, 2>>(a, s);
+  return launch_mm<MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 128, 2>>(a, s);
 }
 
 hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s) {

@@ -86,11 +86,11 @@ hipError_t launch_i8(const I8Call &c, hipStream_t s) {
   if (c.m <= 32) return c.gated ? launch_rows<true, true, 2, 2, 4, false>(a, s) : launch_rows<true, false, 2, 2, 4, false>(a, s);
   if (c.m <= 64) return c.gated ? launch_rows<true, true, 4, 2, 2, false>(a, s) : launch_rows<true, false, 4, 2, 2, false>(a, s);
   if (c.m >= 1000) {
-    if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 256, 256, 4, 2, 64, 4>>(a, s);
-    return launch_mm<MmCfg<true, kRows, kPacked, false, 256, 256, 4, 2, 64, 4>>(a, s);
+    if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 256, 256, 4, 2, 128, 2>>(a, s);
+    return launch_mm<MmCfg<true, kRows, kPacked, false, 256, 256, 4, 2, 128, 2>>(a, s);
   }
-  if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 128, 128, 2, 2, 64, 4>>(a, s);
-  return launch_mm<MmCfg<true, kRows, kPacked, false, 128, 128, 2, 2, 64, 4>>(a, s);
+  if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 128, 128, 2, 2, 128, 2>>(a, s);
+  return launch_mm<MmCfg<true, kRows, kPacked, false, 128, 128, 2, 2, 128, 2>>(a, s);
 }
 
 }  // namespace qg

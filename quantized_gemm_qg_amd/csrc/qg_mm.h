@@ -109,28 +109,45 @@ struct MmCfg {
   static constexpr int SLAB = 16 * PITCH;
   static constexpr int LDS = STAGE * ST > WAVES * SLAB ? STAGE * ST : WAVES * SLAB;
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && (!GATED || NB % 2 == 0), "blocks");
-  static_assert(KB == 64 || KB == 128, "stage depth");
+  static_assert(KB == 128, "stage depth: two MFMA steps");
   static_assert(!I8 || AF == kRows, "int8 activations are rows");
   static_assert(AF != kCols || BM >= 128, "column units for the swizzle");
   static_assert(BF != kCols || BN >= 128, "column units for the swizzle");
-  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(LDS <= 160 * 1024 && ST >= 2 && ST <= 3, "LDS ring");
 };
 
-// Waits until at most `stages` (0 .. 4) stages of LOADS loads each are out.
+// Waits until at most `stages` (0 .. 2) stages of LOADS loads each are out.
 template <int LOADS>
 __device__ __forceinline__ void wait_loads(int stages) {
-  static_assert(4 * LOADS < 64, "outstanding loads");
-  if (stages >= 4) {
-    QG_WAIT_VMCNT(4 * LOADS);
-  } else if (stages == 3) {
-    QG_WAIT_VMCNT(3 * LOADS);
-  } else if (stages == 2) {
+  static_assert(2 * LOADS < 64, "outstanding loads");
+  if (stages >= 2) {
     QG_WAIT_VMCNT(2 * LOADS);
   } else if (stages == 1) {
     QG_WAIT_VMCNT(LOADS);
   } else {
     QG_WAIT_VMCNT(0);
   }
+}
+
+// Workgroup barrier that no memory access moves across.
+__device__ __forceinline__ void mm_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Direct global -> LDS copies of 16 bytes per lane, at a lane offset from a
+// uniform base or at a lane's own address; `lds` (uniform) receives the wave's
+// 1 KB.  Written out because the builtin makes the compiler wait for every
+// outstanding copy before each transposed LDS read (it cannot tell the stages
+// of the ring apart there); the waits are wait_loads above.  The instruction
+// has no destination register.
+__device__ __forceinline__ void mm_copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void mm_copy16_at(const uint8_t *src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
 
 // chunk order of a row's 16-byte chunks
@@ -226,28 +243,28 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   // bytes from one stage to the next
   const int64_t a_step = C::AF == kRows ? C::KB : (int64_t)C::KE * a.lda;
   const int64_t b_step = C::BF == kRows ? C::KB : C::BF == kPacked ? 1024 * C::SUB : (int64_t)C::KE * a.ldb;
-  // an even number of stages (the loop below handles two at a time); what lies
-  // behind the last k is zeros
-  const int steps = ((a.kd + C::KE - 1) / C::KE + 1) & ~1;
+  const int steps = (a.kd + C::KE - 1) / C::KE;
 
+  const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
   auto issue = [&](int s) {
-    uint8_t *st = smem + (s % C::ST) * C::STAGE;
-    const uint8_t *as = a_base + s * a_step;
+    const uint32_t st = ring + (s % C::ST) * C::STAGE;
+    const uint8_t *as = a_base + s * a_step, *bs = b_base + s * b_step;
+    const int64_t up = b_base_up - b_base;
     if ((s + 1) * C::KE <= a.kd) {
 #pragma unroll
-      for (int i = 0; i < C::A_LOADS; ++i) lds_dma16(as + a_off[i], st + a_copy(i) * 1024);
+      for (int i = 0; i < C::A_LOADS; ++i) mm_copy16(as, a_off[i], st + a_copy(i) * 1024);
 #pragma unroll
       for (int i = 0; i < C::B_LOADS; ++i)
-        lds_dma16((b_up[i] ? b_base_up : b_base) + s * b_step + b_off[i], st + C::A + b_copy(i) * 1024);
+        mm_copy16(bs + (b_up[i] ? up : 0), b_off[i], st + C::A + b_copy(i) * 1024);
     } else {
       const int left = a.kd - s * C::KE;
 #pragma unroll
       for (int i = 0; i < C::A_LOADS; ++i)
-        lds_dma16(a_k[i] < left ? as + a_off[i] : (const uint8_t *)mm_zeros, st + a_copy(i) * 1024);
+        mm_copy16_at(a_k[i] < left ? as + a_off[i] : (const uint8_t *)mm_zeros, st + a_copy(i) * 1024);
 #pragma unroll
       for (int i = 0; i < C::B_LOADS; ++i)
-        lds_dma16(b_k[i] < left ? (b_up[i] ? b_base_up : b_base) + s * b_step + b_off[i] : (const uint8_t *)mm_zeros,
-                  st + C::A + b_copy(i) * 1024);
+        mm_copy16_at(b_k[i] < left ? bs + (b_up[i] ? up : 0) + b_off[i] : (const uint8_t *)mm_zeros,
+                     st + C::A + b_copy(i) * 1024);
     }
   };
 
@@ -291,26 +308,23 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     return v;
   };
   struct Frags {
-    u32x4 a[C::SUB][C::MB], b[C::SUB][C::NB];
+    u32x4 a[C::MB], b[C::NB];
   };
-  auto read = [&](int s, Frags &f) {
+  auto read = [&](int s, int u, Frags &f) {
     const uint8_t *st = smem + (s % C::ST) * C::STAGE;
 #pragma unroll
-    for (int u = 0; u < C::SUB; ++u) {
+    for (int j = 0; j < C::NB; ++j) {
+      if constexpr (C::BF == kCols)
+        f.b[j] = cols_frag(st + b_at[j], C::BN, u);
+      else
+        f.b[j] = *(const u32x4 *)(st + b_at[u] + j * (C::BF == kRows ? 16 * C::KB : 1024 * C::SUB));
+    }
 #pragma unroll
-      for (int j = 0; j < C::NB; ++j) {
-        if constexpr (C::BF == kCols)
-          f.b[u][j] = cols_frag(st + b_at[j], C::BN, u);
-        else
-          f.b[u][j] = *(const u32x4 *)(st + b_at[u] + j * (C::BF == kRows ? 16 * C::KB : 1024 * C::SUB));
-      }
-#pragma unroll
-      for (int i = 0; i < C::MB; ++i) {
-        if constexpr (C::AF == kCols)
-          f.a[u][i] = cols_frag(st + a_at[i], C::BM, u);
-        else
-          f.a[u][i] = *(const u32x4 *)(st + a_at[u] + i * 16 * C::KB);
-      }
+    for (int i = 0; i < C::MB; ++i) {
+      if constexpr (C::AF == kCols)
+        f.a[i] = cols_frag(st + a_at[i], C::BM, u);
+      else
+        f.a[i] = *(const u32x4 *)(st + a_at[u] + i * 16 * C::KB);
     }
   };
 
@@ -321,58 +335,57 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     for (int j = 0; j < C::NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   auto multiply = [&](const Frags &f) {
 #pragma unroll
-    for (int u = 0; u < C::SUB; ++u)
+    for (int i = 0; i < C::MB; ++i)
 #pragma unroll
-      for (int i = 0; i < C::MB; ++i)
-#pragma unroll
-        for (int j = 0; j < C::NB; ++j) {
-          if constexpr (C::I8)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, f.b[u][j]),
-                                                              __builtin_bit_cast(i32x4, f.a[u][i]), acc[i][j], 0, 0, 0);
-          else
-            acc[i][j] = mfma_bf16(f.b[u][j], f.a[u][i], acc[i][j]);
-        }
+      for (int j = 0; j < C::NB; ++j) {
+        if constexpr (C::I8)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, f.b[j]),
+                                                            __builtin_bit_cast(i32x4, f.a[i]), acc[i][j], 0, 0, 0);
+        else
+          acc[i][j] = mfma_bf16(f.b[j], f.a[i], acc[i][j]);
+      }
   };
-
-  // The fragments of stage s + 1 are read while those of stage s multiply, so
-  // no product waits for LDS; a stage's buffer is free once its fragments are
-  // in registers, and stage s + ST follows into it.
-#pragma unroll
-  for (int s = 0; s < C::ST; ++s)
-    if (s < steps) issue(s);
-  Frags f[2];
-  wait_loads<C::LOADS>(min(C::ST - 1, steps - 1));
-  __builtin_amdgcn_s_barrier();  // stage 0 is in LDS for every wave
-  read(0, f[0]);
-  auto step = [&](int s, Frags &cur, Frags &nxt) {  // s + 1 < steps
-    // stages s + 2 .. s + ST - 1 may still be out; this wave's reads of stage s are done
-    wait_loads<C::LOADS>(min(C::ST - 2, steps - 2 - s));
-    QG_WAIT_LGKMCNT0();
-    __builtin_amdgcn_s_barrier();  // stage s + 1 is in LDS; every wave holds stage s in registers
-    if (s + C::ST < steps) issue(s + C::ST);
-    read(s + 1, nxt);
-    multiply(cur);
-    constexpr int READS = C::SUB * (C::NB * (C::BF == kCols ? 2 : 1) + C::MB * (C::AF == kCols ? 2 : 1));
-    constexpr int MULS = C::SUB * C::NB * C::MB, PER = MULS / READS > 0 ? MULS / READS : 1;
+  // one LDS read, then its share of the products, and so on
+  auto interleave = [&] {
+    constexpr int READS = C::NB * (C::BF == kCols ? 2 : 1) + C::MB * (C::AF == kCols ? 2 : 1);
+    constexpr int MULS = C::NB * C::MB, PER = MULS / READS > 0 ? MULS / READS : 1;
 #pragma unroll
     for (int r = 0; r < READS; ++r) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // one LDS read,
-      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);  // then its share of the products
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
     }
     if constexpr (MULS > READS * PER) __builtin_amdgcn_sched_group_barrier(0x008, MULS - READS * PER, 0);
   };
-  int s = 0;
-  for (; s + 2 < steps; s += 2) {
-    step(s, f[0], f[1]);
-    step(s + 1, f[1], f[0]);
+
+  // While one half of a stage multiplies, the fragments of the next half are
+  // read, so no product waits for LDS.  A stage's buffer is free once the
+  // fragments of its second half are in registers; stage s + ST follows into it.
+#pragma unroll
+  for (int s = 0; s < C::ST; ++s)
+    if (s < steps) issue(s);
+  wait_loads<C::LOADS>(min(C::ST - 1, steps - 1));
+  mm_barrier();  // stage 0 is in LDS for every wave
+  Frags f[2];
+  read(0, 0, f[0]);
+  for (int s = 0; s + 1 < steps; ++s) {
+    read(s, 1, f[1]);
+    multiply(f[0]);
+    interleave();
+    // stages s + 2 .. s + ST - 1 may still be out; this wave's reads of stage s are done
+    wait_loads<C::LOADS>(min(C::ST - 2, steps - 2 - s));
+    QG_WAIT_LGKMCNT0();
+    mm_barrier();  // stage s + 1 is in LDS, stage s free
+    if (s + C::ST < steps) issue(s + C::ST);
+    read(s + 1, 0, f[0]);
+    multiply(f[1]);
+    interleave();
   }
-  step(s, f[0], f[1]);
+  read(steps - 1, 1, f[1]);
+  multiply(f[0]);
   multiply(f[1]);
 
   // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  mm_barrier();
   uint8_t *slab = smem + wave * C::SLAB;
   const int row_w = m0 + wm * C::MB * 16;           // first row of the wave
   const int col_w = n0 + wn * C::OUT_NB * 16;       // first output column of the wave
