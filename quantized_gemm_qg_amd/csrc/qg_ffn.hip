@@ -53,7 +53,9 @@ __global__ __launch_bounds__(256) void ffn_zero_kernel(uint8_t *p, int64_t ld_by
     for (int64_t c = 2 * (int64_t)threadIdx.x; c < row_bytes; c += 512) *(uint16_t *)(p + r * ld_bytes + c) = 0;
 }
 
-hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s) {
+// (bytes: only says what partial tiles the launch needs, see mm_dispatch)
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes) {
+  if (bytes) *bytes = 0;
   MmArgs a = {};
   a.a = (const uint8_t *)c.x;
   a.lda = c.ldx * 2;
@@ -70,11 +72,15 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s) {
   a.gu_type = c.gu_type;
   a.act = c.act;
   a.group_m = 4;
+  a.counters = c.counters;
+  a.partials = (uint64_t *)c.partials;
+  if (bytes && c.m <= 64) return hipSuccess;
   if (c.m <= 16) return launch_rows<false, true, 1, 2, 4, false>(a, s);
   if (c.m <= 32) return launch_rows<false, true, 2, 2, 4, false>(a, s);
   if (c.m <= 64) return launch_rows<false, true, 4, 2, 2, false>(a, s);
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 128, 2>>(a, s);
-  return launch_mm<MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 128, 2>>(a, s);
+  return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
+                     MmCfg<false, kRows, kRows, true, 128, 128, 2, 2, 2, true>,
+                     MmCfg<false, kRows, kRows, true, 64, 128, 2, 2, 4, true>>(a, s, bytes);
 }
 
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
@@ -92,7 +98,8 @@ hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *
 }
 
 // dx = [dg du] W: contraction over the 2 inter rows of W
-hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s) {
+hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s,
+                         uint64_t *bytes) {
   MmArgs a = {};
   a.a = (const uint8_t *)dgu;
   a.lda = ldd * 2;
@@ -105,13 +112,16 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddx;
   a.otype = QG_O_BF16;
   a.group_m = 4;
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 128, 2>>(a, s);
-  return launch_mm<MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 128, 2>>(a, s);
+  a.counters = c.counters;
+  a.partials = (uint64_t *)c.partials;
+  return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, false>,
+                     MmCfg<false, kRows, kCols, false, 128, 128, 2, 2, 2, true>,
+                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 2, 4, true>>(a, s, bytes);
 }
 
 // dW = [dg du]^T x: contraction over the tokens
 hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
-                         hipStream_t s) {
+                         hipStream_t s, uint64_t *bytes) {
   MmArgs a = {};
   a.a = (const uint8_t *)dgu;
   a.lda = ldd * 2;
@@ -124,8 +134,10 @@ hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.ldy = lddw;
   a.otype = dw_type;
   a.group_m = 4;
-  if (c.m >= 1000) return launch_mm<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 128, 2>>(a, s);
-  return launch_mm<MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 128, 2>>(a, s);
+  a.counters = c.counters;
+  a.partials = (uint64_t *)c.partials;
+  return mm_dispatch<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 2, false>,
+                     MmCfg<false, kCols, kCols, false, 128, 128, 2, 2, 2, true>>(a, s, bytes);
 }
 
 hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s) {

@@ -69,12 +69,27 @@ static MmArgs i8_args(const I8Call &c) {
   a.sb = c.scales;
   a.act = c.act;
   a.group_m = 4;
+  a.counters = c.counters;
+  a.partials = (uint64_t *)c.partials;
   return a;
 }
 
 // Rows whose codes the few-rows kernel holds in LDS (one workgroup then
 // leaves room for another on its CU).
 bool i8_quantizes_in_kernel(int64_t m, int64_t k) { return m <= 4 && m * rows_pitch((int)k) <= 64 * 1024; }
+
+template <bool G, int BM, int BN, int WM, int WN, int ST, bool SPLIT>
+using I8Cfg = MmCfg<true, kRows, kPacked, G, BM, BN, WM, WN, ST, SPLIT>;
+
+// bytes: see mm_dispatch
+static hipError_t i8_tiled(const I8Call &c, hipStream_t s, uint64_t *bytes) {
+  const MmArgs a = i8_args(c);
+  if (c.gated)
+    return mm_dispatch<I8Cfg<true, 256, 256, 4, 2, 2, false>, I8Cfg<true, 128, 128, 2, 2, 2, true>,
+                       I8Cfg<true, 64, 128, 2, 2, 4, true>>(a, s, bytes);
+  return mm_dispatch<I8Cfg<false, 256, 256, 4, 2, 2, false>, I8Cfg<false, 128, 128, 2, 2, 2, true>,
+                     I8Cfg<false, 64, 128, 2, 2, 4, true>>(a, s, bytes);
+}
 
 hipError_t launch_i8(const I8Call &c, hipStream_t s) {
   MmArgs a = i8_args(c);
@@ -85,12 +100,14 @@ hipError_t launch_i8(const I8Call &c, hipStream_t s) {
   if (c.m <= 16) return c.gated ? launch_rows<true, true, 1, 2, 4, false>(a, s) : launch_rows<true, false, 1, 1, 4, false>(a, s);
   if (c.m <= 32) return c.gated ? launch_rows<true, true, 2, 2, 4, false>(a, s) : launch_rows<true, false, 2, 2, 4, false>(a, s);
   if (c.m <= 64) return c.gated ? launch_rows<true, true, 4, 2, 2, false>(a, s) : launch_rows<true, false, 4, 2, 2, false>(a, s);
-  if (c.m >= 1000) {
-    if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 256, 256, 4, 2, 128, 2>>(a, s);
-    return launch_mm<MmCfg<true, kRows, kPacked, false, 256, 256, 4, 2, 128, 2>>(a, s);
-  }
-  if (c.gated) return launch_mm<MmCfg<true, kRows, kPacked, true, 128, 128, 2, 2, 128, 2>>(a, s);
-  return launch_mm<MmCfg<true, kRows, kPacked, false, 128, 128, 2, 2, 128, 2>>(a, s);
+  return i8_tiled(c, s, nullptr);
+}
+
+// Partial tiles of a call on m quantized rows.
+uint64_t i8_partial_bytes(const I8Call &c) {
+  uint64_t b = 0;
+  if (c.m > 64 && !c.quantize) i8_tiled(c, nullptr, &b);
+  return b;
 }
 
 }  // namespace qg

@@ -359,7 +359,10 @@ struct I8Call {
   void *y;
   int32_t otype;
   int64_t ldy;
+  uint32_t *counters;  // split-K counters and partial tiles (i8_partial_bytes)
+  void *partials;
 };
+uint64_t i8_partial_bytes(const I8Call &c);
 hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq, float *qs,
                                 hipStream_t s);
 bool i8_quantizes_in_kernel(int64_t m, int64_t k);
@@ -377,12 +380,16 @@ struct FfnCall {
   void *gu;
   int64_t ldgu;
   int32_t gu_type;
+  uint32_t *counters;  // split-K counters and partial tiles
+  void *partials;
 };
-hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s);
+// bytes: NULL, or the launch is only asked for the partial tiles it needs
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes = nullptr);
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s);
-hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s);
+hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s,
+                         uint64_t *bytes = nullptr);
 hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
-                         hipStream_t s);
+                         hipStream_t s, uint64_t *bytes = nullptr);
 hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s);
 // token log probabilities (qg_logprobs.hip)
 struct LogprobArgs {

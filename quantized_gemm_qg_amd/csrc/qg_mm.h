@@ -33,6 +33,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "qg_device.h"
@@ -86,15 +87,26 @@ struct MmArgs {
   int32_t gu_type;
   int32_t act;
   int32_t group_m;
+  // split over k: `per` stages each; one arrival counter per tile and the
+  // partial tiles [split][tile]
+  int32_t splits, per;
+  uint32_t *counters;
+  uint64_t *partials;
 };
+
+// Partial tiles of a call take at most this much (with the counters it fits the
+// static scratch of qg_gemm_noalloc).
+constexpr uint64_t kMmPartialBytes = (8u << 20) - (128u << 10);
 
 // 16 zero bytes that copies past the last k read
 static __device__ const uint32_t mm_zeros[4] = {0u, 0u, 0u, 0u};
 
-template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, int WN_, int KB_, int ST_>
+// SPLIT: the tile's k may be shared by several workgroups.
+template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, int WN_, int ST_, bool SPLIT_>
 struct MmCfg {
   static constexpr bool I8 = I8_, GATED = GATED_;
-  static constexpr int AF = AF_, BF = BF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, ST = ST_;
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int AF = AF_, BF = BF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = 128, ST = ST_;
   static constexpr int EL = I8 ? 1 : 2;
   static constexpr int KE = KB / EL;             // k per stage
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -109,18 +121,19 @@ struct MmCfg {
   static constexpr int SLAB = 16 * PITCH;
   static constexpr int LDS = STAGE * ST > WAVES * SLAB ? STAGE * ST : WAVES * SLAB;
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && (!GATED || NB % 2 == 0), "blocks");
-  static_assert(KB == 128, "stage depth: two MFMA steps");
   static_assert(!I8 || AF == kRows, "int8 activations are rows");
   static_assert(AF != kCols || BM >= 128, "column units for the swizzle");
   static_assert(BF != kCols || BN >= 128, "column units for the swizzle");
-  static_assert(LDS <= 160 * 1024 && ST >= 2 && ST <= 3, "LDS ring");
+  static_assert(LDS <= 160 * 1024 && ST >= 2 && ST <= 4, "LDS ring");
 };
 
-// Waits until at most `stages` (0 .. 2) stages of LOADS loads each are out.
+// Waits until at most `stages` (0 .. 3) stages of LOADS loads each are out.
 template <int LOADS>
 __device__ __forceinline__ void wait_loads(int stages) {
-  static_assert(2 * LOADS < 64, "outstanding loads");
-  if (stages >= 2) {
+  static_assert(3 * LOADS < 64, "outstanding loads");
+  if (stages >= 3) {
+    QG_WAIT_VMCNT(3 * LOADS);
+  } else if (stages == 2) {
     QG_WAIT_VMCNT(2 * LOADS);
   } else if (stages == 1) {
     QG_WAIT_VMCNT(LOADS);
@@ -166,8 +179,14 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   const int q = lane >> 4, r16 = lane & 15;
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;  // output columns per tile
 
-  int tm, tn;
-  if (!tile_of(blockIdx.x, (a.m + C::BM - 1) / C::BM, (a.n + OUT_BN - 1) / OUT_BN, a.group_m, &tm, &tn)) return;
+  const int m_tiles = (a.m + C::BM - 1) / C::BM, n_tiles = (a.n + OUT_BN - 1) / OUT_BN;
+  int tm, tn, pid = blockIdx.x, split = 0;
+  if constexpr (C::SPLIT) {
+    const int grid1 = gridDim.x / a.splits;  // a multiple of the XCDs
+    split = pid / grid1;
+    pid -= split * grid1;
+  }
+  if (!tile_of(pid, m_tiles, n_tiles, a.group_m, &tm, &tn)) return;
   const int m0 = tm * C::BM, n0 = tn * OUT_BN;
   const int rows = min(C::BM, a.m - m0);
 
@@ -243,7 +262,10 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   // bytes from one stage to the next
   const int64_t a_step = C::AF == kRows ? C::KB : (int64_t)C::KE * a.lda;
   const int64_t b_step = C::BF == kRows ? C::KB : C::BF == kPacked ? 1024 * C::SUB : (int64_t)C::KE * a.ldb;
-  const int steps = (a.kd + C::KE - 1) / C::KE;
+  // stages first .. steps - 1 of k are this workgroup's
+  const int all_steps = (a.kd + C::KE - 1) / C::KE;
+  const int first = C::SPLIT ? split * a.per : 0;
+  const int steps = C::SPLIT ? min(first + a.per, all_steps) : all_steps;
 
   const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
   auto issue = [&](int s) {
@@ -362,12 +384,12 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   // fragments of its second half are in registers; stage s + ST follows into it.
 #pragma unroll
   for (int s = 0; s < C::ST; ++s)
-    if (s < steps) issue(s);
-  wait_loads<C::LOADS>(min(C::ST - 1, steps - 1));
-  mm_barrier();  // stage 0 is in LDS for every wave
+    if (first + s < steps) issue(first + s);
+  wait_loads<C::LOADS>(min(C::ST - 1, steps - 1 - first));
+  mm_barrier();  // the first stage is in LDS for every wave
   Frags f[2];
-  read(0, 0, f[0]);
-  for (int s = 0; s + 1 < steps; ++s) {
+  read(first, 0, f[0]);
+  for (int s = first; s + 1 < steps; ++s) {
     read(s, 1, f[1]);
     multiply(f[0]);
     interleave();
@@ -383,6 +405,56 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   read(steps - 1, 1, f[1]);
   multiply(f[0]);
   multiply(f[1]);
+
+  if constexpr (C::SPLIT) {
+    if (a.splits > 1) {
+      // Publish this part of k (agent-scope stores, complete before the counter
+      // moves); the last workgroup of the tile adds the parts in their order,
+      // its own from memory like the others, and leaves the counter at zero.
+      const int tile = tm * n_tiles + tn;
+      constexpr int WORDS = C::MB * C::NB * 2 * C::THREADS;  // 8-byte words of a tile
+      auto at = [&](int p) {
+        return a.partials + ((int64_t)p * m_tiles * n_tiles + tile) * WORDS + threadIdx.x;
+      };
+      uint64_t *mine = at(split);
+#pragma unroll
+      for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j) {
+          const u32x4 w = __builtin_bit_cast(u32x4, acc[i][j]);
+          uint64_t *d = mine + (i * C::NB + j) * 2 * C::THREADS;
+          __hip_atomic_store(d, w.x | ((uint64_t)w.y << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(d + C::THREADS, w.z | ((uint64_t)w.w << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      __builtin_amdgcn_s_waitcnt(0);
+      mm_barrier();  // every wave's parts are in memory, and the ring is free
+      int *last = (int *)smem;
+      if (threadIdx.x == 0)
+        *last = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (uint32_t)(a.splits - 1);
+      __syncthreads();
+      if (!*last) return;  // uniform over the workgroup
+      __syncthreads();     // (the flag's place is written again below)
+      if (threadIdx.x == 0) __hip_atomic_store(a.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+      for (int p = 0; p < a.splits; ++p) {
+        const uint64_t *src = at(p);
+#pragma unroll
+        for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+          for (int j = 0; j < C::NB; ++j) {
+            const uint64_t *d = src + (i * C::NB + j) * 2 * C::THREADS;
+            const uint64_t lo = __hip_atomic_load(d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const uint64_t hi = __hip_atomic_load(d + C::THREADS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            acc[i][j] += __builtin_bit_cast(Acc, u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
+                                                       (uint32_t)(hi >> 32)});
+          }
+      }
+    }
+  }
 
   // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
   mm_barrier();
@@ -463,16 +535,82 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   }
 }
 
+// What a tile shape and a split of k would cost, in clocks of the busiest CU:
+// its workgroups' stages (matrix time, which workgroups of a CU share, or one
+// stage's latency where they are few), their start and end, and the sum over
+// the parts.  Latency and the fixed part are measured (one workgroup per CU,
+// operands in L2).
+struct MmPlan {
+  int splits = 1, per = 0;
+  int64_t cost = 0;
+};
 template <class C>
-static hipError_t launch_mm(const MmArgs &a, hipStream_t s) {
+static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  const int64_t m_tiles = (m + C::BM - 1) / C::BM, n_tiles = (n + OUT_BN - 1) / OUT_BN, tiles = m_tiles * n_tiles;
+  const int64_t steps = (kd + C::KE - 1) / C::KE;
+  constexpr int64_t matrix = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * 4 / 3;
+  constexpr int64_t latency = C::BM * C::BN <= 64 * 128 ? 700 : 900;
+  constexpr int64_t resident = 160 * 1024 / C::LDS;
+  constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;
+  MmPlan best;
+  const int64_t most = C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(kMmPartialBytes / (partial * tiles)) : 1;
+  for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), 32); ++want) {
+    const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
+    if (splits != want) continue;  // the same as a smaller number of parts
+    const int64_t wgs = (tiles * splits + 255) / 256, rounds = (wgs + resident - 1) / resident;
+    int64_t cost = per * std::max(wgs * matrix, rounds * latency) + 4000 * rounds;
+    if (splits > 1) cost += 2000 + splits * partial / 48;
+    if (best.cost == 0 || cost < best.cost) best = MmPlan{(int)splits, (int)per, cost};
+  }
+  return best;
+}
+
+template <class C>
+static uint64_t mm_partial_bytes(int64_t m, int64_t n, const MmPlan &p) {
+  constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  return p.splits > 1 ? (uint64_t)p.splits * ((m + C::BM - 1) / C::BM) * ((n + OUT_BN - 1) / OUT_BN) * C::BM * C::BN * 4
+                      : 0;
+}
+
+template <class C>
+static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) {
+  constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  MmArgs a = args;
+  a.splits = p.splits;
+  a.per = p.per;
+  if (p.splits > 1 && (!a.counters || !a.partials)) return hipErrorInvalidValue;
   const int64_t total = (int64_t)((a.m + C::BM - 1) / C::BM) * ((a.n + OUT_BN - 1) / OUT_BN);
-  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
+  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds * p.splits;
   auto kern = mm_kernel<C>;
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(C::THREADS), C::LDS, s, a);
   return hipGetLastError();
+}
+
+// The cheapest of the compiled shapes: launches it, or (bytes) only says what
+// partial tiles it needs.
+template <class... Cs>
+static hipError_t mm_dispatch(const MmArgs &a, hipStream_t s, uint64_t *bytes) {
+  MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd)...};
+  int best = 0;
+  for (int i = 1; i < (int)sizeof...(Cs); ++i)
+    if (plans[i].cost < plans[best].cost) best = i;
+  int i = 0;
+  hipError_t e = hipErrorInvalidValue;
+  auto one = [&](auto *cfg) {
+    using C = std::remove_pointer_t<decltype(cfg)>;
+    if (i++ != best) return;
+    if (bytes) {
+      *bytes = mm_partial_bytes<C>(a.m, a.n, plans[best]);
+      e = hipSuccess;
+    } else {
+      e = launch_mm<C>(a, plans[best], s);
+    }
+  };
+  (one((Cs *)nullptr), ...);
+  return e;
 }
 
 }  // namespace qg

@@ -14,16 +14,47 @@ static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)
 static int el_of(int otype) { return otype == QG_O_F32 ? 4 : 2; }
 static bool out_type(int t) { return t == QG_O_BF16 || t == QG_O_F32; }
 
+// Checks a workspace of `need` bytes (0: none).
+static qg_status ws_check(uint64_t need, const void *ws, uint64_t ws_bytes) {
+  if (need == 0) return QG_OK;
+  if (!ws) return QG_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
+  return aligned(ws, 256) ? QG_OK : QG_ERR_ALIGNMENT;
+}
+
 // The tiled products address a tile's rows with 32-bit offsets from a 64-bit
 // base: 256 rows of this pitch stay below 2 GiB.
 constexpr int64_t kMaxPitchBytes = 1 << 23;
 // Tiles are numbered in 32 bits (the smallest tile is 64 x 32 outputs).
 static bool tiles_fit(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 31) / 32) < (1ll << 31) - 8; }
 
-// Int8 workspace: [split-K counters][codes of the quantized rows][their scales]
+// Int8 workspace: [split-K counters][partial tiles][codes of the quantized
+// rows][their scales]; nothing where none of them is needed.
+struct I8Space {
+  uint64_t partials = 0, codes = 0, scales = 0;  // bytes
+  uint64_t total() const {
+    const uint64_t b = partials + codes + scales;
+    return b ? kSplitCounterBytes + b : 0;
+  }
+};
+static I8Space i8_space(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
+  I8Space sp;
+  I8Call c = {};
+  c.n = (int32_t)(gated ? w.desc.n / 2 : w.desc.n);
+  c.k = (int32_t)w.desc.k;
+  c.k_blocks = w.k_blocks;
+  c.gated = gated;
+  c.m = m;
+  c.quantize = (flags & QG_GEMM_QUANTIZE_X) && i8_quantizes_in_kernel(m, w.desc.k);
+  sp.partials = align_up(i8_partial_bytes(c), 256);
+  if ((flags & QG_GEMM_QUANTIZE_X) && !c.quantize) {
+    sp.codes = align_up((uint64_t)m * w.desc.k, 256);
+    sp.scales = align_up((uint64_t)m * 4, 256);
+  }
+  return sp;
+}
 uint64_t i8_ws_bytes(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
-  if (m <= 0 || !(flags & QG_GEMM_QUANTIZE_X) || i8_quantizes_in_kernel(m, w.desc.k)) return 0;
-  return kSplitCounterBytes + align_up((uint64_t)m * w.desc.k, 256) + align_up((uint64_t)m * 4, 256);
+  return m <= 0 || m > (1ll << 30) ? 0 : i8_space(w, gated, m, flags).total();
 }
 
 void i8_describe(const qg_weight &, int64_t, char *buf, uint64_t buf_bytes) {
@@ -45,12 +76,9 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
     return QG_ERR_ALIGNMENT;
   if (!quantize && !aligned(x_scales, 4)) return QG_ERR_ALIGNMENT;
   if (ldx > kMaxPitchBytes) return QG_ERR_UNSUPPORTED;
-  const uint64_t need = i8_ws_bytes(*w, gated, m, flags);
-  if (need > 0) {
-    if (!ws) return QG_ERR_INVALID_ARGUMENT;
-    if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
-    if (!aligned(ws, 256)) return QG_ERR_ALIGNMENT;
-  }
+  const I8Space sp = i8_space(*w, gated, m, flags);
+  const qg_status wst = ws_check(sp.total(), ws, ws_bytes);
+  if (wst != QG_OK) return wst;
   I8Call c = {};
   c.codes = (const uint8_t *)w->data;
   c.scales = (const float *)(c.codes + L.scales_offset);
@@ -67,9 +95,13 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
   c.otype = otype;
   c.ldy = ldy;
   c.quantize = quantize && i8_quantizes_in_kernel(m, d.k);
+  if (sp.partials) {
+    c.counters = (uint32_t *)ws;
+    c.partials = (uint8_t *)ws + kSplitCounterBytes;
+  }
   if (quantize && !c.quantize) {
-    uint8_t *q = (uint8_t *)ws + kSplitCounterBytes;
-    float *qs = (float *)(q + align_up((uint64_t)m * d.k, 256));
+    uint8_t *q = (uint8_t *)ws + kSplitCounterBytes + sp.partials;
+    float *qs = (float *)(q + sp.codes);
     const hipError_t e = launch_quantize_int8(x, m, d.k, ldx, q, d.k, qs, stream);
     if (e != hipSuccess) return hip_status(e);
     c.x = q;
@@ -104,8 +136,43 @@ static qg_status gu_check(const void *gu, int32_t gu_type, int64_t ldgu, int64_t
   return aligned(gu, 16) ? QG_OK : QG_ERR_ALIGNMENT;
 }
 
-static uint64_t ffn_dgu_bytes(int64_t m, int64_t inter) { return align_up((uint64_t)m * dgu_pitch(inter) * 2, 256); }
-
+// Workspaces: [split-K counters][partial tiles][gradient of the
+// pre-activations][the pre-activations, where they are computed again].
+struct FfnSpace {
+  uint64_t partials = 0, dgu = 0, gu = 0;  // bytes
+  uint64_t total() const {
+    const uint64_t b = partials + dgu + gu;
+    return b ? kSplitCounterBytes + b : 0;
+  }
+};
+static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bool recompute) {
+  FfnSpace sp;
+  if (m <= 0 || k <= 0 || inter <= 0 || m > (1ll << 30) || k > (1 << 22) || inter > (1 << 24)) return sp;
+  FfnCall c = {};
+  c.m = m;
+  c.k = k;
+  c.inter = inter;
+  uint64_t b = 0;
+  if (!backward || recompute) {
+    launch_ffn_forward(c, nullptr, &b);
+    sp.partials = b;
+  }
+  if (backward) {
+    launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &b);
+    sp.partials = std::max(sp.partials, b);
+    launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &b);
+    sp.partials = std::max(sp.partials, b);
+    sp.dgu = align_up((uint64_t)m * dgu_pitch(inter) * 2, 256);
+    if (recompute) sp.gu = align_up((uint64_t)m * 2 * inter * 4, 256);
+  }
+  sp.partials = align_up(sp.partials, 256);
+  return sp;
+}
+static void ffn_split_space(FfnCall *c, const FfnSpace &sp, void *ws) {
+  if (!sp.partials) return;
+  c->counters = (uint32_t *)ws;
+  c->partials = (uint8_t *)ws + kSplitCounterBytes;
+}
 }  // namespace qg
 
 using namespace qg;
@@ -146,15 +213,13 @@ extern "C" qg_status qg_gated_gemm(const qg_weight *w, const void *x, const void
 
 extern "C" qg_status qg_ffn_gated_workspace_size(int64_t m, int64_t k, int64_t inter, uint64_t *bytes) {
   if (!bytes || m < 0 || k < 0 || inter < 0) return QG_ERR_INVALID_ARGUMENT;
-  *bytes = 0;
+  *bytes = ffn_space(m, k, inter, false, false).total();
   return QG_OK;
 }
 
 extern "C" qg_status qg_ffn_gated(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k,
                                   int64_t inter, int32_t act, void *h, int64_t ldh, void *gu, int32_t gu_type,
                                   int64_t ldgu, void *ws, uint64_t ws_bytes, hipStream_t stream) {
-  (void)ws;
-  (void)ws_bytes;
   qg_status st = ffn_check(x, ldx, w, ldw, m, k, inter, act);
   if (st != QG_OK) return st;
   if (ldh < inter) return QG_ERR_SHAPE;
@@ -162,13 +227,17 @@ extern "C" qg_status qg_ffn_gated(const void *x, int64_t ldx, const void *w, int
   if (m == 0) return QG_OK;
   if (!h) return QG_ERR_INVALID_ARGUMENT;
   if (!aligned(h, 16)) return QG_ERR_ALIGNMENT;
-  return hip_status(launch_ffn_forward(FfnCall{x, ldx, w, ldw, m, k, inter, act, h, ldh, gu, ldgu, gu_type}, stream));
+  const FfnSpace sp = ffn_space(m, k, inter, false, false);
+  if ((st = ws_check(sp.total(), ws, ws_bytes)) != QG_OK) return st;
+  FfnCall c{x, ldx, w, ldw, m, k, inter, act, h, ldh, gu, ldgu, gu_type, nullptr, nullptr};
+  ffn_split_space(&c, sp, ws);
+  return hip_status(launch_ffn_forward(c, stream));
 }
 
 extern "C" qg_status qg_ffn_gated_backward_workspace_size(int64_t m, int64_t k, int64_t inter, int32_t recompute,
                                                           uint64_t *bytes) {
   if (!bytes || m < 0 || k < 0 || inter < 0) return QG_ERR_INVALID_ARGUMENT;
-  *bytes = ffn_dgu_bytes(m, inter) + (recompute ? align_up((uint64_t)m * 2 * inter * 4, 256) : 0);
+  *bytes = ffn_space(m, k, inter, true, recompute != 0).total();
   return QG_OK;
 }
 
@@ -187,23 +256,22 @@ extern "C" qg_status qg_ffn_gated_backward(const void *x, int64_t ldx, const voi
     return dw ? hip_status(launch_ffn_zero(dw, lddw * el_of(dw_type), k * el_of(dw_type), 2 * inter, stream)) : QG_OK;
   if (!dh) return QG_ERR_INVALID_ARGUMENT;
   if (!dx && !dw) return QG_OK;
-  uint64_t need = 0;
-  qg_ffn_gated_backward_workspace_size(m, k, inter, gu == nullptr, &need);
-  if (!ws) return QG_ERR_INVALID_ARGUMENT;
-  if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
-  if (!aligned(ws, 256)) return QG_ERR_ALIGNMENT;
-  FfnCall c{x, ldx, w, ldw, m, k, inter, act, nullptr, 0, const_cast<void *>(gu), ldgu, gu_type};
+  const FfnSpace sp = ffn_space(m, k, inter, true, gu == nullptr);
+  if ((st = ws_check(sp.total(), ws, ws_bytes)) != QG_OK) return st;
+  uint8_t *dgu = (uint8_t *)ws + kSplitCounterBytes + sp.partials;
+  FfnCall c{x, ldx, w, ldw, m, k, inter, act, nullptr, 0, const_cast<void *>(gu), ldgu, gu_type, nullptr, nullptr};
+  ffn_split_space(&c, sp, ws);
   hipError_t e = hipSuccess;
   if (!gu) {  // the pre-activations again, in fp32
-    c.gu = (uint8_t *)ws + ffn_dgu_bytes(m, inter);
+    c.gu = dgu + sp.dgu;
     c.ldgu = 2 * inter;
     c.gu_type = QG_O_F32;
     e = launch_ffn_forward(c, stream);
   }
   const int64_t ldd = dgu_pitch(inter);
-  if (e == hipSuccess) e = launch_ffn_dgu(c, dh, lddh, ws, ldd, stream);
-  if (e == hipSuccess && dx) e = launch_ffn_dx(c, ws, ldd, dx, lddx, stream);
-  if (e == hipSuccess && dw) e = launch_ffn_dw(c, ws, ldd, dw, dw_type, lddw, stream);
+  if (e == hipSuccess) e = launch_ffn_dgu(c, dh, lddh, dgu, ldd, stream);
+  if (e == hipSuccess && dx) e = launch_ffn_dx(c, dgu, ldd, dx, lddx, stream);
+  if (e == hipSuccess && dw) e = launch_ffn_dw(c, dgu, ldd, dw, dw_type, lddw, stream);
   return hip_status(e);
 }
 
@@ -239,12 +307,8 @@ extern "C" qg_status qg_token_logprobs(const void *logits, int32_t ltype, int64_
   if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(stats, 4) || !aligned(rank, 4) || !aligned(top_ids, 4) ||
       !aligned(top_logp, 4))
     return QG_ERR_ALIGNMENT;
-  const uint64_t need = logprobs_ws_bytes(rows, vocab, top);
-  if (need > 0) {
-    if (!ws) return QG_ERR_INVALID_ARGUMENT;
-    if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
-    if (!aligned(ws, 256)) return QG_ERR_ALIGNMENT;
-  }
+  const qg_status wst = ws_check(logprobs_ws_bytes(rows, vocab, top), ws, ws_bytes);
+  if (wst != QG_OK) return wst;
   LogprobArgs a = {};
   a.logits = logits;
   a.f32 = ltype == QG_O_F32;
