@@ -1189,8 +1189,10 @@ extern "C" qg_status qg_gemm_ex(const qg_weight *w, const void *x, const void *x
   Layout L;
   qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
-  if (L.i8)
+  if (L.i8) {
+    if ((flags & ~kI8Flags) != 0) return QG_ERR_INVALID_ARGUMENT;
     return i8_product(w, L, false, x, x_scales, m, ldx, y, otype, ldy, QG_ACT_SILU, ws, ws_bytes, flags, stream);
+  }
   const qg_layer_desc &d = w->desc;
   if (d.num_experts != 1) return QG_ERR_INVALID_ARGUMENT;
   if (m < 0 || (otype != QG_O_BF16 && otype != QG_O_F32)) return QG_ERR_INVALID_ARGUMENT;
@@ -1267,13 +1269,16 @@ extern "C" qg_status qg_gemm_noalloc(const qg_weight *w, const void *x, const vo
   if (st != QG_OK) return st;
   if (m < 0) return QG_ERR_INVALID_ARGUMENT;
   // the scratch this call needs must fit the static array
-  if (m > 0 && (L.i8 ? i8_ws_bytes(*w, false, m, 0) : dense_ws_bytes(*w, dense_variant(*w, m, 0), m)) >
+  if (m > 0 && (L.i8 ? i8_ws_bytes(*w, false, m, kI8SmallScratch) : dense_ws_bytes(*w, dense_variant(*w, m, 0), m)) >
                    QG_NOALLOC_SCRATCH_BYTES)
     return QG_ERR_BUFFER_TOO_SMALL;
   if (m == 0) return qg_gemm_ex(w, x, x_scales, m, ldx, y, otype, ldy, nullptr, 0, 0, stream);
   void *ws = nullptr;
   st = noalloc_scratch(stream, &ws);
   if (st != QG_OK) return st;
+  if (L.i8)
+    return i8_product(w, L, false, x, x_scales, m, ldx, y, otype, ldy, QG_ACT_SILU, ws, QG_NOALLOC_SCRATCH_BYTES,
+                      kI8SmallScratch, stream);
   return qg_gemm_ex(w, x, x_scales, m, ldx, y, otype, ldy, ws, QG_NOALLOC_SCRATCH_BYTES, 0, stream);
 }
 

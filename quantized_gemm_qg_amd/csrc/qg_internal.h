@@ -194,6 +194,7 @@ qg_status check_weight(const qg_weight *w, Layout *L);
 // Products of an int8 layer (qg_ops.cpp): qg_gemm's (gated false) and
 // qg_gated_gemm's, all argument checks included; the workspace both need.
 constexpr uint32_t kI8Flags = QG_GEMM_BATCH_INVARIANT | QG_GEMM_QUANTIZE_X;
+constexpr uint32_t kI8SmallScratch = 1u << 31;  // (internal) partial tiles within QG_NOALLOC_SCRATCH_BYTES
 qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void *x, const void *x_scales, int64_t m,
                      int64_t ldx, void *y, int32_t otype, int64_t ldy, int32_t act, void *ws, uint64_t ws_bytes,
                      uint32_t flags, hipStream_t stream);
@@ -350,7 +351,7 @@ struct I8Call {
   const uint8_t *codes;
   const float *scales;
   int32_t n, k, k_blocks;
-  bool gated, quantize;
+  bool gated, quantize, small_scratch;
   int32_t act;
   const void *x;
   int64_t ldx;

@@ -94,9 +94,8 @@ struct MmArgs {
   uint64_t *partials;
 };
 
-// Partial tiles of a call take at most this much (with the counters it fits the
-// static scratch of qg_gemm_noalloc).
-constexpr uint64_t kMmPartialBytes = (8u << 20) - (128u << 10);
+// Partial tiles of a call take at most this much.
+constexpr uint64_t kMmPartialBytes = 48u << 20;
 
 // 16 zero bytes that copies past the last k read
 static __device__ const uint32_t mm_zeros[4] = {0u, 0u, 0u, 0u};
@@ -477,39 +476,49 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     return v;
   };
   // writes slab i of `at(j)` to out columns col_w .. of a matrix whose column
-  // 0 is at element `shift` of its rows
-  auto store = [&](int i, auto &&at, void *out, int64_t ld, int otype, int64_t shift) {
-    const int el = otype == QG_O_F32 ? 4 : 2;
+  // 0 is at element `shift` of its rows; the element type is a constant, so the
+  // addresses need no division and the copies unroll
+  auto store_as = [&](auto f32, int i, auto &at, void *out, int64_t ld, int64_t shift) {
+    constexpr bool F32 = decltype(f32)::value;
+    constexpr int EL = F32 ? 4 : 2, CHUNKS = 16 * C::OUT_NB * EL / 16, PER = 16 / EL;
+    constexpr int ROWS = 64 / CHUNKS > 16 ? 16 : 64 / CHUNKS;  // rows per pass of the wave
 #pragma unroll
     for (int j = 0; j < C::OUT_NB; ++j) {
       const f32x4 v = at(j);
-      uint8_t *p = slab + r16 * C::PITCH + (16 * j + 4 * q) * el;
-      if (otype == QG_O_F32)
+      uint8_t *p = slab + r16 * C::PITCH + (16 * j + 4 * q) * EL;
+      if constexpr (F32)
         *(f32x4 *)p = v;
       else
         *(uint2 *)p = uint2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, before its reads
-    const int cpr = 16 * C::OUT_NB * el / 16, per = 16 / el;
-    for (int t = lane; t < 16 * cpr; t += 64) {
-      const int rr = t / cpr, c = (t % cpr) * per;
-      const int row = row_w + 16 * i + rr, col = col_w + c;
-      if (row >= a.m || col >= a.n) continue;
-      const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * el);
-      uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * el;
-      if (col + per <= a.n) {
+    const int c = (lane % CHUNKS) * PER, col = col_w + c;
+#pragma unroll
+    for (int r0 = 0; r0 < 16; r0 += ROWS) {
+      const int rr = r0 + lane / CHUNKS, row = row_w + 16 * i + rr;
+      if (lane >= ROWS * CHUNKS || row >= a.m || col >= a.n) continue;
+      const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * EL);
+      uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * EL;
+      if (col + PER <= a.n) {
         *(u32x4_any *)dst = v;
       } else {
-        for (int b = 0; b < a.n - col; ++b) {
-          const uint32_t w = el == 4 ? v[b] : v[b >> 1] >> (16 * (b & 1));
-          if (el == 4)
-            ((uint32_t *)dst)[b] = w;
+#pragma unroll
+        for (int b = 0; b < PER; ++b) {
+          if (b >= a.n - col) continue;
+          if constexpr (F32)
+            ((uint32_t *)dst)[b] = v[b];
           else
-            ((uint16_t *)dst)[b] = (uint16_t)w;
+            ((uint16_t *)dst)[b] = (uint16_t)(v[b >> 1] >> (16 * (b & 1)));
         }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the reads, before the slab's next writes
+  };
+  auto store = [&](int i, auto &&at, void *out, int64_t ld, int otype, int64_t shift) {
+    if (otype == QG_O_F32)
+      store_as(std::true_type{}, i, at, out, ld, shift);
+    else
+      store_as(std::false_type{}, i, at, out, ld, shift);
   };
 #pragma unroll
   for (int i = 0; i < C::MB; ++i) {
@@ -545,16 +554,18 @@ struct MmPlan {
   int64_t cost = 0;
 };
 template <class C>
-static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd) {
+static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
   const int64_t m_tiles = (m + C::BM - 1) / C::BM, n_tiles = (n + OUT_BN - 1) / OUT_BN, tiles = m_tiles * n_tiles;
   const int64_t steps = (kd + C::KE - 1) / C::KE;
-  constexpr int64_t matrix = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * 4 / 3;
-  constexpr int64_t latency = C::BM * C::BN <= 64 * 128 ? 700 : 900;
+  // (measured over the instruction's own time: 1.7 for 256 x 256 tiles, 2.1 for
+  // the smaller ones, whose operands take more of the way)
+  constexpr int64_t matrix = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * (C::BM == 256 ? 17 : 21) / 10;
+  constexpr int64_t latency = C::BM == 64 ? 700 : C::ST == 2 ? 1170 : 900;
   constexpr int64_t resident = 160 * 1024 / C::LDS;
   constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;
   MmPlan best;
-  const int64_t most = C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(kMmPartialBytes / (partial * tiles)) : 1;
+  const int64_t most = C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(budget / (uint64_t)(partial * tiles)) : 1;
   for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), 32); ++want) {
     const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
     if (splits != want) continue;  // the same as a smaller number of parts
@@ -592,8 +603,8 @@ static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) 
 // The cheapest of the compiled shapes: launches it, or (bytes) only says what
 // partial tiles it needs.
 template <class... Cs>
-static hipError_t mm_dispatch(const MmArgs &a, hipStream_t s, uint64_t *bytes) {
-  MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd)...};
+static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, uint64_t *bytes) {
+  MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
   int best = 0;
   for (int i = 1; i < (int)sizeof...(Cs); ++i)
     if (plans[i].cost < plans[best].cost) best = i;

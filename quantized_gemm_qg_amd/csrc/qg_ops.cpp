@@ -45,6 +45,7 @@ static I8Space i8_space(const qg_weight &w, bool gated, int64_t m, uint32_t flag
   c.k_blocks = w.k_blocks;
   c.gated = gated;
   c.m = m;
+  c.small_scratch = (flags & kI8SmallScratch) != 0;
   c.quantize = (flags & QG_GEMM_QUANTIZE_X) && i8_quantizes_in_kernel(m, w.desc.k);
   sp.partials = align_up(i8_partial_bytes(c), 256);
   if ((flags & QG_GEMM_QUANTIZE_X) && !c.quantize) {
@@ -67,7 +68,7 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
   const qg_layer_desc &d = w->desc;
   const bool quantize = (flags & QG_GEMM_QUANTIZE_X) != 0;
   const int64_t n = gated ? d.n / 2 : d.n;
-  if (m < 0 || !out_type(otype) || (flags & ~kI8Flags) != 0) return QG_ERR_INVALID_ARGUMENT;
+  if (m < 0 || !out_type(otype) || (flags & ~(kI8Flags | kI8SmallScratch)) != 0) return QG_ERR_INVALID_ARGUMENT;
   if (m > (1ll << 30) || !tiles_fit(m, n)) return QG_ERR_UNSUPPORTED;
   if (m == 0) return QG_OK;
   if (!x || !y || (!quantize && !x_scales)) return QG_ERR_INVALID_ARGUMENT;
@@ -95,6 +96,7 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
   c.otype = otype;
   c.ldy = ldy;
   c.quantize = quantize && i8_quantizes_in_kernel(m, d.k);
+  c.small_scratch = (flags & kI8SmallScratch) != 0;
   if (sp.partials) {
     c.counters = (uint32_t *)ws;
     c.partials = (uint8_t *)ws + kSplitCounterBytes;
@@ -205,7 +207,7 @@ extern "C" qg_status qg_gated_gemm(const qg_weight *w, const void *x, const void
   Layout L;
   const qg_status st = check_weight(w, &L);
   if (st != QG_OK) return st;
-  if (act != QG_ACT_SILU && act != QG_ACT_GELU_TANH) return QG_ERR_INVALID_ARGUMENT;
+  if ((act != QG_ACT_SILU && act != QG_ACT_GELU_TANH) || (flags & ~kI8Flags) != 0) return QG_ERR_INVALID_ARGUMENT;
   if (!L.i8) return QG_ERR_UNSUPPORTED;
   if (w->desc.n % 2 != 0) return QG_ERR_SHAPE;
   return i8_product(w, L, true, x, x_scales, m, ldx, h, otype, ldh, act, ws, ws_bytes, flags, stream);
