@@ -439,18 +439,29 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
       for (int i = 0; i < C::MB; ++i)
 #pragma unroll
         for (int j = 0; j < C::NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-      for (int p = 0; p < a.splits; ++p) {
-        const uint64_t *src = at(p);
+      // (the loads of GO parts go out together: one part's latency, not each's)
+      constexpr int GO = C::MB * C::NB <= 4 ? 4 : 2;
+      for (int p0 = 0; p0 < a.splits; p0 += GO) {
+        uint64_t w[GO][C::MB * C::NB][2];
 #pragma unroll
-        for (int i = 0; i < C::MB; ++i)
+        for (int g = 0; g < GO; ++g) {
+          const uint64_t *src = at(min(p0 + g, a.splits - 1));
 #pragma unroll
-          for (int j = 0; j < C::NB; ++j) {
-            const uint64_t *d = src + (i * C::NB + j) * 2 * C::THREADS;
-            const uint64_t lo = __hip_atomic_load(d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const uint64_t hi = __hip_atomic_load(d + C::THREADS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            acc[i][j] += __builtin_bit_cast(Acc, u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
-                                                       (uint32_t)(hi >> 32)});
+          for (int b = 0; b < C::MB * C::NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[g][b][h] = __hip_atomic_load(src + (2 * b + h) * C::THREADS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int g = 0; g < GO; ++g) {
+          if (p0 + g >= a.splits) continue;
+#pragma unroll
+          for (int b = 0; b < C::MB * C::NB; ++b) {
+            const u32x4 v = {(uint32_t)w[g][b][0], (uint32_t)(w[g][b][0] >> 32), (uint32_t)w[g][b][1],
+                             (uint32_t)(w[g][b][1] >> 32)};
+            acc[b / C::NB][b % C::NB] += __builtin_bit_cast(Acc, v);
           }
+        }
       }
     }
   }
@@ -571,7 +582,7 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
     if (splits != want) continue;  // the same as a smaller number of parts
     const int64_t wgs = (tiles * splits + 255) / 256, rounds = (wgs + resident - 1) / resident;
     int64_t cost = per * std::max(wgs * matrix, rounds * latency) + 4000 * rounds;
-    if (splits > 1) cost += 2000 + splits * partial / 48;
+    if (splits > 1) cost += 6000 + splits * partial / 24;
     if (best.cost == 0 || cost < best.cost) best = MmPlan{(int)splits, (int)per, cost};
   }
   return best;
