@@ -39,22 +39,27 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCap = 1024;       // candidates of one chunk
 constexpr int kMaxParts = 64;    // workgroups per row
+static_assert(kCap <= kMaxParts * QG_MAX_ALTERNATIVES, "candidate buffer");
 constexpr int kRecordKeys = kMaxParts * QG_MAX_ALTERNATIVES / kThreads;  // keys of a row's parts, per thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
+// Order of floats as unsigned numbers (no NaN), and back.
+__device__ __forceinline__ uint32_t order_bits(float l) {
+  const uint32_t u = __float_as_uint(l);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
+}
+
 // Order of alternatives as one key: larger logits first, equal ones by lower
 // id (-0 equals +0).
 __device__ __forceinline__ uint64_t alt_key(float l, uint32_t id) {
-  uint32_t u = __float_as_uint(l + 0.f);
-  u = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-  return ((uint64_t)u << 32) | (0xFFFFFFFFu - id);
+  return ((uint64_t)order_bits(l + 0.f) << 32) | (0xFFFFFFFFu - id);
 }
-__device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t u = (uint32_t)(k >> 32);
-  return __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
-}
+__device__ __forceinline__ float key_value(uint64_t k) { return order_value((uint32_t)(k >> 32)); }
 __device__ __forceinline__ int key_id(uint64_t k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
 
 // The largest of three (a NaN loses against a number).  Written out because
@@ -71,17 +76,16 @@ __device__ __forceinline__ float next_above(float l) {
   return u == 0x7F800000u ? l : __uint_as_float((u & 0x80000000u) ? u - 1 : u + 1);
 }
 
-// The value of rank `place` (0 = largest) among the 64 lanes' v.
-__device__ __forceinline__ float wave_rank_value(float v, int place) {
-  const int lane = threadIdx.x & 63;
-  int above = 0;
-#pragma unroll 8
-  for (int g = 0; g < 64; ++g) {
-    const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), g));
-    above += (o > v || (o == v && g < lane)) ? 1 : 0;
+// A number that at least `top` (<= 64) of the 64 lanes' u reach: the top-th
+// largest with its low 12 bits cleared, found bit by bit from ballots.
+__device__ __forceinline__ uint32_t wave_bound(uint32_t u, int top) {
+  uint32_t bound = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 12; --bit) {
+    const uint32_t next = bound | (1u << bit);
+    if (__popcll(__ballot(u >= next)) >= top) bound = next;
   }
-  const int at = __ffsll((unsigned long long)__ballot(above == place)) - 1;
-  return __shfl(v, at);
+  return bound;
 }
 
 // Running maximum and sums (log2 scale: the exponent is c2 (l - m))
@@ -99,7 +103,7 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float c2) {
 }
 
 struct Shared {
-  uint64_t cand[kCap + QG_MAX_ALTERNATIVES];
+  uint64_t cand[kMaxParts * QG_MAX_ALTERNATIVES + QG_MAX_ALTERNATIVES];
   uint64_t list[QG_MAX_ALTERNATIVES];
   float group[64];
   Sums sums[kWaves];
@@ -115,6 +119,7 @@ template <bool F32, int VEC>
 struct Chunk {
   static constexpr int EPV = F32 ? 4 : 8;            // logits per 16 bytes
   static constexpr int EL = F32 ? 4 : 2;
+  static constexpr bool SPREAD = VEC <= 2;
   static constexpr uint32_t NONE = F32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
   static constexpr int SIZE = kThreads * VEC * EPV;  // logits per chunk
   u32x4 d[VEC];
@@ -163,16 +168,18 @@ struct Chunk {
     else
       return __uint_as_float((e & 1) ? d[v][e / 2] & 0xFFFF0000u : d[v][e / 2] << 16);
   }
-  // The thread's place in a chunk at `first` (a wave's 16 bytes x VEC are
-  // contiguous: one address, small offsets), opaque to the compiler: it would
+  // The thread's place in a chunk at `first` (large chunks: a wave's 16 bytes x
+  // VEC are contiguous, one address with small offsets; small ones: 16 bytes of
+  // every thread, then the next of every thread, so that a short row still
+  // gives every group of threads a maximum), opaque to the compiler: it would
   // keep everything that follows from it for every v, in a register each.
   __device__ __forceinline__ static int base_of(int first) {
-    int base = first + (((int)threadIdx.x >> 6) * VEC * 64 + ((int)threadIdx.x & 63)) * EPV;
+    int base = first + (SPREAD ? (int)threadIdx.x : ((int)threadIdx.x >> 6) * VEC * 64 + ((int)threadIdx.x & 63)) * EPV;
     asm volatile("" : "+v"(base));
     return base;
   }
   // first logit of its v-th 16 bytes: their place, and where they were read
-  __device__ __forceinline__ static int place(int base, int v) { return base + v * 64 * EPV; }
+  __device__ __forceinline__ static int place(int base, int v) { return base + v * (SPREAD ? kThreads : 64) * EPV; }
   __device__ __forceinline__ static int id(int base, int v, int vocab) {
     return max(min(place(base, v), vocab - EPV), 0);
   }
@@ -181,8 +188,10 @@ struct Chunk {
 // Merges sh.cand[0 .. n) and sh.list[0 .. have) into sh.list; returns its
 // length.  All threads call; the candidates are visible before the call.
 __device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) {
-  for (int i = threadIdx.x; i < have; i += kThreads) sh.cand[n + i] = sh.list[i];
-  __syncthreads();
+  if (have > 0) {
+    for (int i = threadIdx.x; i < have; i += kThreads) sh.cand[n + i] = sh.list[i];
+    __syncthreads();
+  }
   const int all = n + have;
   for (int i = threadIdx.x; i < all; i += kThreads) {
     const uint64_t k = sh.cand[i];
@@ -199,7 +208,8 @@ __device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) 
 // each of the thread's 16 bytes, most: of all.  Uniform over the workgroup;
 // returns the list's length.
 template <bool F32, int VEC>
-__device__ __forceinline__ int take_alternatives(Shared &sh, const float (&vmax)[VEC], const uint8_t *row, int vocab, int first, float most, int have,
+__device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VEC> &ch, const float (&vmax)[VEC],
+                                                 const uint8_t *row, int vocab, int first, float most, int have,
                                                  int top) {
   using C = Chunk<F32, VEC>;
   const float last = have == top ? key_value(sh.list[top - 1]) : neg_inf();
@@ -207,36 +217,46 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const float (&vmax)
   float bound = next_above(last);  // candidates: l >= bound
   for (int attempt = have == top ? 0 : 1; attempt < 2; ++attempt) {
     if (attempt == 1) {
-      // the top-th largest of the 64 group maxima
+      // what `top` of the 64 group maxima reach
       float g = fmaxf(most, __shfl_xor(most, 1));
       g = fmaxf(g, __shfl_xor(g, 2));
       if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = g;
       __syncthreads();
-      bound = fmaxf(bound, wave_rank_value(sh.group[threadIdx.x & 63], top - 1));
+      bound = fmaxf(bound, order_value(max(wave_bound(order_bits(sh.group[threadIdx.x & 63]), top),
+                                           order_bits(-3.402823466e38f))));
     }
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    // the few 16 bytes that hold candidates are read again (they are in the
-    // caches): unrolled over the registers instead, this search would cost the
-    // kernel half its occupancy
-    uint32_t hit = 0;
+    auto push = [&](float l, int id) {
+      if (l >= bound) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)id);
+      }
+    };
     const int base = C::base_of(first);
+    if constexpr (VEC <= 2) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) hit |= vmax[v] >= bound ? 1u << v : 0u;
-    while (hit != 0) {
-      const int v = __ffs(hit) - 1;
-      hit &= hit - 1;
-      const int i = C::place(base, v);
-      Chunk<F32, 1> one;
-      one.load16(0, row, i, vocab);
-      const int at0 = C::id(base, v, vocab);
+      for (int v = 0; v < VEC; ++v)
+        if (vmax[v] >= bound) {
+          const int at0 = C::id(base, v, vocab);
 #pragma unroll
-      for (int e = 0; e < C::EPV; ++e) {
-        const float l = one.at(0, e);
-        if (l >= bound) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)(at0 + e));
+          for (int e = 0; e < C::EPV; ++e) push(ch.at(v, e), at0 + e);
         }
+    } else {
+      // the few 16 bytes that hold candidates are read again (they are in the
+      // caches): unrolled over the registers, this search would cost the kernel
+      // half its occupancy
+      uint32_t hit = 0;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) hit |= vmax[v] >= bound ? 1u << v : 0u;
+      while (hit != 0) {
+        const int v = __ffs(hit) - 1;
+        hit &= hit - 1;
+        Chunk<F32, 1> one;
+        one.load16(0, row, C::place(base, v), vocab);
+        const int at0 = C::id(base, v, vocab);
+#pragma unroll
+        for (int e = 0; e < C::EPV; ++e) push(one.at(0, e), at0 + e);
       }
     }
     __syncthreads();
@@ -326,7 +346,7 @@ __global__ __launch_bounds__(kThreads, SHARED ? 4 : 5) void logprobs_kernel(Logp
       }
       st = Sums{m, s, t};
       above += hits;
-      if (a.top > 0) have = take_alternatives<F32, VEC>(sh, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
+      if (a.top > 0) have = take_alternatives<F32, VEC>(sh, ch, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
     }
     // join the threads, then the waves
 #pragma unroll
@@ -395,20 +415,12 @@ __global__ __launch_bounds__(kThreads, SHARED ? 4 : 5) void logprobs_kernel(Logp
         above += __shfl_xor(above, off);
       }
       if (a.top > 0) {
-        // the first `deep` keys of each list hold at least `top` keys: their
-        // top-th largest is a bound that at most max(top^2, parts top) keys of
-        // the sorted lists reach, within the buffer
+        // the first `deep` keys of each list are at least `top` keys: what `top`
+        // of their values reach bounds the list (ties and all, the buffer holds
+        // every key of every part)
         const int deep = (a.top + parts - 1) / parts;
         const uint64_t mine = lane < parts * deep ? key(lane % parts, lane / parts) : 0;
-        int larger = 0;
-#pragma unroll 8
-        for (int g = 0; g < 64; ++g) {
-          const uint64_t o = ((uint64_t)__builtin_amdgcn_readlane((uint32_t)(mine >> 32), g) << 32) |
-                             (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine, g);
-          larger += (o > mine || (o == mine && g < lane)) ? 1 : 0;
-        }
-        const int at = __ffsll((unsigned long long)__ballot(larger == a.top - 1)) - 1;
-        const uint64_t bound = __shfl((unsigned long long)mine, at);
+        const uint64_t bound = (uint64_t)wave_bound((uint32_t)(mine >> 32), a.top) << 32;
         if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
 #pragma unroll
@@ -502,18 +514,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 }
 
 namespace {
-// Chunks of 2 x 16 bytes per thread while 8 x 16 would leave CUs without a
-// workgroup; then rows are shared by so many workgroups that each CU gets
-// about four (at most one chunk each, kMaxParts).
+// Chunks of 8 x 16 bytes per thread, or 2 x 16 where those would leave CUs
+// without a workgroup or exceed the row.  Rows are shared by so many workgroups
+// that each CU gets about three (at most one chunk each, kMaxParts).
 struct Split {
   bool small;
   int parts;
 };
 Split logprobs_split(int64_t rows, int64_t vocab, bool f32) {
   const int64_t big = (f32 ? 4 : 8) * kThreads * 8;
-  const bool small = rows * ((vocab + big - 1) / big) < 256;
+  const bool small = vocab < big || rows * ((vocab + big - 1) / big) < 256;
   const int64_t size = small ? big / 4 : big, chunks = (vocab + size - 1) / size;
-  const int64_t want = (1024 + rows - 1) / rows;
+  const int64_t want = (768 + rows - 1) / rows;
   return Split{small, (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, chunks), kMaxParts))};
 }
 }  // namespace
