@@ -93,10 +93,8 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes) 
   a.group_m = 4;
   a.counters = c.counters;
   a.partials = (uint64_t *)c.partials;
-  if (bytes && c.m <= 64) return hipSuccess;
-  if (c.m <= 16) return launch_rows<false, true, 1, 2, 4, false>(a, s);
-  if (c.m <= 32) return launch_rows<false, true, 2, 2, 4, false>(a, s);
-  if (c.m <= 64) return launch_rows<false, true, 4, 2, 2, false>(a, s);
+  // (24 rows of 14336 x 4096: 51.9 us tiled, 71.4 with two row blocks here)
+  if (c.m <= 16) return bytes ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
   return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 4, true>,
