@@ -106,9 +106,12 @@ static MmArgs i8_args(const I8Call &c) {
   return a;
 }
 
-// Rows whose codes the few-rows kernel holds in LDS (one workgroup then
-// leaves room for another on its CU).
-bool i8_quantizes_in_kernel(int64_t m, int64_t k) { return m <= 4 && m * rows_pitch((int)k) <= 64 * 1024; }
+// Rows that the few-rows kernel quantizes for itself: one (14336 x 4096: 13.7 us,
+// 17.6 with a launch of its own for the quantization), or a few short ones
+// (2 x 1024: 5.7 against 7.6 us; 2 x 4096: 10.6 against 8.5).
+bool i8_quantizes_in_kernel(int64_t m, int64_t k) {
+  return m == 1 ? rows_pitch((int)k) <= 64 * 1024 : m <= 4 && m * k <= 2048;
+}
 
 template <bool G, int BM, int BN, int WM, int WN, int ST, bool SPLIT>
 using I8Cfg = MmCfg<true, kRows, kPacked, G, BM, BN, WM, WN, ST, SPLIT>;

@@ -98,9 +98,22 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs 
       }
     }
   };
+  // one row to quantize: its first 16-byte units per thread, asked for ahead of
+  // the weights (loads return in order, so behind them they would wait for all)
+  constexpr int XV = FUSEQ ? 4 : 1;
+  u32x4 xv[XV];
+  if constexpr (FUSEQ) {
+#pragma unroll
+    for (int i = 0; i < XV; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      xv[i] = a.m == 1 && c < a.kd / 8 ? *(const u32x4 *)(a.a + 16 * c) : u32x4{0u, 0u, 0u, 0u};
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
 #pragma unroll
   for (int r = 0; r < KR; ++r)
     if (b_begin + r < b_end) load(b_begin + r, r);
+  __builtin_amdgcn_sched_barrier(0);
 
   const int pitch = rows_pitch(a.kd);
   float *row_scale = nullptr;
@@ -108,29 +121,52 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs 
   if constexpr (FUSEQ) {
     row_scale = (float *)(smem + a.m * pitch);
     red = (uint8_t *)row_scale + 256;
-    for (int r = 0; r < a.m; ++r) {
-      const uint8_t *xr = a.a + (int64_t)r * a.lda;
-      float most = 0.f;
-      for (int c = threadIdx.x; c < a.kd / 8; c += blockDim.x) {
-        float v[8];
-        unpack8(*(const u32x4 *)(xr + 16 * c), v);
+    auto largest_of = [](const u32x4 &w, float most) {
+      float v[8];
+      unpack8(w, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
-      }
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
+      return most;
+    };
+    auto largest = [&](const uint8_t *xr, int c0, int step, float most) {
+      for (int c = c0; c < a.kd / 8; c += step) most = largest_of(*(const u32x4 *)(xr + 16 * c), most);
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) most = fmaxf(most, __shfl_xor(most, off));
+      return most;
+    };
+    auto put = [&](int r, int c, const u32x4 &w, float s) {
+      float v[8];
+      unpack8(w, v);
+      *(uint2 *)(smem + r * pitch + 8 * c) = uint2{i8_codes4(v, s), i8_codes4(v + 4, s)};
+    };
+    auto codes = [&](int r, const uint8_t *xr, float s, int c0, int step) {
+      for (int c = c0; c < a.kd / 8; c += step) put(r, c, *(const u32x4 *)(xr + 16 * c), s);
+    };
+    if (a.m == 1) {  // one row: the whole workgroup
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < XV; ++i) most = largest_of(xv[i], most);
+      most = largest(a.a, threadIdx.x + XV * blockDim.x, blockDim.x, most);
       if (lane == 0) row_max[wave] = most;
       __syncthreads();
       for (int w = 0; w < waves; ++w) most = fmaxf(most, row_max[w]);
       const float s = i8_scale(most);
-      for (int c = threadIdx.x; c < a.kd / 8; c += blockDim.x) {
-        float v[8];
-        unpack8(*(const u32x4 *)(xr + 16 * c), v);
-        *(uint2 *)(smem + r * pitch + 8 * c) = uint2{i8_codes4(v, s), i8_codes4(v + 4, s)};
+#pragma unroll
+      for (int i = 0; i < XV; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < a.kd / 8) put(0, c, xv[i], s);
       }
-      if (threadIdx.x == 0) row_scale[r] = s;
-      __syncthreads();  // row_max is used again; the last barrier publishes the codes
+      codes(0, a.a, s, threadIdx.x + XV * blockDim.x, blockDim.x);
+      if (threadIdx.x == 0) row_scale[0] = s;
+    } else {  // a row per wave, without barriers between them
+      for (int r = wave; r < a.m; r += waves) {
+        const uint8_t *xr = a.a + (int64_t)r * a.lda;
+        const float s = i8_scale(largest(xr, lane, 64, 0.f));
+        codes(r, xr, s, lane, 64);
+        if (lane == 0) row_scale[r] = s;
+      }
     }
+    __syncthreads();
   }
 
   Acc acc[MT][NT];
