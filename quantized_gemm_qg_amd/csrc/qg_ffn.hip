@@ -93,8 +93,12 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes) 
   a.group_m = 4;
   a.counters = c.counters;
   a.partials = (uint64_t *)c.partials;
-  // (24 rows of 14336 x 4096: 51.9 us tiled, 71.4 with two row blocks here)
-  if (c.m <= 16) return bytes ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
+  // Few rows: a workgroup per 16 columns with all of K, unless long rows meet few
+  // columns, where the tiled kernel's parts of k occupy more CUs (16384 x 128: 19
+  // us against 34; 8192 x 600: 15 against 18; 8192 x 2400: 22.4 against 21.2).
+  // From 17 rows on tiled (24 rows of 14336 x 4096: 51.9 us, 71.4 with two row
+  // blocks here).
+  if (c.m <= 16 && (c.k < 6144 || c.inter > 1536)) return bytes ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
   return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 4, true>,

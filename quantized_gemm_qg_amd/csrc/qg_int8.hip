@@ -131,9 +131,13 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, uint64_t *bytes) {
 }
 
 // Calls of the few-rows kernel: up to 16 rows, and up to 32 where N gives the
-// tiled kernel less than half a round of 128-column tiles (23 rows of 4096 x
-// 14336: 14.9 us against 18.5; 32 rows of 14336 x 4096: 19.0 against 15.5).
-static bool i8_few_rows(const I8Call &c) { return c.m <= 16 || (c.m <= 32 && !c.gated && c.n < 8192); }
+// tiled kernel less than half a round of 128-column tiles and the rows are not
+// too long to be read by every workgroup (23 rows of 4096 x 14336: 16.0 us
+// against 18.2 tiled; 32 rows of 8192: 10.8 against 13.1, of 16384: 18.5 against
+// 14.4; 32 rows of 14336 x 4096: 19.0 against 15.5).
+static bool i8_few_rows(const I8Call &c) {
+  return c.m <= 16 || (c.m <= 32 && !c.gated && c.n < 8192 && c.m * c.k <= 24 * 14336);
+}
 
 hipError_t launch_i8(const I8Call &c, hipStream_t s) {
   MmArgs a = i8_args(c);

@@ -50,7 +50,7 @@ template <bool I8, bool GATED>
 constexpr int rows_waves() { return I8 && GATED ? 4 : 8; }
 
 template <bool I8, bool GATED, int MT, int NT, int KR, bool FUSEQ>
-__global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs a) {
+__global__ __launch_bounds__((I8 && GATED) ? 256 : 512, MT == 1 ? 4 : 3) void rows_kernel(MmArgs a) {
   static_assert(!FUSEQ || (I8 && MT == 1), "quantized rows in LDS");
   static_assert(!GATED || NT == 2, "a gate strip and its up strip");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -88,14 +88,17 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs 
   u32x4 bw[KR][NT][2], aw[FUSEQ ? 1 : KR][MT][2];
   auto load = [&](int b, int r) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int t = 0; t < NT; ++t) {
+      const uint8_t *u = bp[t] + (int64_t)b * (I8 ? 2048 : 128);  // uniform
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        bw[r][t][h] = *(const u32x4 *)(bp[t] + (int64_t)b * (I8 ? 2048 : 128) + bo[t] + (I8 ? 1024 : 64) * h);
-      if constexpr (!FUSEQ) {
+      for (int h = 0; h < 2; ++h) bw[r][t][h] = *(const u32x4 *)(u + bo[t] + (I8 ? 1024 : 64) * h);
+    }
+    if constexpr (!FUSEQ) {
+      const uint8_t *u = a.a + (int64_t)b * 128;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) aw[r][i][h] = *(const u32x4 *)(a.a + (int64_t)b * 128 + ao[i] + 64 * h);
-      }
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) aw[r][i][h] = *(const u32x4 *)(u + ao[i] + 64 * h);
     }
   };
   // one row to quantize: its first 16-byte units per thread, asked for ahead of
@@ -110,9 +113,14 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs 
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  // (where a run ends inside KR blocks its last one is loaded again: under a
+  // condition of its own a load would leave the compiler no count to wait by,
+  // and it would wait for all of them)
+  const bool any = b_begin < b_end;
+  if (any) {
 #pragma unroll
-  for (int r = 0; r < KR; ++r)
-    if (b_begin + r < b_end) load(b_begin + r, r);
+    for (int r = 0; r < KR; ++r) load(min(b_begin + r, b_end - 1), r);
+  }
   __builtin_amdgcn_sched_barrier(0);
 
   const int pitch = rows_pitch(a.kd);
@@ -194,24 +202,19 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512) void rows_kernel(MmArgs 
         }
       }
   };
-  int b = b_begin;
-  for (; b + 2 * KR <= b_end; b += KR) {
+  if (any) {
+    int b = b_begin;
+    for (; b + KR < b_end; b += KR) {
 #pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      multiply(b + r, r);
-      load(b + KR + r, r);
+      for (int r = 0; r < KR; ++r) {
+        multiply(b + r, r);
+        load(min(b + KR + r, b_end - 1), r);
+      }
     }
-  }
 #pragma unroll
-  for (int r = 0; r < KR; ++r) {
-    if (b + r >= b_end) continue;
-    multiply(b + r, r);
-    if (b + KR + r < b_end) load(b + KR + r, r);
+    for (int r = 0; r < KR; ++r)
+      if (b + r < b_end) multiply(b + r, r);
   }
-  b += KR;
-#pragma unroll
-  for (int r = 0; r < KR - 1; ++r)
-    if (b + r < b_end) multiply(b + r, r);
   if (wave == waves - 1 && blocks * KE < a.kd) {
     // the block that K ends in: lanes behind the end read zeros for both
     // operands (int8 weights are padded with zeros: the rows read their first
