@@ -1909,7 +1909,7 @@ extern "C" qg_status qg_describe_dispatch_ex(const qg_weight *w, int64_t m, uint
   if (!buf || buf_bytes == 0 || m < 0 || (flags & ~(L.i8 ? kI8Flags : (uint32_t)QG_GEMM_BATCH_INVARIANT)) != 0)
     return QG_ERR_INVALID_ARGUMENT;
   if (L.i8) {
-    i8_describe(*w, m, buf, buf_bytes);
+    i8_describe(*w, m, flags, buf, buf_bytes);
     return QG_OK;
   }
   if (flags && w->desc.num_experts > 1) return QG_ERR_INVALID_ARGUMENT;

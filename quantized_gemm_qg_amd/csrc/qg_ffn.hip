@@ -72,9 +72,9 @@ __global__ __launch_bounds__(256) void ffn_zero_kernel(uint8_t *p, int64_t ld_by
     for (int64_t c = 2 * (int64_t)threadIdx.x; c < row_bytes; c += 512) *(uint16_t *)(p + r * ld_bytes + c) = 0;
 }
 
-// (bytes: only says what partial tiles the launch needs, see mm_dispatch)
-hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes) {
-  if (bytes) *bytes = 0;
+// (info: nothing is launched, see mm_dispatch)
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info) {
+  if (info) *info = MmInfo();
   MmArgs a = {};
   a.a = (const uint8_t *)c.x;
   a.lda = c.ldx * 2;
@@ -98,11 +98,11 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes) 
   // us against 34; 8192 x 600: 15 against 18; 8192 x 2400: 22.4 against 21.2).
   // From 17 rows on tiled (24 rows of 14336 x 4096: 51.9 us, 71.4 with two row
   // blocks here).
-  if (c.m <= 16 && (c.k < 6144 || c.inter > 1536)) return bytes ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
+  if (c.m <= 16 && (c.k < 6144 || c.inter > 1536)) return info ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
   return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 4, true>,
-                     MmCfg<false, kRows, kRows, true, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, bytes);
+                     MmCfg<false, kRows, kRows, true, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
@@ -128,7 +128,7 @@ hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *
 
 // dx = [dg du] W: contraction over the 2 inter rows of W
 hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s,
-                         uint64_t *bytes) {
+                         MmInfo *info) {
   MmArgs a = {};
   a.a = (const uint8_t *)dgu;
   a.lda = ldd * 2;
@@ -146,12 +146,12 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true>,
-                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, bytes);
+                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
 // dW = [dg du]^T x: contraction over the tokens
 hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
-                         hipStream_t s, uint64_t *bytes) {
+                         hipStream_t s, MmInfo *info) {
   MmArgs a = {};
   a.a = (const uint8_t *)dgu;
   a.lda = ldd * 2;
@@ -168,7 +168,7 @@ hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.partials = (uint64_t *)c.partials;
   return mm_dispatch<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 2, true>,
-                     MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 4, true>>(a, kMmPartialBytes, s, bytes);
+                     MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
 hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s) {

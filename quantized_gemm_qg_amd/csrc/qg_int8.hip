@@ -116,23 +116,23 @@ bool i8_quantizes_in_kernel(int64_t m, int64_t k) {
 template <bool G, int BM, int BN, int WM, int WN, int ST, bool SPLIT>
 using I8Cfg = MmCfg<true, kRows, kPacked, G, BM, BN, WM, WN, ST, SPLIT>;
 
-// bytes: see mm_dispatch
-static hipError_t i8_tiled(const I8Call &c, hipStream_t s, uint64_t *bytes) {
+// info: see mm_dispatch
+static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
   const MmArgs a = i8_args(c);
   // (the static scratch of qg_gemm_noalloc holds less)
   const uint64_t budget = c.small_scratch ? (8u << 20) - (128u << 10) : kMmPartialBytes;
   if (c.gated)
     return mm_dispatch<I8Cfg<true, 256, 256, 4, 2, 2, false>, I8Cfg<true, 128, 128, 4, 2, 2, true>,
-                       I8Cfg<true, 128, 128, 4, 2, 4, true>, I8Cfg<true, 64, 128, 2, 4, 4, true>>(a, budget, s, bytes);
+                       I8Cfg<true, 128, 128, 4, 2, 4, true>, I8Cfg<true, 64, 128, 2, 4, 4, true>>(a, budget, s, info);
   // (224 columns: 14336 of them in 4096 rows are four whole rounds of the CUs)
   return mm_dispatch<I8Cfg<false, 256, 256, 4, 2, 2, false>, I8Cfg<false, 256, 224, 4, 2, 2, false>,
                      I8Cfg<false, 128, 128, 4, 2, 2, true>, I8Cfg<false, 128, 128, 4, 2, 4, true>,
-                     I8Cfg<false, 64, 128, 2, 4, 4, true>>(a, budget, s, bytes);
+                     I8Cfg<false, 64, 128, 2, 4, 4, true>>(a, budget, s, info);
 }
 
 // Calls of the few-rows kernel: up to 16 rows, and up to 32 where N gives the
 // tiled kernel less than half a round of 128-column tiles and the rows are not
-// too long to be read by every workgroup (23 rows of 4096 x 14336: 16.0 us
+// too long to be read by every workgroup (23 rows of 4096 x 14336: 14.8 us
 // against 18.2 tiled; 32 rows of 8192: 10.8 against 13.1, of 16384: 18.5 against
 // 14.4; 32 rows of 14336 x 4096: 19.0 against 15.5).
 static bool i8_few_rows(const I8Call &c) {
@@ -146,15 +146,17 @@ hipError_t launch_i8(const I8Call &c, hipStream_t s) {
     return c.gated ? launch_rows<true, true, 1, 2, 4, true>(a, s) : launch_rows<true, false, 1, 1, 8, true>(a, s);
   }
   if (!i8_few_rows(c)) return i8_tiled(c, s, nullptr);
-  if (c.m > 16) return launch_rows<true, false, 2, 1, 4, false>(a, s);
+  if (c.m > 16) return launch_rows<true, false, 2, 1, 2, false>(a, s);
   return c.gated ? launch_rows<true, true, 1, 2, 4, false>(a, s) : launch_rows<true, false, 1, 1, 4, false>(a, s);
 }
 
-// Partial tiles of a call on m quantized rows.
-uint64_t i8_partial_bytes(const I8Call &c) {
-  uint64_t b = 0;
-  if (!c.quantize && !i8_few_rows(c)) i8_tiled(c, nullptr, &b);
-  return b;
+MmInfo i8_info(const I8Call &c) {
+  MmInfo info;
+  if (c.quantize || i8_few_rows(c))
+    info.bm = c.m > 16 ? 32 : 16;
+  else
+    i8_tiled(c, nullptr, &info);
+  return info;
 }
 
 }  // namespace qg

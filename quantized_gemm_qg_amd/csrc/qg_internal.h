@@ -199,7 +199,7 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
                      int64_t ldx, void *y, int32_t otype, int64_t ldy, int32_t act, void *ws, uint64_t ws_bytes,
                      uint32_t flags, hipStream_t stream);
 uint64_t i8_ws_bytes(const qg_weight &w, bool gated, int64_t m, uint32_t flags);
-void i8_describe(const qg_weight &w, int64_t m, char *buf, uint64_t buf_bytes);
+void i8_describe(const qg_weight &w, int64_t m, uint32_t flags, char *buf, uint64_t buf_bytes);
 
 // ---------------------------------------------------------------------------
 // kernel launch parameters
@@ -344,6 +344,12 @@ hipError_t launch_silu_mul(const void *gu, bool gu_f32, int64_t rows, int64_t in
                            void *h, int64_t ldh, void *hs, hipStream_t s);
 hipError_t launch_moe_combine(const void *y, bool y_f32, int64_t ldy, const float *wts, int64_t tokens, int topk,
                               int64_t n, const void *bias, void *out, bool out_f32, int64_t ldo, hipStream_t s);
+// Kernel choice of one product: tile rows and columns (0 columns: the few-rows
+// kernel), parts of k, and the bytes of its partial tiles.
+struct MmInfo {
+  uint64_t bytes = 0;
+  int bm = 0, bn = 0, splits = 1;
+};
 // int8 products (qg_int8.hip): quantized rows (x int8 [m][ldx], x_scales [m])
 // times the packed codes; gated: n outputs from 2 n weight columns; quantize:
 // x is bf16 (where i8_quantizes_in_kernel).
@@ -360,10 +366,10 @@ struct I8Call {
   void *y;
   int32_t otype;
   int64_t ldy;
-  uint32_t *counters;  // split-K counters and partial tiles (i8_partial_bytes)
+  uint32_t *counters;  // split-K counters and partial tiles (i8_info)
   void *partials;
 };
-uint64_t i8_partial_bytes(const I8Call &c);
+MmInfo i8_info(const I8Call &c);
 hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q, int64_t ldq, float *qs,
                                 hipStream_t s);
 bool i8_quantizes_in_kernel(int64_t m, int64_t k);
@@ -384,13 +390,13 @@ struct FfnCall {
   uint32_t *counters;  // split-K counters and partial tiles
   void *partials;
 };
-// bytes: NULL, or the launch is only asked for the partial tiles it needs
-hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, uint64_t *bytes = nullptr);
+// info: NULL, or nothing is launched and the choice reported
+hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s);
 hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *dx, int64_t lddx, hipStream_t s,
-                         uint64_t *bytes = nullptr);
+                         MmInfo *info = nullptr);
 hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *dw, int dw_type, int64_t lddw,
-                         hipStream_t s, uint64_t *bytes = nullptr);
+                         hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_ffn_zero(void *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows, hipStream_t s);
 // token log probabilities (qg_logprobs.hip)
 struct LogprobArgs {

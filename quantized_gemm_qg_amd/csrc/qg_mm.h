@@ -611,11 +611,11 @@ static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) 
   return hipGetLastError();
 }
 
-// The cheapest of the compiled shapes: launches it, or (bytes) only says what
-// partial tiles it needs.
+// The cheapest of the compiled shapes: launches it, or (info) only says which it
+// is and what partial tiles it needs.
 template <class... Cs>
-static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, uint64_t *bytes) {
-  MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
+static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, MmInfo *info) {
+  const MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
   int best = 0;
   for (int i = 1; i < (int)sizeof...(Cs); ++i)
     if (plans[i].cost < plans[best].cost) best = i;
@@ -624,8 +624,8 @@ static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, u
   auto one = [&](auto *cfg) {
     using C = std::remove_pointer_t<decltype(cfg)>;
     if (i++ != best) return;
-    if (bytes) {
-      *bytes = mm_partial_bytes<C>(a.m, a.n, plans[best]);
+    if (info) {
+      *info = MmInfo{mm_partial_bytes<C>(a.m, a.n, plans[best]), C::BM, C::BN, plans[best].splits};
       e = hipSuccess;
     } else {
       e = launch_mm<C>(a, plans[best], s);

@@ -37,8 +37,7 @@ struct I8Space {
     return b ? kSplitCounterBytes + b : 0;
   }
 };
-static I8Space i8_space(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
-  I8Space sp;
+static I8Call i8_call(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
   I8Call c = {};
   c.n = (int32_t)(gated ? w.desc.n / 2 : w.desc.n);
   c.k = (int32_t)w.desc.k;
@@ -47,19 +46,29 @@ static I8Space i8_space(const qg_weight &w, bool gated, int64_t m, uint32_t flag
   c.m = m;
   c.small_scratch = (flags & kI8SmallScratch) != 0;
   c.quantize = (flags & QG_GEMM_QUANTIZE_X) && i8_quantizes_in_kernel(m, w.desc.k);
-  sp.partials = align_up(i8_partial_bytes(c), 256);
+  return c;
+}
+static I8Space i8_space(const I8Call &c, uint32_t flags) {
+  I8Space sp;
+  sp.partials = align_up(i8_info(c).bytes, 256);
   if ((flags & QG_GEMM_QUANTIZE_X) && !c.quantize) {
-    sp.codes = align_up((uint64_t)m * w.desc.k, 256);
-    sp.scales = align_up((uint64_t)m * 4, 256);
+    sp.codes = align_up((uint64_t)c.m * c.k, 256);
+    sp.scales = align_up((uint64_t)c.m * 4, 256);
   }
   return sp;
 }
 uint64_t i8_ws_bytes(const qg_weight &w, bool gated, int64_t m, uint32_t flags) {
-  return m <= 0 || m > (1ll << 30) ? 0 : i8_space(w, gated, m, flags).total();
+  return m <= 0 || m > (1ll << 30) ? 0 : i8_space(i8_call(w, gated, m, flags), flags).total();
 }
 
-void i8_describe(const qg_weight &, int64_t, char *buf, uint64_t buf_bytes) {
-  snprintf(buf, buf_bytes, "i8_tiled BM=128 BN=128");
+void i8_describe(const qg_weight &w, int64_t m, uint32_t flags, char *buf, uint64_t buf_bytes) {
+  const I8Call c = i8_call(w, false, std::min<int64_t>(std::max<int64_t>(m, 1), 1 << 30), flags);
+  const MmInfo i = i8_info(c);
+  if (i.bn == 0)
+    snprintf(buf, buf_bytes, "i8_rows M<=%d%s", i.bm, c.quantize ? " quantizing" : "");
+  else
+    snprintf(buf, buf_bytes, i.splits > 1 ? "i8_tiled BM=%d BN=%d splits=%d" : "i8_tiled BM=%d BN=%d", i.bm, i.bn,
+             i.splits);
 }
 
 qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void *x, const void *x_scales, int64_t m,
@@ -77,26 +86,19 @@ qg_status i8_product(const qg_weight *w, const Layout &L, bool gated, const void
     return QG_ERR_ALIGNMENT;
   if (!quantize && !aligned(x_scales, 4)) return QG_ERR_ALIGNMENT;
   if (ldx > kMaxPitchBytes) return QG_ERR_UNSUPPORTED;
-  const I8Space sp = i8_space(*w, gated, m, flags);
+  I8Call c = i8_call(*w, gated, m, flags);
+  const I8Space sp = i8_space(c, flags);
   const qg_status wst = ws_check(sp.total(), ws, ws_bytes);
   if (wst != QG_OK) return wst;
-  I8Call c = {};
   c.codes = (const uint8_t *)w->data;
   c.scales = (const float *)(c.codes + L.scales_offset);
-  c.n = (int32_t)n;
-  c.k = (int32_t)d.k;
-  c.k_blocks = L.k_blocks;
-  c.gated = gated;
   c.act = act;
   c.x = x;
   c.ldx = ldx;
   c.x_scales = (const float *)x_scales;
-  c.m = m;
   c.y = y;
   c.otype = otype;
   c.ldy = ldy;
-  c.quantize = quantize && i8_quantizes_in_kernel(m, d.k);
-  c.small_scratch = (flags & kI8SmallScratch) != 0;
   if (sp.partials) {
     c.counters = (uint32_t *)ws;
     c.partials = (uint8_t *)ws + kSplitCounterBytes;
@@ -154,16 +156,16 @@ static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bo
   c.m = m;
   c.k = k;
   c.inter = inter;
-  uint64_t b = 0;
+  MmInfo i;
   if (!backward || recompute) {
-    launch_ffn_forward(c, nullptr, &b);
-    sp.partials = b;
+    launch_ffn_forward(c, nullptr, &i);
+    sp.partials = i.bytes;
   }
   if (backward) {
-    launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &b);
-    sp.partials = std::max(sp.partials, b);
-    launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &b);
-    sp.partials = std::max(sp.partials, b);
+    launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &i);
+    sp.partials = std::max(sp.partials, i.bytes);
+    launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &i);
+    sp.partials = std::max(sp.partials, i.bytes);
     sp.dgu = align_up((uint64_t)m * dgu_pitch(inter) * 2, 256);
     if (recompute) sp.gu = align_up((uint64_t)m * 2 * inter * 4, 256);
   }

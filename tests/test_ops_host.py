@@ -54,6 +54,19 @@ def test_packed_layout(n, k):
     assert (s[:n] == scales).all() and (s[n:] == 0).all()
 
 
+def test_described_choice():
+    """The description names the kernel that a call takes; a call whose tiles are
+    split over k, and only such a call, needs a workspace."""
+    w = bound(layer(4096, 14336))
+    rows = {m: qg.describe_dispatch(w, m) for m in (1, 16, 17, 23, 128, 4096)}
+    assert rows[1] == rows[16] == "i8_rows M<=16" and rows[17] == rows[23] == "i8_rows M<=32"
+    assert rows[128].startswith("i8_tiled") and rows[4096].startswith("i8_tiled")
+    assert qg.describe_dispatch(w, 1, qg.GEMM_QUANTIZE_X) == "i8_rows M<=16 quantizing"
+    assert qg.describe_dispatch(w, 23, qg.GEMM_QUANTIZE_X) == rows[23]
+    for m in (1, 23, 128, 333, 1000, 4096):
+        assert ("splits" in qg.describe_dispatch(w, m)) == (qg.gemm_workspace_size_ex(w, m, 0) > 0), m
+
+
 def test_int8_product_refusals():
     w = bound(layer())
 
