@@ -51,23 +51,20 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-// act(g) and its derivative
-__device__ __forceinline__ float act_value(float g, int act) {
-  if (act == QG_ACT_SILU) return g / (1.f + __expf(-g));
-  const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-  return 0.5f * g * (1.f + t);
+// act(g) = g p(g) and its derivative, p = 1 / (1 + exp(-z)): z = g for SiLU; for
+// GELU z = 2 sqrt(2 / pi) (g + 0.044715 g^3), as (1 + tanh(y)) / 2 = p(2 y), which
+// costs an exponential and a reciprocal and keeps the relative accuracy where
+// 1 + tanh cancels.  derivative: p + g p (1 - p) z'.
+__device__ __forceinline__ float act_gate(float g, int act) {
+  const float z = act == QG_ACT_SILU ? g : 1.5957691216057308f * g * (1.f + 0.044715f * g * g);
+  return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
+__device__ __forceinline__ float act_value(float g, int act) { return g * act_gate(g, act); }
 __device__ __forceinline__ void act_both(float g, int act, float *v, float *dv) {
-  if (act == QG_ACT_SILU) {
-    const float p = 1.f / (1.f + __expf(-g));
-    *v = g * p;
-    *dv = p * (1.f + g * (1.f - p));
-  } else {
-    const float c = 0.7978845608028654f;
-    const float t = tanhf(c * (g + 0.044715f * g * g * g));
-    *v = 0.5f * g * (1.f + t);
-    *dv = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * c * (1.f + 0.134145f * g * g);
-  }
+  const float p = act_gate(g, act), r = p * (1.f - p);
+  const float dz = act == QG_ACT_SILU ? 1.f : 1.5957691216057308f * (1.f + 0.134145f * g * g);
+  *v = g * p;
+  *dv = r > 0.f ? p + g * r * dz : p;  // (r = 0: dz may have overflowed)
 }
 
 struct MmArgs {

@@ -207,6 +207,33 @@ def test_inf_and_nan_stay_in_their_rows_and_columns():
     within(h[clean], c.h[clean], (c.e_h() * (1 + U16) + U16 * c.h.abs())[clean] + 1e-37)
 
 
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+def test_activation_and_derivative_over_their_whole_range(act):
+    """One token with x = (1, 1, 0 ..): g is the weights' first column and u = 1,
+    so dW's first column is act'(g) and its second act(g).  Tails and
+    overflowing squares included."""
+    vals = [0.0, 1e-30, 1e-3, 0.3, 0.75, 1.0, 2.0, 5.0, 12.0, 30.0, 200.0, 1e5, 1e13, 1e20, 3e38]
+    g = torch.tensor(vals + [-v for v in vals]).to(torch.bfloat16)
+    n, k = g.numel(), 32
+    c = Case(1, k, n, act)
+    c.xd[:] = 0
+    c.xd[0, :2] = 1
+    c.wd[:] = 0
+    c.wd[:n, 0] = g.cuda()
+    c.wd[n:, 1] = 1
+    c.dhd[:] = 1
+    h, gu, ldgu = c.forward(qg.O_F32)
+    v, dv = act64(g.to(D), act)
+    # the gate p in fp32 (its exponent off by 2^-22 of itself, 150 at most where p
+    # is a normal number), then one rounding to bf16
+    tol = U16 + 2.0 ** -14
+    within(h[0], v, tol * v.abs() + 1e-36)
+    _, dw = c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu)
+    # act' = p + g p (1 - p) z': near its zero the two cancel
+    within(dw[:n, 0], dv, tol * dv.abs() + 2.0 ** -20 + 1e-36)
+    within(dw[n:, 1], v, tol * v.abs() + 1e-36)
+
+
 def test_no_tokens():
     c = Case(1, 64, 16, qg.ACT_SILU)
     dw = torch.full((33, 64), 7.0, device="cuda")
