@@ -9,14 +9,14 @@
 // row of nothing else has logp -inf, entropy 0 and gradient 0.
 //
 // One pass over the logits.  A workgroup walks its part of a row in chunks
-// that its threads hold in registers (32 or 128 bytes each), so the
+// that its threads hold in registers (32 to 128 bytes each), so the
 // maximum, the sums under it and the search for alternatives read memory once.
 // Every thread keeps its own running maximum and sums (no barrier between the
 // maximum and the exponentials); they meet once per workgroup.
 //
 // Alternatives: a bound b that at least `top` logits reach turns the search
 // into a collection of the few logits >= b.  For the first chunk b is the
-// top-th largest of 64 group maxima (4 threads each); afterwards it is the
+// top-th largest of 64 group maxima (4 threads or 1); afterwards it is the
 // last alternative of the list so far (later ids lose ties, so > b).  The
 // candidates meet the list in LDS and each finds its place by counting the
 // larger keys; keys (value, id) are distinct, so the order of arrival does not
@@ -40,11 +40,8 @@ namespace qg {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
-constexpr int kCap = 1024;       // candidates of one chunk
+constexpr int kThreads = 256;    // of a workgroup (or 64: one wave, see logprobs_split)
 constexpr int kMaxParts = 64;    // workgroups per row
-static_assert(kCap <= kMaxParts * QG_MAX_ALTERNATIVES, "candidate buffer");
 constexpr int kRecordKeys = kMaxParts * QG_MAX_ALTERNATIVES / kThreads;  // keys of a row's parts, per thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -107,26 +104,29 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float c2) {
   return Sums{m, a.s * fa + b.s * fb, fa * (a.t + da * a.s) + fb * (b.t + db * b.s)};
 }
 
+template <int T, bool SHARED>
 struct Shared {
-  uint64_t cand[kMaxParts * QG_MAX_ALTERNATIVES + QG_MAX_ALTERNATIVES];
+  static constexpr int CAP = 4 * T;  // candidates of one chunk
+  static constexpr int KEYS = SHARED ? kMaxParts * QG_MAX_ALTERNATIVES : CAP;
+  static_assert(CAP <= KEYS, "candidate buffer");
+  uint64_t cand[KEYS + QG_MAX_ALTERNATIVES];
   uint64_t list[QG_MAX_ALTERNATIVES];
   float group[64];
-  Sums sums[kWaves];
-  uint64_t best[kWaves];
-  int above[kWaves];
+  Sums sums[T / 64];
+  uint64_t best[T / 64];
+  int above[T / 64];
   int count;
   int flag;
 };
 
 }  // namespace
 
-template <bool F32, int VEC>
+template <bool F32, int VEC, int T>
 struct Chunk {
   static constexpr int EPV = F32 ? 4 : 8;            // logits per 16 bytes
   static constexpr int EL = F32 ? 4 : 2;
-  static constexpr bool SPREAD = VEC <= 2;
   static constexpr uint32_t NONE = F32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
-  static constexpr int SIZE = kThreads * VEC * EPV;  // logits per chunk
+  static constexpr int SIZE = T * VEC * EPV;  // logits per chunk
   u32x4 d[VEC];
 
   // Chunk at logit `first` of a row of `vocab`.  16 bytes that the row's end
@@ -173,18 +173,17 @@ struct Chunk {
     else
       return __uint_as_float((e & 1) ? d[v][e / 2] & 0xFFFF0000u : d[v][e / 2] << 16);
   }
-  // The thread's place in a chunk at `first` (large chunks: a wave's 16 bytes x
-  // VEC are contiguous, one address with small offsets; small ones: 16 bytes of
-  // every thread, then the next of every thread, so that a short row still
-  // gives every group of threads a maximum), opaque to the compiler: it would
-  // keep everything that follows from it for every v, in a register each.
+  // The thread's place in a chunk at `first` (16 bytes of every thread, then the
+  // next of every thread: a row that fills a part of the chunk still gives every
+  // group of threads a maximum and every wave work), opaque to the compiler: it
+  // would keep everything that follows from it for every v, in a register each.
   __device__ __forceinline__ static int base_of(int first) {
-    int base = first + (SPREAD ? (int)threadIdx.x : ((int)threadIdx.x >> 6) * VEC * 64 + ((int)threadIdx.x & 63)) * EPV;
+    int base = first + (int)threadIdx.x * EPV;
     asm volatile("" : "+v"(base));
     return base;
   }
   // first logit of its v-th 16 bytes: their place, and where they were read
-  __device__ __forceinline__ static int place(int base, int v) { return base + v * (SPREAD ? kThreads : 64) * EPV; }
+  __device__ __forceinline__ static int place(int base, int v) { return base + v * T * EPV; }
   __device__ __forceinline__ static int id(int base, int v, int vocab) {
     return max(min(place(base, v), vocab - EPV), 0);
   }
@@ -192,13 +191,14 @@ struct Chunk {
 
 // Merges sh.cand[0 .. n) and sh.list[0 .. have) into sh.list; returns its
 // length.  All threads call; the candidates are visible before the call.
-__device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) {
+template <int T, bool SHARED>
+__device__ __forceinline__ int merge_list(Shared<T, SHARED> &sh, int n, int have, int top) {
   if (have > 0) {
-    for (int i = threadIdx.x; i < have; i += kThreads) sh.cand[n + i] = sh.list[i];
+    for (int i = threadIdx.x; i < have; i += T) sh.cand[n + i] = sh.list[i];
     __syncthreads();
   }
   const int all = n + have;
-  for (int i = threadIdx.x; i < all; i += kThreads) {
+  for (int i = threadIdx.x; i < all; i += T) {
     const uint64_t k = sh.cand[i];
     int r = 0;
 #pragma unroll 16
@@ -212,20 +212,22 @@ __device__ __forceinline__ int merge_list(Shared &sh, int n, int have, int top) 
 // The chunk's part in the list of alternatives; vmax: the largest logit of
 // each of the thread's 16 bytes, most: of all.  Uniform over the workgroup;
 // returns the list's length.
-template <bool F32, int VEC>
-__device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VEC> &ch, const float (&vmax)[VEC],
+template <bool F32, int VEC, int T, bool SHARED>
+__device__ __forceinline__ int take_alternatives(Shared<T, SHARED> &sh, const Chunk<F32, VEC, T> &ch, const float (&vmax)[VEC],
                                                  const uint8_t *row, int vocab, int first, float most, int have,
                                                  int top) {
-  using C = Chunk<F32, VEC>;
+  using C = Chunk<F32, VEC, T>;
+  constexpr int CAP = Shared<T, SHARED>::CAP;
   const float last = have == top ? key_value(sh.list[top - 1]) : neg_inf();
   if (!__syncthreads_or(most > last)) return have;
   float bound = next_above(last);  // candidates: l >= bound
   for (int attempt = have == top ? 0 : 1; attempt < 2; ++attempt) {
     if (attempt == 1) {
       // what `top` of the 64 group maxima reach
-      float g = fmaxf(most, __shfl_xor(most, 1));
-      g = fmaxf(g, __shfl_xor(g, 2));
-      if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = g;
+      float g = most;
+#pragma unroll
+      for (int off = 1; off < T / 64; off <<= 1) g = fmaxf(g, __shfl_xor(g, off));
+      if (threadIdx.x % (T / 64) == 0) sh.group[threadIdx.x / (T / 64)] = g;
       __syncthreads();
       bound = fmaxf(bound, order_value(max(wave_bound(order_bits(sh.group[threadIdx.x & 63]), top),
                                            order_bits(-3.402823466e38f))));
@@ -235,7 +237,7 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VE
     auto push = [&](float l, int id) {
       if (l >= bound) {
         const int at = atomicAdd(&sh.count, 1);
-        if (at < kCap) sh.cand[at] = alt_key(l, (uint32_t)id);
+        if (at < CAP) sh.cand[at] = alt_key(l, (uint32_t)id);
       }
     };
     const int base = C::base_of(first);
@@ -257,7 +259,7 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VE
       while (hit != 0) {
         const int v = __ffs(hit) - 1;
         hit &= hit - 1;
-        Chunk<F32, 1> one;
+        Chunk<F32, 1, T> one;
         one.load16(0, row, C::place(base, v), vocab);
         const int at0 = C::id(base, v, vocab);
 #pragma unroll
@@ -266,14 +268,14 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VE
     }
     __syncthreads();
     const int n = sh.count;
-    if (n <= kCap) return merge_list(sh, n, have, top);
+    if (n <= CAP) return merge_list(sh, n, have, top);
     __syncthreads();  // (count is cleared for the next attempt)
   }
   // one by one: the largest key below the one before it
   int n = 0;
   for (uint64_t below = ~0ull; n < top; ++n) {
     uint64_t best = 0;
-    for (int i = first + (int)threadIdx.x; i < min(first + C::SIZE, vocab); i += kThreads) {  // (read again: rare)
+    for (int i = first + (int)threadIdx.x; i < min(first + C::SIZE, vocab); i += T) {  // (read again: rare)
       const float l = F32 ? ((const float *)row)[i] : bf16_bits_to_f32(((const uint16_t *)row)[i]);
       const uint64_t k = alt_key(l, (uint32_t)i);
       if (l > last && k < below && k > best) best = k;
@@ -286,7 +288,7 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VE
     if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = best;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+    for (int w = 0; w < T / 64; ++w) best = sh.best[w] > best ? sh.best[w] : best;
     __syncthreads();
     if (best == 0) break;  // uniform
     if (threadIdx.x == 0) sh.cand[n] = best;
@@ -299,27 +301,34 @@ __device__ __forceinline__ int take_alternatives(Shared &sh, const Chunk<F32, VE
 // The record of one part of a row: sums, count and the sorted alternatives.
 __host__ __device__ constexpr int64_t record_bytes(int top) { return 16 + 8 * (int64_t)((top + 1) & ~1); }
 
-// SHARED: gridDim.x workgroups share a row.
-template <bool F32, int VEC, bool SHARED>
-__global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
-  using C = Chunk<F32, VEC>;
-  __shared__ Shared sh;
+// SHARED: gridDim.x workgroups share a row.  T: threads of a workgroup.
+template <bool F32, int VEC, bool SHARED, int T = kThreads>
+__global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 : 5) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
+  using C = Chunk<F32, VEC, T>;
+  __shared__ Shared<T, SHARED> sh;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int vocab = (int)a.vocab, chunks = (vocab + C::SIZE - 1) / C::SIZE;
   const float c2 = a.scale * kLog2e;
   const int parts = SHARED ? gridDim.x : 1, part = SHARED ? blockIdx.x : 0;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
+    const int c_begin = part * chunks / parts, c_end = (part + 1) * chunks / parts;
+    // the first chunk is asked for ahead of the token and its logit, which take
+    // two trips to memory (with 8 units that would cost a wave's registers)
+    constexpr bool AHEAD = VEC <= 4;
+    C ch;
+    if constexpr (AHEAD) {
+      ch.load(lp, c_begin * C::SIZE, C::base_of(c_begin * C::SIZE), vocab);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const int tok = a.tokens ? a.tokens[row] : -1;
     const bool in = tok >= 0 && tok < vocab;
     const float lt = !in ? __builtin_inff()
                      : F32 ? ((const float *)lp)[tok] : bf16_bits_to_f32(((const uint16_t *)lp)[tok]);
     Sums st = {neg_inf(), 0.f, 0.f};
     int above = 0, have = 0;
-    const int c_end = (part + 1) * chunks / parts;
-    for (int c = part * chunks / parts; c < c_end; ++c) {
-      C ch;
-      ch.load(lp, c * C::SIZE, C::base_of(c * C::SIZE), vocab);
+    for (int c = c_begin; c < c_end; ++c) {
+      if (!AHEAD || c > c_begin) ch.load(lp, c * C::SIZE, C::base_of(c * C::SIZE), vocab);
       float most = neg_inf(), vmax[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
@@ -351,7 +360,7 @@ __global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs
       }
       st = Sums{m, s, t};
       above += hits;
-      if (a.top > 0) have = take_alternatives<F32, VEC>(sh, ch, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
+      if (a.top > 0) have = take_alternatives<F32, VEC, T, SHARED>(sh, ch, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
     }
     // join the threads, then the waves
 #pragma unroll
@@ -365,7 +374,7 @@ __global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs
     st = sh.sums[0];
     above = sh.above[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
+    for (int w = 1; w < T / 64; ++w) {
       st = join(st, sh.sums[w], c2);
       above += sh.above[w];
     }
@@ -400,8 +409,10 @@ __global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs
       };
       // every load of the records goes out at once: this thread's keys (one
       // position of a list each), this lane's sums
-      uint64_t all[kRecordKeys];
+      uint64_t all[kRecordKeys], mine = 0;
       if (a.top > 0) {
+        const int deep = (a.top + parts - 1) / parts;
+        mine = lane < parts * deep ? key(lane % parts, lane / parts) : 0;
 #pragma unroll
         for (int j = 0; j < kRecordKeys; ++j) {
           const int i = j * kThreads + (int)threadIdx.x, pos = i / kMaxParts, p = i % kMaxParts;
@@ -420,11 +431,9 @@ __global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs
         above += __shfl_xor(above, off);
       }
       if (a.top > 0) {
-        // the first `deep` keys of each list are at least `top` keys: what `top`
+        // the first `deep` keys of each list (`mine`) are at least `top` keys: what `top`
         // of their values reach bounds the list (ties and all, the buffer holds
         // every key of every part)
-        const int deep = (a.top + parts - 1) / parts;
-        const uint64_t mine = lane < parts * deep ? key(lane % parts, lane / parts) : 0;
         const uint64_t bound = (uint64_t)wave_bound((uint32_t)(mine >> 32), a.top) << 32;
         if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
@@ -466,7 +475,7 @@ __global__ __launch_bounds__(kThreads, SHARED || VEC <= 2 ? 4 : 5) void logprobs
 // bytes: 1021 x 100003 bf16, 408 MB, in 77 us (5.3 TB/s).
 template <bool F32, int VEC>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
-  using C = Chunk<F32, VEC>;
+  using C = Chunk<F32, VEC, kThreads>;
   constexpr int EL = F32 ? 4 : 2;
   const int vocab = (int)a.vocab;
   const float c2 = a.scale * kLog2e;
@@ -523,19 +532,24 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 }
 
 namespace {
-// Chunks of 8 x 16 bytes per thread, or 2 x 16 where those would leave CUs
-// without a workgroup or exceed the row.  Rows are shared by so many workgroups
-// that each CU gets about three (at most one chunk each, kMaxParts).
+// 16-byte units per thread and chunk, workgroups per row and their threads.  A
+// row that one chunk holds takes the smallest that does and one workgroup (19
+// rows of 6201 fp32: 9.3 us, 14.0 with smaller chunks that workgroups share);
+// from 1024 of them on, which fill the CUs, one wave, so that no row waits at
+// barriers (3963 rows of 4197 bf16: 22 us against 34; 1000 rows of 12000 bf16:
+// 24 against 17).  Longer ones take
+// the largest, or the smallest where the large chunks would leave CUs without a
+// workgroup, and are shared by so many workgroups that each CU gets about three
+// (at most one chunk each, kMaxParts).
 struct Split {
-  bool small;
-  int parts;
+  int vec, parts, threads;
 };
 Split logprobs_split(int64_t rows, int64_t vocab, bool f32) {
-  const int64_t big = (f32 ? 4 : 8) * kThreads * 8;
-  const bool small = vocab < big || rows * ((vocab + big - 1) / big) < 256;
-  const int64_t size = small ? big / 4 : big, chunks = (vocab + size - 1) / size;
-  const int64_t want = (768 + rows - 1) / rows;
-  return Split{small, (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, chunks), kMaxParts))};
+  const int64_t unit = (f32 ? 4 : 8) * kThreads;  // logits per unit of a chunk
+  if (vocab <= 8 * unit) return Split{vocab <= 2 * unit ? 2 : vocab <= 4 * unit ? 4 : 8, 1, rows >= 1024 ? 64 : kThreads};
+  const int vec = rows * ((vocab + 8 * unit - 1) / (8 * unit)) < 256 ? 2 : 8;
+  const int64_t chunks = (vocab + vec * unit - 1) / (vec * unit), want = (768 + rows - 1) / rows;
+  return Split{vec, (int)std::min<int64_t>(std::min<int64_t>(want, chunks), kMaxParts), kThreads};
 }
 }  // namespace
 
@@ -554,14 +568,17 @@ hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s) {
   const dim3 grid((unsigned)sp.parts, (unsigned)std::min<int64_t>(a.rows, 65535));
   uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 1024
   uint8_t *records = (uint8_t *)ws + kSplitCounterBytes;
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, s, a, counters, records); };
-  // (small chunks of a row that is not shared: a vocabulary of one chunk)
-  if (a.f32)
-    sp.parts > 1 ? (sp.small ? go(logprobs_kernel<true, 2, true>) : go(logprobs_kernel<true, 8, true>))
-                 : (sp.small ? go(logprobs_kernel<true, 2, false>) : go(logprobs_kernel<true, 8, false>));
-  else
-    sp.parts > 1 ? (sp.small ? go(logprobs_kernel<false, 2, true>) : go(logprobs_kernel<false, 8, true>))
-                 : (sp.small ? go(logprobs_kernel<false, 2, false>) : go(logprobs_kernel<false, 8, false>));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(sp.threads), 0, s, a, counters, records); };
+  auto typed = [&](auto f32) {
+    constexpr bool F = decltype(f32)::value;
+    if (sp.parts > 1)
+      sp.vec == 2 ? go(logprobs_kernel<F, 2, true>) : go(logprobs_kernel<F, 8, true>);
+    else if (sp.threads == 64)
+      go(logprobs_kernel<F, 8, false, 64>);
+    else
+      sp.vec == 2 ? go(logprobs_kernel<F, 2, false>) : sp.vec == 4 ? go(logprobs_kernel<F, 4, false>) : go(logprobs_kernel<F, 8, false>);
+  };
+  a.f32 ? typed(std::true_type{}) : typed(std::false_type{});
   return hipGetLastError();
 }
 
