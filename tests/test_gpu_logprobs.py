@@ -132,6 +132,16 @@ def test_forward(rows, vocab, kind, dtype):
             assert ((got - want)[fin].abs() <= tol[:, None].expand_as(got)[fin]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,kind", [(1024, 300, "plain"), (1024, 300, "equal"), (1100, 4099, "plain"), (1100, 4099, "masked"),
+                                             (1100, 4099, "ties"), (1100, 4099, "sorted"), (1025, 2500, "lowest"),
+                                             (1024, 9001, "strided"), (20, 6201, "ties"), (20, 12001, "sorted"), (800, 17000, "plain")])
+def test_forward_of_rows_that_a_chunk_holds(rows, vocab, kind, dtype):
+    """Many short rows (a wave each), few of them (a workgroup each), and rows of
+    a chunk and a piece of the next."""
+    test_forward(rows, vocab, kind, dtype)
+
+
 def test_repeated_calls_give_the_same_bits():
     l, tok = make("plain", 3, 131072, torch.bfloat16, 1)
     d = place(l, torch.bfloat16, 0, 0)
