@@ -100,9 +100,11 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info) {
   // blocks here).
   if (c.m <= 16 && (c.k < 6144 || c.inter > 1536)) return info ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
   return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
+                     MmCfg<false, kRows, kRows, true, 192, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 4, true>,
-                     MmCfg<false, kRows, kRows, true, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, info);
+                     MmCfg<false, kRows, kRows, true, 64, 128, 2, 4, 4, true>,
+                     MmCfg<false, kRows, kRows, true, 32, 128, 1, 4, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
@@ -146,7 +148,8 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true>,
-                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true>>(a, kMmPartialBytes, s, info);
+                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true>,
+                     MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
 // dW = [dg du]^T x: contraction over the tokens

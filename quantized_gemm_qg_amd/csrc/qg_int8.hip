@@ -122,12 +122,14 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
   // (the static scratch of qg_gemm_noalloc holds less)
   const uint64_t budget = c.small_scratch ? (8u << 20) - (128u << 10) : kMmPartialBytes;
   if (c.gated)
-    return mm_dispatch<I8Cfg<true, 256, 256, 4, 2, 2, false>, I8Cfg<true, 128, 128, 4, 2, 2, true>,
-                       I8Cfg<true, 128, 128, 4, 2, 4, true>, I8Cfg<true, 64, 128, 2, 4, 4, true>>(a, budget, s, info);
+    return mm_dispatch<I8Cfg<true, 256, 256, 4, 2, 2, false>, I8Cfg<true, 192, 256, 4, 2, 2, false>,
+                       I8Cfg<true, 128, 128, 4, 2, 2, true>, I8Cfg<true, 128, 128, 4, 2, 4, true>,
+                       I8Cfg<true, 64, 128, 2, 4, 4, true>, I8Cfg<true, 32, 128, 1, 4, 4, true>>(a, budget, s, info);
   // (224 columns: 14336 of them in 4096 rows are four whole rounds of the CUs)
   return mm_dispatch<I8Cfg<false, 256, 256, 4, 2, 2, false>, I8Cfg<false, 256, 224, 4, 2, 2, false>,
-                     I8Cfg<false, 128, 128, 4, 2, 2, true>, I8Cfg<false, 128, 128, 4, 2, 4, true>,
-                     I8Cfg<false, 64, 128, 2, 4, 4, true>>(a, budget, s, info);
+                     I8Cfg<false, 192, 256, 4, 2, 2, false>, I8Cfg<false, 128, 128, 4, 2, 2, true>,
+                     I8Cfg<false, 128, 128, 4, 2, 4, true>, I8Cfg<false, 64, 128, 2, 4, 4, true>,
+                     I8Cfg<false, 32, 128, 1, 8, 4, true>>(a, budget, s, info);
 }
 
 // Calls of the few-rows kernel: up to 16 rows, and up to 32 where N gives the

@@ -34,6 +34,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "qg_device.h"
@@ -553,34 +554,44 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
 }
 
 // What a tile shape and a split of k would cost, in clocks of the busiest CU:
-// its workgroups' stages (matrix time, which workgroups of a CU share, or one
-// stage's latency where they are few), their start and end, and the sum over
-// the parts.  Latency and the fixed part are measured (one workgroup per CU,
-// operands in L2).
+// its workgroups' stages (matrix or LDS time, which workgroups of a CU share, or
+// one stage's latency where they are few) beside the operands' way from memory,
+// each workgroup's start and end, and the sum over the parts.  The latencies,
+// the fixed parts and the factor 1.7 over the matrix instructions' own time are
+// measured.  What the shapes are for: 256 x 256 where its tiles fill the CUs; 192
+// rows where a batch is little more than a whole number of them (gated int8,
+// 322 rows of 14004 x 2528: 39.5 us, 50 in 128 x 128, 42 in 256 x 256); 128 x 128,
+// with two stages two workgroups share a CU, with four one has more in flight;
+// 64 and 32 rows for small batches (bf16, 128 rows of 2816 x 1024: 10.0 and 8.7
+// us).  Workgroups are counted per XCD, where all parts of a tile run (28
+// tiles in 9 parts, 36 on some XCDs' 32 CUs, took 36 us, in 8 parts 29).
 struct MmPlan {
   int splits = 1, per = 0;
-  int64_t cost = 0;
+  double cost = 0;
 };
 template <class C>
 static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
   const int64_t m_tiles = (m + C::BM - 1) / C::BM, n_tiles = (n + OUT_BN - 1) / OUT_BN, tiles = m_tiles * n_tiles;
   const int64_t steps = (kd + C::KE - 1) / C::KE;
-  // (measured over the instruction's own time: 1.7 for 256 x 256 tiles, 2.1 for
-  // the smaller ones, whose operands take more of the way)
-  constexpr int64_t matrix = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * (C::BM == 256 ? 17 : 21) / 10;
-  constexpr int64_t latency = C::BM == 64 ? 700 : C::ST == 2 ? 1170 : 900;
+  constexpr int64_t mfma = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * 17 / 10;
+  constexpr int64_t lds = (C::WAVES * (C::MB + C::NB) * 16 * C::KB + C::STAGE) / 128 * 21 / 20;
+  constexpr int64_t matrix = mfma > lds ? mfma : lds;
+  constexpr int64_t latency = C::BM <= 64 ? 700 : C::ST == 2 ? 1170 : 900;
   constexpr int64_t resident = 160 * 1024 / C::LDS;
   constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;
+  const double memory = (double)(m + (C::GATED ? 2 * n : n)) * kd * C::EL / 2100;
   MmPlan best;
   const int64_t most = C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(budget / (uint64_t)(partial * tiles)) : 1;
   for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), 32); ++want) {
     const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
     if (splits != want) continue;  // the same as a smaller number of parts
-    const int64_t wgs = (tiles * splits + 255) / 256, rounds = (wgs + resident - 1) / resident;
-    int64_t cost = per * std::max(wgs * matrix, rounds * latency) + 4000 * rounds;
+    const int64_t wgs = ((tiles + kXcds - 1) / kXcds * splits + 31) / 32, rounds = (wgs + resident - 1) / resident;
+    if (splits > 1 && rounds > 1) break;  // (more parts than places: slower than fewer)
+    const double stages = (double)per * std::max(wgs * matrix, rounds * latency);
+    double cost = std::sqrt(stages * stages + memory * memory) + 4000. * wgs;
     if (splits > 1) cost += 6000 + splits * partial / 24;
-    if (best.cost == 0 || cost < best.cost) best = MmPlan{(int)splits, (int)per, cost};
+    if (best.per == 0 || cost < best.cost) best = MmPlan{(int)splits, (int)per, cost};
   }
   return best;
 }

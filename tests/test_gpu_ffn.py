@@ -165,6 +165,17 @@ def test_backward(m, k, inter, act):
     assert torch.equal(dw16, dw.to(torch.bfloat16).to(D))
 
 
+# every tile shape of the three products, whole and in parts of k
+TILES = [(36, 32, 8848), (85, 32, 9950), (394, 32, 13727), (399, 32, 4700), (429, 608, 4836), (77, 4160, 1916), (620, 2496, 803),
+         (1345, 2016, 71), (1345, 2976, 100), (403, 8320, 64), (173, 5632, 65)]
+
+
+@pytest.mark.parametrize("m,k,inter", TILES)
+def test_every_tile_shape(m, k, inter):
+    test_forward(m, k, inter, qg.ACT_SILU)
+    test_backward(m, k, inter, qg.ACT_GELU_TANH)
+
+
 def test_backward_from_pre_activations_saved_in_bf16():
     c = Case(130, 256, 96, qg.ACT_SILU, seed=5)
     _, gu, ldgu = c.forward(qg.O_BF16)

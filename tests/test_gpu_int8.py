@@ -193,6 +193,18 @@ def test_gated_matches_64_bits(m, inter, k, act):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("m,n,k", [(36, 97, 2560), (34, 75, 32), (65, 13423, 32), (1653, 148, 3712), (66, 16413, 32), (691, 1788, 4192),
+                                   (999, 4854, 2016), (274, 13932, 32), (583, 18164, 32), (811, 15081, 32)])
+def test_every_tile_shape(m, n, k):
+    test_product_matches_64_bits(m, n, k, qg.O_F32)
+
+
+@pytest.mark.parametrize("m,inter,k", [(19, 64, 2560), (36, 8848, 32), (1468, 66, 2656), (85, 9950, 32), (827, 2575, 1056),
+                                       (1300, 838, 1152), (350, 7001, 96), (394, 13727, 32)])
+def test_every_gated_tile_shape(m, inter, k):
+    test_gated_matches_64_bits(m, inter, k, qg.ACT_GELU_TANH)
+
+
 def test_another_stream_and_noalloc():
     lay = Int8Layer(320, 2048, 9)
     st = torch.cuda.Stream()
