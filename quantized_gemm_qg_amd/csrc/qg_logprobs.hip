@@ -23,13 +23,14 @@
 // matter.  Where ties or an order against the walk give more candidates than
 // the buffer holds, the chunk's alternatives are found one by one.
 //
-// Many rows are bound by their bytes: 2048 x 131072 bf16 (537 MB) in 101 us
-// without alternatives and 125 us with 20 of them.  One row of 131072 fp32 takes
-// 12 us: a chain of latencies (the loads, the bound and list of each part, the
-// arrival, the join of the lists), not bytes.
-//
 // With few rows, several workgroups share a row (arrival counters, the last
 // one joins the parts in their order, so the sums do not depend on timing).
+//
+// Many rows are bound by their bytes: 2048 x 131072 bf16 (537 MB) in 101 us
+// without alternatives and 125 us with 20 of them.  One row of 131072 fp32 takes
+// 11.5 us, a chain of latencies: 2.0 until its logits are there, 3.4 for the
+// alternatives and sums of a part, 0.7 to publish them, 1.3 for the last
+// workgroup to read the parts, 2.7 to join them.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"
@@ -42,6 +43,7 @@ namespace {
 
 constexpr int kThreads = 256;    // of a workgroup (or 64: one wave, see logprobs_split)
 constexpr int kMaxParts = 64;    // workgroups per row
+constexpr int kCounterPitch = 16;  // rows' arrival counters, 64 bytes apart: in one line they wait for each other
 constexpr int kRecordKeys = kMaxParts * QG_MAX_ALTERNATIVES / kThreads;  // keys of a row's parts, per thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -94,28 +96,51 @@ __device__ __forceinline__ uint32_t wave_bound(uint32_t u, int top) {
 struct Sums {
   float m, s, t;
 };
-// b after a: the sums move under the larger maximum.  t is in units of the
+// The sums under another maximum m (-inf: there is none).  t is in units of the
 // exponent (base 2).
-__device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float c2) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == neg_inf()) return Sums{m, a.s + b.s, a.t + b.t};
-  const float da = fmaxf((a.m - m) * c2, -200.f), db = fmaxf((b.m - m) * c2, -200.f);
-  const float fa = exp2f(da), fb = exp2f(db);
-  return Sums{m, a.s * fa + b.s * fb, fa * (a.t + da * a.s) + fb * (b.t + db * b.s)};
+__device__ __forceinline__ Sums under(const Sums &a, float m, float c2) {
+  const float d = fmaxf((a.m - (m == neg_inf() ? 0.f : m)) * c2, -200.f), f = __builtin_amdgcn_exp2f(d);
+  return Sums{m, a.s * f, f * (a.t + d * a.s)};
+}
+// Reductions over a wave, the result in every lane: pairs, quads, 8 and 16
+// lanes by data-parallel moves, then across the rows of 16.
+template <int CTRL>
+__device__ __forceinline__ int lanes_moved(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, 0xF, 0xF, true);
+}
+template <class V, class Op>
+__device__ __forceinline__ V wave_reduce(V x, Op op) {
+  auto moved = [](V v, auto ctrl) { return __builtin_bit_cast(V, lanes_moved<decltype(ctrl)::value>(__builtin_bit_cast(int, v))); };
+  x = op(x, moved(x, std::integral_constant<int, 0xB1>{}));   // quad_perm 1 0 3 2
+  x = op(x, moved(x, std::integral_constant<int, 0x4E>{}));   // quad_perm 2 3 0 1
+  x = op(x, moved(x, std::integral_constant<int, 0x141>{}));  // row_half_mirror
+  x = op(x, moved(x, std::integral_constant<int, 0x140>{}));  // row_mirror
+  x = op(x, (V)__shfl_xor(x, 16));
+  return op(x, (V)__shfl_xor(x, 32));
+}
+__device__ __forceinline__ Sums wave_sums(const Sums &a, float c2) {
+  const auto add = [](float x, float y) { return x + y; };
+  const float m = wave_reduce(a.m, [](float x, float y) { return fmaxf(x, y); });
+  const Sums u = under(a, m, c2);
+  return Sums{m, wave_reduce(u.s, add), wave_reduce(u.t, add)};
 }
 
-template <int T, bool SHARED>
+template <int T, int VEC, bool SHARED>
 struct Shared {
-  static constexpr int CAP = 4 * T;  // candidates of one chunk
+  static constexpr int CAP = 4 * T;       // candidates of one chunk
+  static constexpr int UNITS = 256;       // 16-byte units that hold them
+  static constexpr bool DATA = VEC <= 2;  // units by value (else read again)
   static constexpr int KEYS = SHARED ? kMaxParts * QG_MAX_ALTERNATIVES : CAP;
   static_assert(CAP <= KEYS, "candidate buffer");
-  uint64_t cand[KEYS + QG_MAX_ALTERNATIVES];
+  uint64_t cand[KEYS + QG_MAX_ALTERNATIVES + 8];
   uint64_t list[QG_MAX_ALTERNATIVES];
+  u32x4 unit[DATA ? UNITS : 1];
+  int place[UNITS];
   float group[64];
   Sums sums[T / 64];
   uint64_t best[T / 64];
   int above[T / 64];
-  int count;
+  int count, units;
   int flag;
 };
 
@@ -191,18 +216,19 @@ struct Chunk {
 
 // Merges sh.cand[0 .. n) and sh.list[0 .. have) into sh.list; returns its
 // length.  All threads call; the candidates are visible before the call.
-template <int T, bool SHARED>
-__device__ __forceinline__ int merge_list(Shared<T, SHARED> &sh, int n, int have, int top) {
-  if (have > 0) {
-    for (int i = threadIdx.x; i < have; i += T) sh.cand[n + i] = sh.list[i];
-    __syncthreads();
-  }
+template <int T, int VEC, bool SHARED>
+__device__ __forceinline__ int merge_list(Shared<T, VEC, SHARED> &sh, int n, int have, int top) {
   const int all = n + have;
+  // (zeros, below every key, to a multiple of 8)
+  for (int i = threadIdx.x; i < have + 8; i += T) sh.cand[n + i] = i < have ? sh.list[i] : 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < all; i += T) {
     const uint64_t k = sh.cand[i];
     int r = 0;
-#pragma unroll 16
-    for (int j = 0; j < all; ++j) r += sh.cand[j] > k;
+    for (int j0 = 0; j0 < all; j0 += 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r += sh.cand[j0 + j] > k;
+    }
     if (r < top) sh.list[r] = k;
   }
   __syncthreads();
@@ -213,63 +239,68 @@ __device__ __forceinline__ int merge_list(Shared<T, SHARED> &sh, int n, int have
 // each of the thread's 16 bytes, most: of all.  Uniform over the workgroup;
 // returns the list's length.
 template <bool F32, int VEC, int T, bool SHARED>
-__device__ __forceinline__ int take_alternatives(Shared<T, SHARED> &sh, const Chunk<F32, VEC, T> &ch, const float (&vmax)[VEC],
+__device__ __forceinline__ int take_alternatives(Shared<T, VEC, SHARED> &sh, const Chunk<F32, VEC, T> &ch, const float (&vmax)[VEC],
                                                  const uint8_t *row, int vocab, int first, float most, int have,
                                                  int top) {
   using C = Chunk<F32, VEC, T>;
-  constexpr int CAP = Shared<T, SHARED>::CAP;
+  using S = Shared<T, VEC, SHARED>;
   const float last = have == top ? key_value(sh.list[top - 1]) : neg_inf();
   if (!__syncthreads_or(most > last)) return have;
   float bound = next_above(last);  // candidates: l >= bound
   for (int attempt = have == top ? 0 : 1; attempt < 2; ++attempt) {
     if (attempt == 1) {
       // what `top` of the 64 group maxima reach
+      // (of the first wave's threads where they hold everything)
       float g = most;
-#pragma unroll
-      for (int off = 1; off < T / 64; off <<= 1) g = fmaxf(g, __shfl_xor(g, off));
-      if (threadIdx.x % (T / 64) == 0) sh.group[threadIdx.x / (T / 64)] = g;
+      const int per = vocab - first <= 64 * C::EPV ? 1 : T / 64;
+      for (int off = 1; off < per; off <<= 1) g = fmaxf(g, __shfl_xor(g, off));
+      if (threadIdx.x % per == 0 && threadIdx.x < 64 * per) sh.group[threadIdx.x / per] = g;
       __syncthreads();
       bound = fmaxf(bound, order_value(max(wave_bound(order_bits(sh.group[threadIdx.x & 63]), top),
                                            order_bits(-3.402823466e38f))));
     }
-    if (threadIdx.x == 0) sh.count = 0;
+    if (threadIdx.x == 0) sh.count = sh.units = 0;
     __syncthreads();
-    auto push = [&](float l, int id) {
-      if (l >= bound) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < CAP) sh.cand[at] = alt_key(l, (uint32_t)id);
-      }
-    };
+    // the few 16-byte units that hold candidates, then their logits, one per
+    // thread: short code (unrolled over a thread's logits, fetching the
+    // instructions took longer than anything else)
     const int base = C::base_of(first);
-    if constexpr (VEC <= 2) {
+    uint32_t hit = 0;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v)
-        if (vmax[v] >= bound) {
-          const int at0 = C::id(base, v, vocab);
+    for (int v = 0; v < VEC; ++v) hit |= vmax[v] >= bound ? 1u << v : 0u;
+    if (hit != 0) {
+      int at = atomicAdd(&sh.units, __popc(hit));
+      if constexpr (S::DATA) {
 #pragma unroll
-          for (int e = 0; e < C::EPV; ++e) push(ch.at(v, e), at0 + e);
+        for (int v = 0; v < VEC; ++v) {
+          if ((hit >> v & 1u) == 0 || at >= S::UNITS) continue;
+          sh.place[at] = C::place(base, v);
+          sh.unit[at++] = ch.d[v];
         }
-    } else {
-      // the few 16 bytes that hold candidates are read again (they are in the
-      // caches): unrolled over the registers, this search would cost the kernel
-      // half its occupancy
-      uint32_t hit = 0;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) hit |= vmax[v] >= bound ? 1u << v : 0u;
-      while (hit != 0) {
-        const int v = __ffs(hit) - 1;
-        hit &= hit - 1;
-        Chunk<F32, 1, T> one;
-        one.load16(0, row, C::place(base, v), vocab);
-        const int at0 = C::id(base, v, vocab);
-#pragma unroll
-        for (int e = 0; e < C::EPV; ++e) push(one.at(0, e), at0 + e);
+      } else {
+        for (; hit != 0 && at < S::UNITS; hit &= hit - 1) sh.place[at++] = C::place(base, __ffs(hit) - 1);
       }
     }
     __syncthreads();
-    const int n = sh.count;
-    if (n <= CAP) return merge_list(sh, n, have, top);
-    __syncthreads();  // (count is cleared for the next attempt)
+    const int units = sh.units;
+    if (units <= S::UNITS) {
+      for (int i = threadIdx.x; i < units * C::EPV; i += T) {
+        const int u = i / C::EPV, e = i % C::EPV, from = sh.place[u], id = max(min(from, vocab - C::EPV), 0) + e;
+        float l = neg_inf();
+        if constexpr (S::DATA)
+          l = F32 ? ((const float *)&sh.unit[u])[e] : bf16_bits_to_f32(((const uint16_t *)&sh.unit[u])[e]);
+        else if (id >= from && id < vocab)
+          l = F32 ? ((const float *)row)[id] : bf16_bits_to_f32(((const uint16_t *)row)[id]);
+        if (l >= bound) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < S::CAP) sh.cand[at] = alt_key(l, (uint32_t)id);
+        }
+      }
+      __syncthreads();
+      const int n = sh.count;
+      if (n <= S::CAP) return merge_list(sh, n, have, top);
+    }
+    __syncthreads();  // (the counts are cleared for the next attempt)
   }
   // one by one: the largest key below the one before it
   int n = 0;
@@ -303,22 +334,26 @@ __host__ __device__ constexpr int64_t record_bytes(int top) { return 16 + 8 * (i
 
 // SHARED: gridDim.x workgroups share a row.  T: threads of a workgroup.
 template <bool F32, int VEC, bool SHARED, int T = kThreads>
-__global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 : 5) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
+__global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs a, uint32_t *counters, uint8_t *records) {
   using C = Chunk<F32, VEC, T>;
-  __shared__ Shared<T, SHARED> sh;
+  __shared__ Shared<T, VEC, SHARED> sh;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int vocab = (int)a.vocab, chunks = (vocab + C::SIZE - 1) / C::SIZE;
+  const int vocab = (int)a.vocab;
   const float c2 = a.scale * kLog2e;
   const int parts = SHARED ? gridDim.x : 1, part = SHARED ? blockIdx.x : 0;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
-    const int c_begin = part * chunks / parts, c_end = (part + 1) * chunks / parts;
+    // this workgroup's logits, in equal parts (a short last one would have no
+    // good bound for its alternatives, and the others would wait for it)
+    const int64_t all_units = (vocab + C::EPV - 1) / C::EPV;
+    const int begin = SHARED ? (int)(part * all_units / parts) * C::EPV : 0;
+    const int end = SHARED ? min((int)((part + 1) * all_units / parts) * C::EPV, vocab) : vocab;
     // the first chunk is asked for ahead of the token and its logit, which take
     // two trips to memory (with 8 units that would cost a wave's registers)
     constexpr bool AHEAD = VEC <= 4;
     C ch;
     if constexpr (AHEAD) {
-      ch.load(lp, c_begin * C::SIZE, C::base_of(c_begin * C::SIZE), vocab);
+      ch.load(lp, begin, C::base_of(begin), end);
       __builtin_amdgcn_sched_barrier(0);
     }
     const int tok = a.tokens ? a.tokens[row] : -1;
@@ -327,8 +362,8 @@ __global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 
                      : F32 ? ((const float *)lp)[tok] : bf16_bits_to_f32(((const uint16_t *)lp)[tok]);
     Sums st = {neg_inf(), 0.f, 0.f};
     int above = 0, have = 0;
-    for (int c = c_begin; c < c_end; ++c) {
-      if (!AHEAD || c > c_begin) ch.load(lp, c * C::SIZE, C::base_of(c * C::SIZE), vocab);
+    for (int first = begin; first < end; first += C::SIZE) {
+      if (!AHEAD || first > begin) ch.load(lp, first, C::base_of(first), end);
       float most = neg_inf(), vmax[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
@@ -360,23 +395,28 @@ __global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 
       }
       st = Sums{m, s, t};
       above += hits;
-      if (a.top > 0) have = take_alternatives<F32, VEC, T, SHARED>(sh, ch, vmax, lp, vocab, c * C::SIZE, most, have, a.top);
+      if (a.top > 0) have = take_alternatives<F32, VEC, T, SHARED>(sh, ch, vmax, lp, end, first, most, have, a.top);
     }
     // join the threads, then the waves
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-      st = join(st, Sums{__shfl_xor(st.m, off), __shfl_xor(st.s, off), __shfl_xor(st.t, off)}, c2);
+    st = wave_sums(st, c2);
     if (lane == 0) {
       sh.sums[wave] = st;
       sh.above[wave] = above;
     }
     __syncthreads();
-    st = sh.sums[0];
-    above = sh.above[0];
+    {
+      float m = neg_inf();
 #pragma unroll
-    for (int w = 1; w < T / 64; ++w) {
-      st = join(st, sh.sums[w], c2);
-      above += sh.above[w];
+      for (int w = 0; w < T / 64; ++w) m = fmaxf(m, sh.sums[w].m);
+      st = Sums{m, 0.f, 0.f};
+      above = 0;
+#pragma unroll
+      for (int w = 0; w < T / 64; ++w) {
+        const Sums u = under(sh.sums[w], m, c2);
+        st.s += u.s;
+        st.t += u.t;
+        above += sh.above[w];
+      }
     }
     if constexpr (SHARED) {
       // publish this part, and let the last workgroup of the row join them:
@@ -394,7 +434,7 @@ __global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
       if (threadIdx.x == 0)
-        sh.flag = __hip_atomic_fetch_add(counters + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+        sh.flag = __hip_atomic_fetch_add(counters + row * kCounterPitch, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                   (uint32_t)(parts - 1);
       __syncthreads();
       if (!sh.flag) {  // uniform over the workgroup
@@ -425,11 +465,8 @@ __global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 
         st = Sums{word(lane, 0), word(lane, 1), word(lane, 2)};
         above = __float_as_int(word(lane, 3));
       }
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        st = join(st, Sums{__shfl_xor(st.m, off), __shfl_xor(st.s, off), __shfl_xor(st.t, off)}, c2);
-        above += __shfl_xor(above, off);
-      }
+      st = wave_sums(st, c2);
+      above = wave_reduce(above, [](int x, int y) { return x + y; });
       if (a.top > 0) {
         // the first `deep` keys of each list (`mine`) are at least `top` keys: what `top`
         // of their values reach bounds the list (ties and all, the buffer holds
@@ -437,13 +474,19 @@ __global__ __launch_bounds__(T, SHARED && VEC <= 2 ? 3 : SHARED || VEC <= 2 ? 4 
         const uint64_t bound = (uint64_t)wave_bound((uint32_t)(mine >> 32), a.top) << 32;
         if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
+        int n = 0;
 #pragma unroll
-        for (int j = 0; j < kRecordKeys; ++j)
-          if (all[j] != 0 && all[j] >= bound) sh.cand[atomicAdd(&sh.count, 1)] = all[j];
+        for (int j = 0; j < kRecordKeys; ++j) n += all[j] != 0 && all[j] >= bound;
+        if (n > 0) {
+          int at = atomicAdd(&sh.count, n);
+#pragma unroll
+          for (int j = 0; j < kRecordKeys; ++j)
+            if (all[j] != 0 && all[j] >= bound) sh.cand[at++] = all[j];
+        }
         __syncthreads();
         have = merge_list(sh, sh.count, 0, a.top);
       }
-      if (threadIdx.x == 0) __hip_atomic_store(counters + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (threadIdx.x == 0) __hip_atomic_store(counters + row * kCounterPitch, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     const bool empty = st.m == neg_inf() && st.s == 0.f;
     const float most = st.m == neg_inf() ? 0.f : st.m;
@@ -532,15 +575,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
 }
 
 namespace {
+static_assert(768 * kCounterPitch * 4 <= kSplitCounterBytes, "counters of shared rows");
 // 16-byte units per thread and chunk, workgroups per row and their threads.  A
 // row that one chunk holds takes the smallest that does and one workgroup (19
 // rows of 6201 fp32: 9.3 us, 14.0 with smaller chunks that workgroups share);
 // from 1024 of them on, which fill the CUs, one wave, so that no row waits at
 // barriers (3963 rows of 4197 bf16: 22 us against 34; 1000 rows of 12000 bf16:
-// 24 against 17).  Longer ones take
-// the largest, or the smallest where the large chunks would leave CUs without a
-// workgroup, and are shared by so many workgroups that each CU gets about three
-// (at most one chunk each, kMaxParts).
+// 24 against 17).  Longer ones take the largest, or the smallest where the large
+// chunks would leave CUs without a workgroup, and are shared by so many
+// workgroups that each CU gets about three (at most one chunk each, kMaxParts).
 struct Split {
   int vec, parts, threads;
 };
@@ -566,7 +609,7 @@ uint64_t logprobs_ws_bytes(int64_t rows, int64_t vocab, int top) {
 hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s) {
   const Split sp = logprobs_split(a.rows, a.vocab, a.f32);
   const dim3 grid((unsigned)sp.parts, (unsigned)std::min<int64_t>(a.rows, 65535));
-  uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 1024
+  uint32_t *counters = (uint32_t *)ws;  // one per row: shared rows are fewer than 768
   uint8_t *records = (uint8_t *)ws + kSplitCounterBytes;
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(sp.threads), 0, s, a, counters, records); };
   auto typed = [&](auto f32) {
