@@ -94,11 +94,13 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info) {
   a.counters = c.counters;
   a.partials = (uint64_t *)c.partials;
   // Few rows: a workgroup per 16 columns with all of K, unless long rows meet few
-  // columns, where the tiled kernel's parts of k occupy more CUs (16384 x 128: 19
-  // us against 34; 8192 x 600: 15 against 18; 8192 x 2400: 22.4 against 21.2).
-  // From 17 rows on tiled (24 rows of 14336 x 4096: 51.9 us, 71.4 with two row
-  // blocks here).
-  if (c.m <= 16 && (c.k < 6144 || c.inter > 1536)) return info ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
+  // columns, where the tiled kernel's parts of k occupy more CUs (8 rows: 400 x
+  // 2560 8.6 us against 10.8, 1700 x 8192 17.1 against 23.6, 2400 x 8192 20.6
+  // against 26.1; 4000 x 8192 34.7 against 27.5, 1500 x 2048 8.3 against 7.8; 2
+  // rows of 3000 x 8192 24.3 against 22.7).  From 17 rows on tiled (24 rows of
+  // 14336 x 4096: 51.9 us, 71.4 with two row blocks here).
+  if (c.m <= 16 && (c.k < 2560 || c.inter > (c.m <= 4 ? 2048 : 3000)))
+    return info ? hipSuccess : launch_rows<false, true, 1, 2, 4, false>(a, s);
   return mm_dispatch<MmCfg<false, kRows, kRows, true, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 192, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kRows, true, 128, 128, 4, 2, 2, true>,

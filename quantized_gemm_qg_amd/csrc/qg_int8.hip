@@ -133,12 +133,17 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
 }
 
 // Calls of the few-rows kernel: up to 16 rows, and up to 32 where N gives the
-// tiled kernel less than half a round of 128-column tiles and the rows are not
-// too long to be read by every workgroup (23 rows of 4096 x 14336: 14.8 us
-// against 18.2 tiled; 32 rows of 8192: 10.8 against 13.1, of 16384: 18.5 against
-// 14.4; 32 rows of 14336 x 4096: 19.0 against 15.5).
+// tiled kernel less than half a round of 128-column tiles, as long as the rows
+// are not too long to be read by every workgroup (32 rows of 8192 columns: k =
+// 8192 10.8 us against 13.1 tiled, 16384 18.5 against 14.4; with few columns the
+// workgroups are too few sooner: 24 rows of 1000 x 14336 15.4 against 12.3, 16
+// rows 13.1 against 12.1, 8 rows 10.4 against 11.9).  32 rows of 14336 x 4096:
+// 19.0 against 15.5.  Gated, from 2 rows on, not with many columns (4 rows: 8192
+// x 4096 15.5 us against 18.0, 12288 x 4096 22.0 against 20.9, 14336 x 4096 26.0
+// against 23.6).
 static bool i8_few_rows(const I8Call &c) {
-  return c.m <= 16 || (c.m <= 32 && !c.gated && c.n < 8192 && c.m * c.k <= 24 * 14336);
+  if (c.gated) return c.m == 1 || (c.m <= 16 && c.n < 10000);
+  return c.m <= 8 || (c.m <= 32 && (c.m <= 16 || c.n < 8192) && c.m * c.k <= (c.n <= 1536 ? 200000 : 24 * 14336));
 }
 
 hipError_t launch_i8(const I8Call &c, hipStream_t s) {
