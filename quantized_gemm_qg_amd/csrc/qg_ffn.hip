@@ -8,6 +8,8 @@
 // (fp32 ones run at 1/16 of the rate): the rounding errors of its elements are
 // independent, so each gradient's relative error grows from the output
 // rounding's 1.7e-3 (2-norm) to sqrt(2) times that.
+// 4096 tokens, 14336 x 4096: forward with pre-activations 801 us (1.20 PFLOP/s), the
+// elementwise pass 157, dx 724, dW 758.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"

@@ -27,10 +27,10 @@
 // one joins the parts in their order, so the sums do not depend on timing).
 //
 // Many rows are bound by their bytes: 2048 x 131072 bf16 (537 MB) in 101 us
-// without alternatives and 125 us with 20 of them.  One row of 131072 fp32 takes
-// 11.5 us, a chain of latencies: 2.0 until its logits are there, 3.4 for the
-// alternatives and sums of a part, 0.7 to publish them, 1.3 for the last
-// workgroup to read the parts, 2.7 to join them.
+// without alternatives and 118 us with 20 of them and a fifth of the tokens
+// masked.  One row of 131072 fp32 takes 11.4 us, a chain of latencies: 2.0 until
+// its logits are there, 3.4 for the alternatives and sums of a part, 0.7 to
+// publish them, 1.3 for the last workgroup to read the parts, 2.7 to join them.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"

@@ -13,18 +13,25 @@
 //
 // A workgroup computes a BM x BN tile with WM x WN waves as blocks of 16 x 16
 // (v_mfma_i32_16x16x64_i8 / v_mfma_f32_16x16x32_bf16: both take 64 bytes of k
-// per row, 16 per lane).  The operands go through a ring of ST stages of KB
-// bytes of k, filled by global_load_lds_dwordx4 (1 KB per wave and copy, no
+// per row, 16 per lane).  The operands go through a ring of ST stages of 128
+// bytes of k (a cache line per row; with 64 every line was fetched twice), filled by global_load_lds_dwordx4 (1 KB per wave and copy, no
 // register staging), and from LDS into a second set of operand registers while
-// the first one multiplies.  Bank conflicts: row chunks of 16 bytes sit at slot chunk ^ f(row), the
-// 32-byte column units of kCols at unit ^ f(k); packed pieces are read in the
-// order they are stored.  Past the last k both operands read a line of zeros
-// (nothing is multiplied by what lies behind a row), past the last row or
-// column the last valid one (never stored).
+// the first one multiplies.  Bank conflicts: row chunks of 16 bytes sit at slot
+// chunk ^ f(row), the 32-byte column units of kCols at unit ^ f(k); packed pieces
+// are read in the order they are stored.  Past the last k both operands read a
+// line of zeros (nothing is multiplied by what lies behind a row), past the last
+// row or column the last valid one (never stored).
 //
 // The weights are the MFMA's first operand, so a lane holds four consecutive
 // columns of one row: the epilogue packs them with one LDS write per block and
 // stores 16 bytes per lane along the rows.
+//
+// Bounds and rates: large products by the matrix cores, which run into the power
+// limit (1.65-1.75 GHz; busy 65-72 % of the cycles in bf16, 55 % in int8): int8 4096
+// x 14336 x 4096 215 us (2.2 POP/s), bf16 4096 x 4096 x 28672 with one operand
+// transposed 724 us (1.33 PFLOP/s), with both 758 us.  128 x 128 tiles by LDS (96 KB
+// read and 32 KB written per stage, 1024 clocks for 512 of products), small
+// batches by the latency of their stages and of the join.
 //
 // Gated: the tile's B columns are half gate and half up columns of the same
 // BN / 2 outputs, and every wave owns both halves of its outputs, so
@@ -161,8 +168,7 @@ __device__ __forceinline__ void mm_copy16_at(const uint8_t *src, uint32_t lds) {
 }
 
 // chunk order of a row's 16-byte chunks
-template <int KB>
-__device__ __forceinline__ int row_swz(int row) { return KB == 128 ? (row & 7) : ((row >> 1) & 3); }
+__device__ __forceinline__ int row_swz(int row) { return row & 7; }
 // unit order of a k row's 32-byte column units
 __device__ __forceinline__ int col_swz(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
@@ -212,7 +218,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   for (int i = 0; i < C::A_LOADS; ++i) {
     if constexpr (C::AF == kRows) {
       const int row = a_copy(i) * (64 / CPR) + lane / CPR;
-      const int c = (lane % CPR) ^ row_swz<C::KB>(row);
+      const int c = (lane % CPR) ^ row_swz(row);
       a_off[i] = (uint32_t)((int64_t)min(row, rows - 1) * a.lda + 16 * c);
       a_k[i] = 16 * c / C::EL;
     } else {
@@ -226,7 +232,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   for (int i = 0; i < C::B_LOADS; ++i) {
     if constexpr (C::BF == kRows) {
       const int row = b_copy(i) * (64 / CPR) + lane / CPR;
-      const int c = (lane % CPR) ^ row_swz<C::KB>(row);
+      const int c = (lane % CPR) ^ row_swz(row);
       const int col = b_col(row / 16, row % 16, &b_up[i]);
       b_off[i] = (uint32_t)((int64_t)(min(col, a.n - 1) - n0) * a.ldb + 16 * c);
       b_k[i] = 16 * c / C::EL;
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   } else {
 #pragma unroll
     for (int u = 0; u < C::SUB; ++u)
-      a_at[u] = (wm * C::MB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(r16));
+      a_at[u] = (wm * C::MB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz(r16));
   }
   if constexpr (C::BF == kCols) {
 #pragma unroll
@@ -311,7 +317,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   } else {
 #pragma unroll
     for (int u = 0; u < C::SUB; ++u)
-      b_at[u] = C::A + (C::BF == kRows ? (wn * C::NB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz<C::KB>(r16))
+      b_at[u] = C::A + (C::BF == kRows ? (wn * C::NB * 16 + r16) * C::KB + 16 * ((4 * u + q) ^ row_swz(r16))
                                        : (wn * C::NB * C::SUB + u) * 1024 + 16 * lane);
   }
   auto cols_frag = [&](const uint8_t *p, int width, int u) {

@@ -6,6 +6,9 @@
 // 16 bytes per lane and load, all loads of a run in flight before its first
 // product, so nothing is staged and no barrier stands between loads.
 //
+// One token of 14336 x 4096: int8 12.7 us (4.6 TB/s of weights), int8 gated 22.4
+// us (5.3 TB/s), bf16 gated 43.2 us (5.4 TB/s); a copy reaches 5.1 TB/s.
+//
 // FUSEQ (int8, the rows' codes fit in LDS): x is bf16 and every workgroup
 // quantizes it for itself while its first weights are on their way, which
 // costs it a read of x from L2 and saves a launch.  Otherwise the rows come
