@@ -537,7 +537,8 @@ qg_status qg_ffn_gated(const void *x, int64_t ldx, const void *w, int64_t ldw, i
                        uint64_t ws_bytes, hipStream_t stream);
 
 /* Backward pass of qg_ffn_gated: with dh the gradient of h,
- *   du = dh act(g), dg = dh u act'(g)      (fp32, rounded once to bf16)
+ *   du = dh act(g), dg = dh u act'(g)      (fp32, rounded once to bf16; kept
+ *       in two bf16 parts for dx up to 16 and for dw up to 32 tokens)
  *   dx = dg Wg + du Wu,  dw = [dg du]^T x  (summed in fp32, rounded once).
  *   x, w  as in the forward pass.  dh device, bf16 [m][lddh], lddh >= inter.
  *   dx    device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.

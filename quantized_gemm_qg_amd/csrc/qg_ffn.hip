@@ -7,7 +7,10 @@
 // [dg du] is rounded to bf16 once because the matrix cores take bf16 operands
 // (fp32 ones run at 1/16 of the rate): the rounding errors of its elements are
 // independent, so each gradient's relative error grows from the output
-// rounding's 1.7e-3 (2-norm) to sqrt(2) times that.
+// rounding's 1.7e-3 (2-norm) to sqrt(2) times that.  With few tokens single
+// elements decide and nothing is bound by the matrix cores, so there [dg du] is
+// kept as the sum of two bf16 numbers (dx up to 16 tokens, dW up to 32: as far
+// as one tile or stage holds both parts).
 // 4096 tokens, 14336 x 4096: forward with pre-activations 801 us (1.20 PFLOP/s), the
 // elementwise pass 157, dx 724, dW 758.
 #include <hip/hip_runtime.h>
@@ -28,7 +31,8 @@ namespace qg {
 // 2817: 17.2 against 5.1 us).
 template <bool F32, int VEC>
 __global__ __launch_bounds__(256) void ffn_dgu_kernel(const void *gu, int64_t ldgu, const uint16_t *dh, int64_t lddh,
-                                                      int64_t inter, int act, uint16_t *dgu, int64_t ldd) {
+                                                      int64_t inter, int act, uint16_t *dgu, int64_t ldd,
+                                                      int64_t halves) {
   struct alignas(2 * VEC) Bf {
     uint16_t v[VEC];
   };
@@ -36,11 +40,14 @@ __global__ __launch_bounds__(256) void ffn_dgu_kernel(const void *gu, int64_t ld
     float v[VEC];
   };
   const int64_t row = blockIdx.y, c = VEC * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-  uint16_t *d = dgu + row * ldd;
+  uint16_t *d = dgu + row * ldd, *d2 = d + halves * ldd;
   if (c >= inter) {  // padding columns
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-      if (inter + c + e < ldd) d[inter + c + e] = 0;
+      if (inter + c + e < ldd) {
+        d[inter + c + e] = 0;
+        if (halves > 0) d2[inter + c + e] = 0;
+      }
     return;
   }
   float g[VEC], u[VEC];
@@ -56,17 +63,28 @@ __global__ __launch_bounds__(256) void ffn_dgu_kernel(const void *gu, int64_t ld
     for (int e = 0; e < VEC; ++e) g[e] = bf16_bits_to_f32(gv.v[e]), u[e] = bf16_bits_to_f32(uv.v[e]);
   }
   const Bf hv = *(const Bf *)(dh + row * lddh + c);
-  Bf dg, du;
+  // what the first part's rounding left (nothing of an infinity or a NaN)
+  auto rest = [](float v, uint16_t first) {
+    return (uint16_t)((first & 0x7F80u) == 0x7F80u ? 0 : bf16_rne(v - bf16_bits_to_f32(first)));
+  };
+  Bf dg, du, dg2, du2;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     const float h = bf16_bits_to_f32(hv.v[e]);
     float v, dv;
     act_both(g[e], act, &v, &dv);
-    dg.v[e] = (uint16_t)bf16_rne(h * u[e] * dv);
-    du.v[e] = (uint16_t)bf16_rne(h * v);
+    const float g1 = h * u[e] * dv, u1 = h * v;
+    dg.v[e] = (uint16_t)bf16_rne(g1);
+    du.v[e] = (uint16_t)bf16_rne(u1);
+    dg2.v[e] = rest(g1, dg.v[e]);
+    du2.v[e] = rest(u1, du.v[e]);
   }
   *(Bf *)(d + c) = dg;
   *(Bf *)(d + inter + c) = du;
+  if (halves > 0) {
+    *(Bf *)(d2 + c) = dg2;
+    *(Bf *)(d2 + inter + c) = du2;
+  }
 }
 
 __global__ __launch_bounds__(256) void ffn_zero_kernel(uint8_t *p, int64_t ld_bytes, int64_t row_bytes, int64_t rows) {
@@ -111,6 +129,10 @@ hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info) {
                      MmCfg<false, kRows, kRows, true, 32, 128, 1, 4, 4, true>>(a, kMmPartialBytes, s, info);
 }
 
+// Rows from the first to the second part of [dg du], 0: there is no second one.
+static int64_t ffn_halves(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 0; }
+int64_t ffn_dgu_rows(int64_t m) { return m + ffn_halves(m); }
+
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s) {
   const bool f32 = c.gu_type == QG_O_F32;
   const bool four = c.inter % 4 == 0 && lddh % 4 == 0 && ((uintptr_t)dh & 7) == 0 && (f32 || c.ldgu % 4 == 0);
@@ -120,7 +142,7 @@ hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *
     auto go = [&](auto kern) {
       hipLaunchKernelGGL(kern, grid, dim3(256), 0, s,
                          (const void *)((const uint8_t *)c.gu + r0 * c.ldgu * (f32 ? 4 : 2)), c.ldgu,
-                         (const uint16_t *)dh + r0 * lddh, lddh, c.inter, c.act, (uint16_t *)dgu + r0 * ldd, ldd);
+                         (const uint16_t *)dh + r0 * lddh, lddh, c.inter, c.act, (uint16_t *)dgu + r0 * ldd, ldd, ffn_halves(c.m));
     };
     if (four)
       f32 ? go(ffn_dgu_kernel<true, 4>) : go(ffn_dgu_kernel<false, 4>);
@@ -149,11 +171,17 @@ hipError_t launch_ffn_dx(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.group_m = 4;
   a.counters = c.counters;
   a.partials = (uint64_t *)c.partials;
+  using Few = MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true>;
+  if (c.m <= 16) {
+    a.halves = (int32_t)ffn_halves(c.m);
+    a.m += a.halves;
+    return mm_dispatch<Few>(a, kMmPartialBytes, s, info);
+  }
   return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true>,
                      MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true>,
-                     MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true>>(a, kMmPartialBytes, s, info);
+                     Few>(a, kMmPartialBytes, s, info);
 }
 
 // dW = [dg du]^T x: contraction over the tokens
@@ -173,6 +201,8 @@ hipError_t launch_ffn_dw(const FfnCall &c, const void *dgu, int64_t ldd, void *d
   a.group_m = 4;
   a.counters = c.counters;
   a.partials = (uint64_t *)c.partials;
+  a.halves = (int32_t)ffn_halves(c.m);
+  a.kd += a.halves;
   return mm_dispatch<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 2, false>,
                      MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 2, true>,
                      MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 4, true>>(a, kMmPartialBytes, s, info);

@@ -390,6 +390,8 @@ struct FfnCall {
   uint32_t *counters;  // split-K counters and partial tiles
   void *partials;
 };
+// rows of [dg du] in the workspace (of few tokens: two parts)
+int64_t ffn_dgu_rows(int64_t m);
 // info: NULL, or nothing is launched and the choice reported
 hipError_t launch_ffn_forward(const FfnCall &c, hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_ffn_dgu(const FfnCall &c, const void *dh, int64_t lddh, void *dgu, int64_t ldd, hipStream_t s);

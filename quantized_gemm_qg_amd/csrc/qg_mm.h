@@ -91,6 +91,11 @@ struct MmArgs {
   int64_t ldgu;
   int32_t gu_type;
   int32_t act;
+  // bf16 backward of few tokens: the operand A is the sum of two bf16 parts, the
+  // second one `halves` (0: there is none) rows behind the first.  kRows: both
+  // are rows of one tile, m counts to the last, and output row r is r plus
+  // r + halves; kCols: kd counts to the last (one stage), B's row repeats.
+  int32_t halves;
   int32_t group_m;
   // split over k: `per` stages each; one arrival counter per tile and the
   // partial tiles [split][tile]
@@ -124,6 +129,7 @@ struct MmCfg {
   static constexpr int PITCH = 16 * OUT_NB * 4 + 16;                  // bytes of a slab row (fp32)
   static constexpr int SLAB = 16 * PITCH;
   static constexpr int LDS = STAGE * ST > WAVES * SLAB ? STAGE * ST : WAVES * SLAB;
+  static constexpr bool ROW_HALVES = !I8 && AF == kRows && BF == kCols && BM == 32, K_HALVES = AF == kCols;
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && (!GATED || NB % 2 == 0), "blocks");
   static_assert(!I8 || AF == kRows, "int8 activations are rows");
   static_assert(AF != kCols || BM >= 128, "column units for the swizzle");
@@ -246,7 +252,8 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     } else {
       const int k = b_copy(i) * (512 / C::BN) + lane / (C::BN / 8), s = lane % (C::BN / 8);
       const int col = 16 * ((s >> 1) ^ col_swz(k)) + 8 * (s & 1);
-      b_off[i] = (uint32_t)(k * a.ldb + 2 * min(col, ((a.n + 7) & ~7) - 8 - n0));
+      const int row = C::K_HALVES && a.halves > 0 && k >= a.halves ? k - a.halves : k;
+      b_off[i] = (uint32_t)(row * a.ldb + 2 * min(col, ((a.n + 7) & ~7) - 8 - n0));
       b_k[i] = k;
       b_up[i] = false;
     }
@@ -283,12 +290,14 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
         mm_copy16(bs + (b_up[i] ? up : 0), b_off[i], st + C::A + b_copy(i) * 1024);
     } else {
       const int left = a.kd - s * C::KE;
+      // (between two halves nothing)
+      auto in = [&](int k) { return k < left && !(C::K_HALVES && k >= left - a.halves && k < a.halves); };
 #pragma unroll
       for (int i = 0; i < C::A_LOADS; ++i)
-        mm_copy16_at(a_k[i] < left ? as + a_off[i] : (const uint8_t *)mm_zeros, st + a_copy(i) * 1024);
+        mm_copy16_at(in(a_k[i]) ? as + a_off[i] : (const uint8_t *)mm_zeros, st + a_copy(i) * 1024);
 #pragma unroll
       for (int i = 0; i < C::B_LOADS; ++i)
-        mm_copy16_at(b_k[i] < left ? bs + (b_up[i] ? up : 0) + b_off[i] : (const uint8_t *)mm_zeros,
+        mm_copy16_at(in(b_k[i]) ? bs + (b_up[i] ? up : 0) + b_off[i] : (const uint8_t *)mm_zeros,
                      st + C::A + b_copy(i) * 1024);
     }
   };
@@ -470,6 +479,14 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     }
   }
 
+  if constexpr (C::ROW_HALVES) {
+    if (a.halves > 0) {
+#pragma unroll
+      for (int j = 0; j < C::NB; ++j) acc[0][j] += acc[1][j];
+    }
+  }
+  const int m_out = C::ROW_HALVES && a.halves > 0 ? a.m - a.halves : a.m;
+
   // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
   mm_barrier();
   uint8_t *slab = smem + wave * C::SLAB;
@@ -511,7 +528,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
 #pragma unroll
     for (int r0 = 0; r0 < 16; r0 += ROWS) {
       const int rr = r0 + lane / CHUNKS, row = row_w + 16 * i + rr;
-      if (lane >= ROWS * CHUNKS || row >= a.m || col >= a.n) continue;
+      if (lane >= ROWS * CHUNKS || row >= m_out || col >= a.n) continue;
       const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * EL);
       uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * EL;
       if (col + PER <= a.n) {

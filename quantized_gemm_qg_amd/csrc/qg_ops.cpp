@@ -166,7 +166,7 @@ static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bo
     sp.partials = std::max(sp.partials, i.bytes);
     launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
-    sp.dgu = align_up((uint64_t)m * dgu_pitch(inter) * 2, 256);
+    sp.dgu = align_up((uint64_t)ffn_dgu_rows(m) * dgu_pitch(inter) * 2, 256);
     if (recompute) sp.gu = align_up((uint64_t)m * 2 * inter * 4, 256);
   }
   sp.partials = align_up(sp.partials, 256);
