@@ -514,9 +514,12 @@ __global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs
 // dl in one pass: 16 bytes per thread and step, VEC steps of a row in flight.
 // Reads and writes of one 16 bytes are the same thread's, so dl may be l.  From
 // the last row on: what the forward pass read last is found in the caches
-// (forward and backward of 2048 x 131072 bf16: 334 -> 330 us).  Bound by its
-// bytes: 1021 x 100003 bf16, 408 MB, in 77 us (5.3 TB/s).
-template <bool F32, int VEC>
+// (forward and backward of 2048 x 131072 bf16: 334 -> 330 us).  PAST: a gradient
+// larger than the L2s (32 MB) is written past the caches, where it would push
+// out the logits and be written back behind the next reads (forward and backward
+// of 1021 x 100003 bf16 140 -> 121 us); a smaller one stays for who reads it next.
+// Bound by its bytes.
+template <bool F32, int VEC, bool PAST>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs a) {
   using C = Chunk<F32, VEC, kThreads>;
   constexpr int EL = F32 ? 4 : 2;
@@ -557,7 +560,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
         }
         if (empty) w = u32x4{0u, 0u, 0u, 0u};
         if (i + C::EPV <= vocab) {
-          *(u32x4_any *)(dp + (int64_t)i * EL) = w;
+          if constexpr (PAST)
+            __builtin_nontemporal_store(w, (u32x4_any *)(dp + (int64_t)i * EL));
+          else
+            *(u32x4_any *)(dp + (int64_t)i * EL) = w;
         } else {
           uint8_t *p = dp + (int64_t)at * EL;
 #pragma unroll
@@ -631,10 +637,12 @@ hipError_t launch_logprobs_backward(const LogprobArgs &a, hipStream_t s) {
   // one workgroup per chunk up to about eight per CU, then more chunks each
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (2048 + a.rows - 1) / a.rows));
   const dim3 grid((unsigned)parts, (unsigned)std::min<int64_t>(a.rows, 65535));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, s, a); };
+  const bool past = a.rows * a.vocab * (a.f32 ? 4 : 2) > (32 << 20);
   if (a.f32)
-    hipLaunchKernelGGL((logprobs_backward_kernel<true, 4>), grid, dim3(kThreads), 0, s, a);
+    past ? go(logprobs_backward_kernel<true, 4, true>) : go(logprobs_backward_kernel<true, 4, false>);
   else
-    hipLaunchKernelGGL((logprobs_backward_kernel<false, 4>), grid, dim3(kThreads), 0, s, a);
+    past ? go(logprobs_backward_kernel<false, 4, true>) : go(logprobs_backward_kernel<false, 4, false>);
   return hipGetLastError();
 }
 

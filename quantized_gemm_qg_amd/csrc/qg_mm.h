@@ -29,7 +29,7 @@
 // Bounds and rates: large products by the matrix cores, which run into the power
 // limit (1.65-1.75 GHz; busy 65-72 % of the cycles in bf16, 55 % in int8): int8 4096
 // x 14336 x 4096 215 us (2.2 POP/s), bf16 4096 x 4096 x 28672 with one operand
-// transposed 724 us (1.33 PFLOP/s), with both 758 us.  128 x 128 tiles by LDS (96 KB
+// transposed 724 us (1.33 PFLOP/s), with both 742 us.  128 x 128 tiles by LDS (96 KB
 // read and 32 KB written per stage, 1024 clocks for 512 of products), small
 // batches by the latency of their stages and of the join.
 //
@@ -532,7 +532,13 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
       const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * EL);
       uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * EL;
       if (col + PER <= a.n) {
-        *(u32x4_any *)dst = v;
+        // (a weight gradient is read once, much later: past the caches; the backward
+        // of one token through 14336 x 4096 124 -> 100 us, while the forward's
+        // outputs, read next, lose: 790 -> 810 us at 4096 tokens)
+        if constexpr (C::AF == kCols)
+          __builtin_nontemporal_store(v, (u32x4_any *)dst);
+        else
+          *(u32x4_any *)dst = v;
       } else {
 #pragma unroll
         for (int b = 0; b < PER; ++b) {

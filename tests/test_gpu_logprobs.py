@@ -232,6 +232,11 @@ def test_backward(rows, vocab, pad, shift, kind, dtype):
     assert torch.equal(d[:, :vocab], ref)
 
 
+def test_backward_of_a_gradient_larger_than_the_caches():
+    test_backward(170, 100003, 0, 0, "masked", torch.bfloat16)
+    test_backward(70, 131072, 5, 1, "plain", torch.float32)
+
+
 def test_gradient_against_differences():
     l, tok = make("plain", 3, 50, torch.float32, 8)
     scale = 1.5
