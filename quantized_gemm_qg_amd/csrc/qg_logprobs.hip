@@ -27,7 +27,7 @@
 // one joins the parts in their order, so the sums do not depend on timing).
 //
 // Many rows are bound by their bytes: 2048 x 131072 bf16 (537 MB) in 101 us
-// without alternatives and 118 us with 20 of them and a fifth of the tokens
+// without alternatives and 114 us with 20 of them and a fifth of the tokens
 // masked.  One row of 131072 fp32 takes 11.4 us, a chain of latencies: 2.0 until
 // its logits are there, 3.4 for the alternatives and sums of a part, 0.7 to
 // publish them, 1.3 for the last workgroup to read the parts, 2.7 to join them.
@@ -157,8 +157,16 @@ struct Chunk {
   // Chunk at logit `first` of a row of `vocab`.  16 bytes that the row's end
   // cuts are read whole, ending with the row, and what is the neighbour's of
   // them is masked; so is everything behind the end.
-  __device__ __forceinline__ void load(const uint8_t *row, int first, int base, int vocab) {
+  __device__ __forceinline__ void load(const uint8_t *row, int first, int base, int vocab, bool once) {
     if (first + SIZE <= vocab) {
+      if (once) {
+        asm volatile("");  // (else both branches become one, of plain loads)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          d[v] = __builtin_nontemporal_load((const u32x4_any *)(row + (int64_t)place(base, v) * EL));
+        asm volatile("");
+        return;
+      }
 #pragma unroll
       for (int v = 0; v < VEC; ++v) d[v] = *(const u32x4_any *)(row + (int64_t)place(base, v) * EL);
       return;
@@ -341,6 +349,10 @@ __global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs
   const int vocab = (int)a.vocab;
   const float c2 = a.scale * kLog2e;
   const int parts = SHARED ? gridDim.x : 1, part = SHARED ? blockIdx.x : 0;
+  // no statistics are asked for, so no gradient reads the logits again: they are
+  // read past the caches (3391 x 38531 fp32 98 -> 90 us; with a gradient, 1021 x
+  // 100003 bf16, 119 -> 136 us)
+  const bool once = a.stats == nullptr;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
     // this workgroup's logits, in equal parts (a short last one would have no
@@ -353,7 +365,7 @@ __global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs
     constexpr bool AHEAD = VEC <= 4;
     C ch;
     if constexpr (AHEAD) {
-      ch.load(lp, begin, C::base_of(begin), end);
+      ch.load(lp, begin, C::base_of(begin), end, once);
       __builtin_amdgcn_sched_barrier(0);
     }
     const int tok = a.tokens ? a.tokens[row] : -1;
@@ -363,7 +375,7 @@ __global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs
     Sums st = {neg_inf(), 0.f, 0.f};
     int above = 0, have = 0;
     for (int first = begin; first < end; first += C::SIZE) {
-      if (!AHEAD || first > begin) ch.load(lp, first, C::base_of(first), end);
+      if (!AHEAD || first > begin) ch.load(lp, first, C::base_of(first), end, once);
       float most = neg_inf(), vmax[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
@@ -539,7 +551,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobArgs
     for (int first = (int)blockIdx.x * C::SIZE; first < vocab; first += (int)gridDim.x * C::SIZE) {
       C ch;
       const int base = C::base_of(first);
-      ch.load(lp, first, base, vocab);
+      ch.load(lp, first, base, vocab, false);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int i = C::place(base, v), at = C::id(base, v, vocab);

@@ -6,8 +6,14 @@
 // 16 bytes per lane and load, all loads of a run in flight before its first
 // product, so nothing is staged and no barrier stands between loads.
 //
-// One token of 14336 x 4096: int8 12.7 us (4.6 TB/s of weights), int8 gated 22.4
-// us (5.3 TB/s), bf16 gated 43.2 us (5.4 TB/s); a copy reaches 5.1 TB/s.
+// One token of 14336 x 4096: int8 12.7 us (4.6 TB/s of weights), int8 gated 20.8
+// us (5.6 TB/s), bf16 gated 43.2 us (5.4 TB/s); a copy reaches 5.1 TB/s.
+//
+// PAST (int8 weights from 64 MB on, which are no longer in the caches when their
+// layer's turn comes again): loads past the caches (one gated token of 14336 x 4096
+// 23.3 -> 21.7 us from memory, one of 8192 x 8192 ungated 15.9 -> 14.6; but 23 rows
+// of 4096 x 14336, which the caches hold, 18.3 -> 21.1).  Not bf16, whose lines take
+// two loads each (45.3 -> 48.2).
 //
 // FUSEQ (int8, the rows' codes fit in LDS): x is bf16 and every workgroup
 // quantizes it for itself while its first weights are on their way, which
@@ -52,7 +58,7 @@ constexpr int64_t rows_lds_bytes(bool fuseq, int64_t m, int64_t k, int waves) {
 template <bool I8, bool GATED>
 constexpr int rows_waves() { return I8 && GATED ? 4 : 8; }
 
-template <bool I8, bool GATED, int MT, int NT, int KR, bool FUSEQ>
+template <bool I8, bool GATED, int MT, int NT, int KR, bool FUSEQ, bool PAST>
 __global__ __launch_bounds__((I8 && GATED) ? 256 : 512, MT == 1 ? 4 : 3) void rows_kernel(MmArgs a) {
   static_assert(!FUSEQ || (I8 && MT == 1), "quantized rows in LDS");
   static_assert(!GATED || NT == 2, "a gate strip and its up strip");
@@ -94,7 +100,10 @@ __global__ __launch_bounds__((I8 && GATED) ? 256 : 512, MT == 1 ? 4 : 3) void ro
     for (int t = 0; t < NT; ++t) {
       const uint8_t *u = bp[t] + (int64_t)b * (I8 ? 2048 : 128);  // uniform
 #pragma unroll
-      for (int h = 0; h < 2; ++h) bw[r][t][h] = *(const u32x4 *)(u + bo[t] + (I8 ? 1024 : 64) * h);
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 *p = (const u32x4 *)(u + bo[t] + (I8 ? 1024 : 64) * h);
+        bw[r][t][h] = PAST ? __builtin_nontemporal_load(p) : *p;
+      }
     }
     if constexpr (!FUSEQ) {
       const uint8_t *u = a.a + (int64_t)b * 128;
@@ -298,7 +307,10 @@ static hipError_t launch_rows(const MmArgs &a, hipStream_t s) {
   const int waves = runs < rows_waves<I8, GATED>() ? runs : rows_waves<I8, GATED>();
   const int strips = (a.n + 15) / 16, per = GATED ? 1 : NT;
   const int64_t lds = rows_lds_bytes<MT, NT>(FUSEQ, a.m, a.kd, waves);
-  auto kern = rows_kernel<I8, GATED, MT, NT, KR, FUSEQ>;
+  auto kern = rows_kernel<I8, GATED, MT, NT, KR, FUSEQ, false>;
+  if constexpr (I8 && MT == 1) {
+    if ((int64_t)a.n * a.kd * (GATED ? 2 : 1) >= (64 << 20)) kern = rows_kernel<I8, GATED, MT, NT, KR, FUSEQ, true>;
+  }
   hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((strips + per - 1) / per), dim3(64 * waves), lds, s, a);
