@@ -164,7 +164,7 @@ MmInfo i8_info(const I8Call &c) {
   if (c.quantize || i8_few_rows(c))
     info.bm = c.m > 16 ? 32 : 16;
   else
-    i8_tiled(c, nullptr, &info);
+    (void)i8_tiled(c, nullptr, &info);
   return info;
 }
 

@@ -158,13 +158,13 @@ static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bo
   c.inter = inter;
   MmInfo i;
   if (!backward || recompute) {
-    launch_ffn_forward(c, nullptr, &i);
+    (void)launch_ffn_forward(c, nullptr, &i);
     sp.partials = i.bytes;
   }
   if (backward) {
-    launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &i);
+    (void)launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
-    launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &i);
+    (void)launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
     sp.dgu = align_up((uint64_t)ffn_dgu_rows(m) * dgu_pitch(inter) * 2, 256);
     if (recompute) sp.gu = align_up((uint64_t)m * 2 * inter * 4, 256);
