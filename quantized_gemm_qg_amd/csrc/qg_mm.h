@@ -152,9 +152,13 @@ __device__ __forceinline__ void wait_loads(int stages) {
   }
 }
 
-// Workgroup barrier that no memory access moves across.
+// Workgroup barrier that no memory access moves across and that no wave reaches
+// with an LDS access out: s_barrier itself waits for none, and the compiler may
+// sink the products that a read feeds (and its wait) below it, while other waves
+// write the same LDS behind it.
 __device__ __forceinline__ void mm_barrier() {
   asm volatile("" ::: "memory");
+  QG_WAIT_LGKMCNT0();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -405,9 +409,8 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     read(s, 1, f[1]);
     multiply(f[0]);
     interleave();
-    // stages s + 2 .. s + ST - 1 may still be out; this wave's reads of stage s are done
+    // stages s + 2 .. s + ST - 1 may still be out
     wait_loads<C::LOADS>(min(C::ST - 2, steps - 2 - s));
-    QG_WAIT_LGKMCNT0();
     mm_barrier();  // stage s + 1 is in LDS, stage s free
     if (s + C::ST < steps) issue(s + C::ST);
     read(s + 1, 0, f[0]);
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   const int m_out = C::ROW_HALVES && a.halves > 0 ? a.m - a.halves : a.m;
 
   // ---- epilogue: 16-row slabs through a wave-private part of the ring ----
-  mm_barrier();
+  mm_barrier();  // the last fragments are in registers for every wave, the ring is free
   uint8_t *slab = smem + wave * C::SLAB;
   const int row_w = m0 + wm * C::MB * 16;           // first row of the wave
   const int col_w = n0 + wn * C::OUT_NB * 16;       // first output column of the wave
