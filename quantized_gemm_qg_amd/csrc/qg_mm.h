@@ -651,14 +651,28 @@ static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) 
   return hipGetLastError();
 }
 
-// The cheapest of the compiled shapes: launches it, or (info) only says which it
-// is and what partial tiles it needs.
+// Whether the 32-bit offsets of the copies, from the 64-bit base of a tile and a
+// stage, reach all of a stage's rows at these pitches.
+template <class C>
+static bool mm_reaches(const MmArgs &a) {
+  constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  const int64_t far_a = (C::AF == kRows ? C::BM - 1 : C::KE - 1) * a.lda + (C::AF == kRows ? C::KB : 2 * C::BM);
+  const int64_t far_b = C::BF == kRows   ? (OUT_BN - 1) * a.ldb + C::KB
+                        : C::BF == kCols ? (C::KE - 1) * a.ldb + 2 * C::BN
+                                         : (int64_t)(OUT_BN / 16 + 1) * a.ldb;
+  return far_a <= (1ll << 32) && far_b <= (1ll << 32);
+}
+
+// The cheapest of the compiled shapes that reach their operands' rows: launches
+// it, or (info; the pitches count here too) only says which it is and what
+// partial tiles it needs.
 template <class... Cs>
 static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, MmInfo *info) {
   const MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
-  int best = 0;
-  for (int i = 1; i < (int)sizeof...(Cs); ++i)
-    if (plans[i].cost < plans[best].cost) best = i;
+  const bool reach[] = {mm_reaches<Cs>(a)...};
+  int best = -1;
+  for (int i = 0; i < (int)sizeof...(Cs); ++i)
+    if (reach[i] && (best < 0 || plans[i].cost < plans[best].cost)) best = i;
   int i = 0;
   hipError_t e = hipErrorInvalidValue;
   auto one = [&](auto *cfg) {

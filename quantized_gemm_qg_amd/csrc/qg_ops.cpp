@@ -23,7 +23,9 @@ static qg_status ws_check(uint64_t need, const void *ws, uint64_t ws_bytes) {
 }
 
 // The tiled products address a tile's rows with 32-bit offsets from a 64-bit
-// base: 256 rows of this pitch stay below 2 GiB.
+// base: 256 rows of this pitch stay below 2 GiB.  (The gradient of the
+// pre-activations has rows of up to 64 MiB, of which 64 are within reach: shapes
+// of more rows are left out where theirs are not.)
 constexpr int64_t kMaxPitchBytes = 1 << 23;
 // Tiles are numbered in 32 bits (the smallest tile is 64 x 32 outputs).
 static bool tiles_fit(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 31) / 32) < (1ll << 31) - 8; }
@@ -149,6 +151,7 @@ struct FfnSpace {
     return b ? kSplitCounterBytes + b : 0;
   }
 };
+// (the choice of a shape depends on the pitch of the gradient, not on the caller's)
 static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bool recompute) {
   FfnSpace sp;
   if (m <= 0 || k <= 0 || inter <= 0 || m > (1ll << 30) || k > (1 << 22) || inter > (1 << 24)) return sp;
@@ -162,9 +165,9 @@ static FfnSpace ffn_space(int64_t m, int64_t k, int64_t inter, bool backward, bo
     sp.partials = i.bytes;
   }
   if (backward) {
-    (void)launch_ffn_dx(c, nullptr, 0, nullptr, 0, nullptr, &i);
+    (void)launch_ffn_dx(c, nullptr, dgu_pitch(inter), nullptr, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
-    (void)launch_ffn_dw(c, nullptr, 0, nullptr, 0, 0, nullptr, &i);
+    (void)launch_ffn_dw(c, nullptr, dgu_pitch(inter), nullptr, 0, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
     sp.dgu = align_up((uint64_t)ffn_dgu_rows(m) * dgu_pitch(inter) * 2, 256);
     if (recompute) sp.gu = align_up((uint64_t)m * 2 * inter * 4, 256);

@@ -297,3 +297,41 @@ def test_graph_replays():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(eager, (h, dx, dw)))
+
+
+def test_dx_of_a_feed_forward_size_whose_rows_lie_megabytes_apart():
+    """8.5 million inner columns: 128 rows of [dg du] are further apart than 32
+    bits of bytes.  Only 64 columns and their weights are not zero, so the
+    products' bound is that of 128 terms."""
+    m, k, inter = 129, 264, 8500000
+    gen = torch.Generator().manual_seed(3)
+    at = torch.randint(inter, (64,), generator=gen).unique()
+    at[0], at[-1] = 0, inter - 1
+    n = at.numel()
+    bf = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16)  # noqa: E731
+    g, u, dh, wg, wu = bf(m, n), bf(m, n), bf(m, n), bf(n, k), bf(n, k)
+    gu = torch.zeros(m, 2 * inter, dtype=torch.bfloat16, device="cuda")
+    dhd = torch.zeros(m, inter, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(2 * inter, k, dtype=torch.bfloat16, device="cuda")
+    cols = at.cuda()
+    gu[:, cols], gu[:, inter + cols], dhd[:, cols] = g.cuda(), u.cuda(), dh.cuda()
+    w[cols], w[inter + cols] = wg.cuda(), wu.cuda()
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full((m, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    wsb = qg.ffn_gated_backward_workspace_size(m, k, inter)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    ws[:65536] = 0
+    print(f"ffn dx m={m} k={k} inter={inter}, workspace {wsb} bytes", flush=True)
+    qg.ffn_gated_backward(x, k, w, k, dhd, inter, m, k, inter, qg.ACT_SILU, dx, k, None, 0, 0, ws, wsb, gu=gu,
+                          gu_type=qg.O_BF16, ldgu=2 * inter)
+    got = dx.cpu().to(D)
+    del gu, dhd, w, ws
+    torch.cuda.empty_cache()
+    g, u, dh = g.to(D), u.to(D), dh.to(D)
+    a, da = act64(g, qg.ACT_SILU)
+    dgu, both = torch.cat((dh * u * da, dh * a), 1), torch.cat((wg, wu)).to(D)
+    act = 2.0 ** -20 * (1 + g.abs())
+    e = torch.cat((dh.abs() * act * u.abs(), dh.abs() * act), 1) + U16 * dgu.abs()
+    bound = e @ both.abs() + 2 * n * 2 * U32 * ((dgu.abs() + e) @ both.abs())
+    ref = dgu @ both
+    within(got, ref, bound * (1 + U16) + U16 * ref.abs() + 1e-37)
