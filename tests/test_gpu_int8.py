@@ -241,3 +241,34 @@ def test_graph_replays():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, eager)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 16400, 4096), (5, 16400, 4096), (2, 65600, 1024)])
+def test_weights_read_past_the_caches(m, n, k):
+    """Few rows of 64 MB of weights and more, quantized in the kernel and before it."""
+    assert n * k >= 64 << 20
+    test_product_matches_64_bits(m, n, k, qg.O_BF16)
+
+
+@pytest.mark.parametrize("m,inter,k", [(1, 8200, 4096), (4, 8200, 4096)])
+def test_gated_weights_read_past_the_caches(m, inter, k):
+    assert 2 * inter * k >= 64 << 20
+    test_gated_matches_64_bits(m, inter, k, qg.ACT_SILU)
+
+
+@pytest.mark.parametrize("m,k", [(3, 16416), (2, 40000), (1, 130816), (4100, 32), (8200, 264)])
+def test_quantize_rows_longer_and_more_than_one_pass_holds(m, k):
+    """Rows that a workgroup's registers do not hold, and more rows than workgroups."""
+    test_quantize_int8(m, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 40, 16416), (1, 17, 65408), (1, 17, 65568), (3, 33, 40000), (4200, 48, 64)])
+def test_products_that_quantize_long_rows(m, n, k):
+    """In the kernel (one row up to 64 K codes, past what its threads ask for
+    ahead) and by a launch of its own."""
+    test_product_matches_64_bits(m, n, k, qg.O_F32)
+
+
+@pytest.mark.parametrize("m,inter,k", [(1, 20, 9248), (1, 17, 40000), (2, 17, 20512)])
+def test_gated_products_that_quantize_long_rows(m, inter, k):
+    test_gated_matches_64_bits(m, inter, k, qg.ACT_GELU_TANH)
