@@ -284,3 +284,40 @@ def test_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, out))
+
+
+@pytest.mark.parametrize("rows,vocab,kind,dtype", [
+    (40, 131072, "plain", torch.bfloat16), (40, 131072, "masked", torch.bfloat16), (40, 131072, "ties", torch.bfloat16),
+    (40, 131072, "strided", torch.bfloat16), (20, 100003, "plain", torch.float32), (20, 100003, "masked", torch.float32),
+    (20, 100003, "ties", torch.float32), (20, 100003, "strided", torch.float32),
+    (385, 33000, "plain", torch.bfloat16), (260, 25001, "sorted", torch.float32)])
+def test_forward_of_tens_and_hundreds_of_long_rows(rows, vocab, kind, dtype):
+    """Rows that a few workgroups share in large chunks: one chunk each, or a
+    chunk and a piece of the next."""
+    test_forward(rows, vocab, kind, dtype)
+
+
+@pytest.mark.parametrize("kind", ["masked", "ties"])
+def test_forward_of_rows_that_four_units_a_thread_hold(kind):
+    test_forward(20, 3001, kind, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,pad,shift", [(1, 5, 0, 0), (5, 64, 1, 1), (300, 9001, 0, 0), (1100, 4099, 5, 1), (1, 131072, 0, 0),
+                                                  (3, 100003, 5, 1), (40, 131072, 0, 0), (40, 131072, 3, 3), (800, 17000, 0, 0)])
+def test_forward_without_statistics(rows, vocab, pad, shift, dtype):
+    """The same bits as with them (their rows are read past the caches)."""
+    print(f"logprobs without stats rows={rows} vocab={vocab} {dtype}", flush=True)
+    l, tok = make("masked", rows, vocab, dtype, rows + vocab)
+    d = place(l, dtype, pad, shift)
+    d.vocab = vocab
+    ltype = qg.O_F32 if dtype == torch.float32 else qg.O_BF16
+    for top in (0, 20):
+        o = forward(d, ltype, tok.cuda(), 0.7, top)
+        n = {name: torch.full_like(t, 7) for name, t in o.items()}
+        wsb = qg.token_logprobs_workspace_size(rows, vocab, top)
+        ws = torch.zeros(max(wsb, 1), dtype=torch.uint8, device="cuda")
+        qg.token_logprobs(d, ltype, rows, vocab, d.stride(0), tok.cuda(), 0.7, top, n["logp"], n["entropy"], None, n["rank"],
+                          n["top_ids"] if top else None, n["top_logp"] if top else None, ws, wsb)
+        for name in ("logp", "entropy", "rank") + (("top_ids", "top_logp") if top else ()):
+            assert torch.equal(n[name], o[name]), name
