@@ -335,3 +335,24 @@ def test_dx_of_a_feed_forward_size_whose_rows_lie_megabytes_apart():
     bound = e @ both.abs() + 2 * n * 2 * U32 * ((dgu.abs() + e) @ both.abs())
     ref = dgu @ both
     within(got, ref, bound * (1 + U16) + U16 * ref.abs() + 1e-37)
+
+
+@pytest.mark.parametrize("m", [1, 20, 40])
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+def test_backward_of_aligned_rows_gives_the_bits_of_unaligned_ones(m, act):
+    """The elementwise pass takes four elements a thread where rows of dh (and
+    of bf16 pre-activations) allow it, else one: the same results, of which the
+    other tests compare the latter with 64 bits."""
+    c = Case(m, 264, 100, act, seed=m)
+    _, gu, ldgu = c.forward(qg.O_F32)
+    i = c.inter
+    narrow = torch.full((m, 2 * i + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide = torch.full((m, 2 * i + 4), float("nan"), dtype=torch.bfloat16, device="cuda")
+    narrow[:, :2 * i] = wide[:, :2 * i] = gu[:m, :2 * i]
+    one = [c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu), c.backward(gu=narrow, gu_type=qg.O_BF16, ldgu=2 * i + 3)]
+    assert c.lddh % 4 != 0
+    c.lddh = i + 4
+    c.dhd = c._pad(c.dh, c.lddh)
+    four = [c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu), c.backward(gu=wide, gu_type=qg.O_BF16, ldgu=2 * i + 4)]
+    for (dx1, dw1), (dx4, dw4) in zip(one, four):
+        assert torch.equal(dx1, dx4) and torch.equal(dw1, dw4)
