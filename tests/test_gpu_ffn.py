@@ -11,6 +11,7 @@ import torch
 
 import quantized_gemm_qg_amd as qg
 from gpu_harness import require_gpu
+from gradient_check import check_block_gradients
 
 pytestmark = pytest.mark.gpu
 U32, U16 = 2.0 ** -24, 2.0 ** -8
@@ -356,3 +357,13 @@ def test_backward_of_aligned_rows_gives_the_bits_of_unaligned_ones(m, act):
     four = [c.backward(gu=gu, gu_type=qg.O_F32, ldgu=ldgu), c.backward(gu=wide, gu_type=qg.O_BF16, ldgu=2 * i + 4)]
     for (dx1, dw1), (dx4, dw4) in zip(one, four):
         assert torch.equal(dx1, dx4) and torch.equal(dw1, dw4)
+
+
+@pytest.mark.parametrize("act", [qg.ACT_SILU, qg.ACT_GELU_TANH])
+@pytest.mark.parametrize("m", [9, 70])
+def test_each_gradient_against_differences_along_itself(m, act):
+    """The roundings of [dg du] and of the output take each at most 2^-8 of a
+    part's norm."""
+    c = Case(m, 136, 45, act, seed=11)
+    dx, dw = c.backward()
+    check_block_gradients(c.x.to(D), c.w.to(D), c.dh.to(D), act == qg.ACT_SILU, dx, dw, 2 * U16)
