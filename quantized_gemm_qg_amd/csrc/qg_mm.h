@@ -168,7 +168,11 @@ __device__ __forceinline__ void mm_barrier() {
 // 1 KB.  Written out because the builtin makes the compiler wait for every
 // outstanding copy before each transposed LDS read (it cannot tell the stages
 // of the ring apart there); the waits are wait_loads above.  The instruction
-// has no destination register.
+// has no destination register.  m0 is a reserved register, which the compiler
+// does not preserve around such a clobber and warns about for every copy: these
+// kernels name it nowhere else, so there is nothing to preserve.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void mm_copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
@@ -176,6 +180,7 @@ __device__ __forceinline__ void mm_copy16(const uint8_t *base, uint32_t off, uin
 __device__ __forceinline__ void mm_copy16_at(const uint8_t *src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // chunk order of a row's 16-byte chunks
 __device__ __forceinline__ int row_swz(int row) { return row & 7; }

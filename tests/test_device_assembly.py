@@ -1,5 +1,5 @@
-"""Workgroup barriers of the compiled kernels of the language-model operators
-(CPU: the device assembly that the build's own flags give).
+"""The compiled kernels of the language-model operators: what the source leaves
+to the compiler (CPU: the device assembly that the build's own flags give).
 
 s_barrier does not wait for LDS accesses that a wave still has in flight, and
 the compiler may sink what consumes a read below the barrier.  Behind a barrier
@@ -96,12 +96,32 @@ def test_the_count_follows_every_path():
     assert lds_accesses_out_at_barriers(loop)[0] > 0
 
 
-@pytest.mark.parametrize("src", ["qg_ffn.hip", "qg_int8.hip", "qg_logprobs.hip"])
-def test_no_barrier_is_reached_with_lds_accesses_out(src, tmp_path):
-    b = build_module()
-    asm = tmp_path / "device.s"
-    subprocess.run([b.hipcc(), "-S", "--cuda-device-only", *b._flags(), *b.EXTRA.get(src, []), "-x", "hip",
-                    os.path.join(b.CSRC, src), "-o", str(asm)], check=True, capture_output=True)
-    found = {name: lds_accesses_out_at_barriers(lines) for name, lines in kernels(asm.read_text())}
+@pytest.fixture(scope="module", params=["qg_ffn.hip", "qg_int8.hip", "qg_logprobs.hip"])
+def compiled(request, tmp_path_factory):
+    """Device assembly of one source, and what the compiler said."""
+    b, asm = build_module(), tmp_path_factory.mktemp("asm") / "device.s"
+    r = subprocess.run([b.hipcc(), "-S", "--cuda-device-only", *b._flags(), *b.EXTRA.get(request.param, []), "-x", "hip",
+                        os.path.join(b.CSRC, request.param), "-o", str(asm)], check=True, capture_output=True, text=True)
+    return asm.read_text(), r.stderr
+
+
+def test_no_barrier_is_reached_with_lds_accesses_out(compiled):
+    found = {name: lds_accesses_out_at_barriers(lines) for name, lines in kernels(compiled[0])}
     assert sum(map(len, found.values())) > 0
     assert {name: n for name, n in found.items() if any(n)} == {}
+
+
+def test_only_the_written_out_copies_use_m0(compiled):
+    """Where there are any: they change m0 behind the compiler's back (a clobber
+    of a reserved register does not make it save it)."""
+    written_out, uses = False, {True: [], False: []}
+    for line in compiled[0].splitlines():
+        if "#ASMSTART" in line or "#ASMEND" in line:
+            written_out = "#ASMSTART" in line
+        elif re.search(r"\bm0\b", line.split(";")[0]):
+            uses[written_out].append(line)
+    assert not uses[True] or uses[False] == []
+
+
+def test_the_device_code_compiles_without_warnings(compiled):
+    assert compiled[1] == ""
