@@ -132,18 +132,33 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
                      I8Cfg<false, 32, 128, 1, 8, 4, true>>(a, budget, s, info);
 }
 
-// Calls of the few-rows kernel: up to 16 rows, and up to 32 where N gives the
-// tiled kernel less than half a round of 128-column tiles, as long as the rows
-// are not too long to be read by every workgroup (32 rows of 8192 columns: k =
-// 8192 10.8 us against 13.1 tiled, 16384 18.5 against 14.4; with few columns the
-// workgroups are too few sooner: 24 rows of 1000 x 14336 15.4 against 12.3, 16
-// rows 13.1 against 12.1, 8 rows 10.4 against 11.9).  32 rows of 14336 x 4096:
-// 19.0 against 15.5.  Gated, from 2 rows on, not with many columns (4 rows: 8192
-// x 4096 15.5 us against 18.0, 12288 x 4096 22.0 against 20.9, 14336 x 4096 26.0
+// Calls of the few-rows kernel: up to 8 rows, and up to 32 as long as the rows
+// that every workgroup reads (m k bytes) are not too long beside its 16 columns of
+// weights.  The bounds are where the two kernels cross, by N: with few columns the
+// tiled kernel's parts of k occupy more CUs; up to 4096 columns every workgroup
+// has a CU to itself; above, the second round on the CUs brings the crossing down,
+// the more so with two row blocks (17 rows and more), whose registers leave one
+// workgroup per CU.  us here / tiled, weights of layers in turn that no cache
+// holds (bytes m k in brackets):
+//   N 1000   16 x 11264 [180 K] 11.0 / 11.0, 16 x 14336 [229 K] 13.4 / 12.0
+//   N 1536   24 x 8192 [197 K] 10.4 / 10.6, 28 x 8192 [229 K] 11.0 / 10.6
+//   N 4096   20 x 14336 [287 K] 16.2 / 17.2, 24 x 14336 [344 K] 17.3 / 17.3, 32 x
+//            14336 [459 K] 19.5 / 17.3
+//   N 5120   20 x 4096 [82 K] 10.0 / 10.3, 32 x 4096 [131 K] 12.2 / 10.5; 12 x 8192
+//            [98 K] 13.7 / 14.1, 16 x 14336 [229 K] 25.2 / 19.1
+//   N 7168   24 x 4096 [98 K] 11.0 / 11.6, 24 x 14336 [344 K] 31.0 / 23.2; 16 x 8192
+//            [131 K] 16.2 / 16.6, 12 x 14336 [172 K] 23.6 / 23.0
+// 17 rows and more of 8192 columns and more: tiled (32 rows of 14336 x 4096: 21.7
+// here, 18.2 tiled).  Gated, from 2 rows on, not with many columns (4 rows: 8192 x
+// 4096 15.5 us against 18.0, 12288 x 4096 22.0 against 20.9, 14336 x 4096 26.0
 // against 23.6).
 static bool i8_few_rows(const I8Call &c) {
   if (c.gated) return c.m == 1 || (c.m <= 16 && c.n < 10000);
-  return c.m <= 8 || (c.m <= 32 && (c.m <= 16 || c.n < 8192) && c.m * c.k <= (c.n <= 1536 ? 200000 : 24 * 14336));
+  if (c.m <= 8 || c.m > 32) return c.m <= 8;
+  const int64_t read = c.m * c.k;
+  if (c.n <= 1536) return read <= 200000;
+  if (c.n <= 4096) return read <= 24 * 14336;
+  return c.m <= 16 ? read <= 32 * 4096 : c.n < 8192 && read <= 24 * 4096;
 }
 
 hipError_t launch_i8(const I8Call &c, hipStream_t s) {

@@ -185,3 +185,16 @@ def test_sizes_refuse_null_and_negative():
     out = ctypes.c_uint64()
     assert qg._lib.qg_ffn_gated_backward_workspace_size(-1, 8, 1, 0, ctypes.byref(out)) == qg.QG_ERR_INVALID_ARGUMENT
     assert qg._lib.qg_token_logprobs_workspace_size(1, 100, 33, ctypes.byref(out)) == qg.QG_ERR_UNSUPPORTED
+
+
+def test_described_choice_at_9_to_32_rows():
+    """Both sides of the measured crossings of the few-rows and the tiled kernel."""
+    def kernel(m, n, k):
+        return qg.describe_dispatch(bound(layer(n, k)), m).split()[0]
+
+    for m, n, k in ((16, 1000, 11264), (24, 1536, 8192), (24, 4096, 14336), (32, 4096, 8192), (20, 5120, 4096), (17, 7168, 4096),
+                    (16, 14336, 8192), (8, 14336, 28672)):
+        assert kernel(m, n, k) == "i8_rows", (m, n, k)
+    for m, n, k in ((16, 1000, 14336), (28, 1536, 8192), (28, 4096, 14336), (32, 5120, 4096), (17, 5120, 11264), (24, 7168, 14336),
+                    (16, 5120, 14336), (17, 8192, 4096), (33, 4096, 64)):
+        assert kernel(m, n, k) == "i8_tiled", (m, n, k)
