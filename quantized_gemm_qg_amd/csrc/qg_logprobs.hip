@@ -349,10 +349,15 @@ __global__ __launch_bounds__(T, SHARED ? 4 : 5) void logprobs_kernel(LogprobArgs
   const int vocab = (int)a.vocab;
   const float c2 = a.scale * kLog2e;
   const int parts = SHARED ? gridDim.x : 1, part = SHARED ? blockIdx.x : 0;
-  // no statistics are asked for, so no gradient reads the logits again: they are
-  // read past the caches (3391 x 38531 fp32 98 -> 90 us; with a gradient, 1021 x
-  // 100003 bf16, 119 -> 136 us)
-  const bool once = a.stats == nullptr;
+  // Logits that the last-level cache (256 MB) does not hold and that no gradient
+  // reads again (no statistics are asked for) are read past the caches: 2048 x
+  // 131072 bf16 (537 MB), written just before, 314 us for both against 336, 512 x
+  // 131072 fp32 (268 MB) 152 against 159.  Smaller ones are found there, as the
+  // head layer wrote them: past the caches 256 x 131072 bf16 (67 MB) 54.8 against
+  // 48.3, 4000 x 8192 49.4 against 42.5, 64 x 131072 23.3 against 22.0.  (A reader
+  // behind it costs large ones what they gain: 214 against 205; a gradient more,
+  // 1021 x 100003 bf16 136 against 119.)
+  const bool once = a.stats == nullptr && a.rows * a.vocab * (F32 ? 4 : 2) >= (256ll << 20);
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const uint8_t *lp = (const uint8_t *)a.logits + row * a.ldl * (F32 ? 4 : 2);
     // this workgroup's logits, in equal parts (a short last one would have no

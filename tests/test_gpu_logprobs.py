@@ -306,7 +306,7 @@ def test_forward_of_rows_that_four_units_a_thread_hold(kind):
 @pytest.mark.parametrize("rows,vocab,pad,shift", [(1, 5, 0, 0), (5, 64, 1, 1), (300, 9001, 0, 0), (1100, 4099, 5, 1), (1, 131072, 0, 0),
                                                   (3, 100003, 5, 1), (40, 131072, 0, 0), (40, 131072, 3, 3), (800, 17000, 0, 0)])
 def test_forward_without_statistics(rows, vocab, pad, shift, dtype):
-    """The same bits as with them (their rows are read past the caches)."""
+    """The same bits as with them."""
     print(f"logprobs without stats rows={rows} vocab={vocab} {dtype}", flush=True)
     l, tok = make("masked", rows, vocab, dtype, rows + vocab)
     d = place(l, dtype, pad, shift)
@@ -321,3 +321,32 @@ def test_forward_without_statistics(rows, vocab, pad, shift, dtype):
                           n["top_ids"] if top else None, n["top_logp"] if top else None, ws, wsb)
         for name in ("logp", "entropy", "rank") + (("top_ids", "top_logp") if top else ()):
             assert torch.equal(n[name], o[name]), name
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(520, 131072, torch.float32), (1030, 131073, torch.bfloat16), (9000, 16001, torch.bfloat16)])
+def test_logits_read_past_the_caches(rows, vocab, dtype):
+    """More than 256 MB of logits and no statistics: the same bits as with them."""
+    print(f"logprobs past the caches rows={rows} vocab={vocab} {dtype}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    l = torch.empty(rows, vocab + 3, dtype=dtype, device="cuda")
+    assert rows * vocab * l.element_size() > 256 << 20
+    l[:] = torch.randn(rows, vocab + 3, generator=gen, device="cuda")
+    d = l[:, :vocab]
+    d.vocab = vocab
+    tok = torch.randint(vocab, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    ltype = qg.O_F32 if dtype == torch.float32 else qg.O_BF16
+    o = forward(d, ltype, tok, 0.7, 20)
+    n = {name: torch.full_like(t, 7) for name, t in o.items()}
+    wsb = qg.token_logprobs_workspace_size(rows, vocab, 20)
+    ws = torch.zeros(max(wsb, 1), dtype=torch.uint8, device="cuda")
+    qg.token_logprobs(d, ltype, rows, vocab, vocab + 3, tok, 0.7, 20, n["logp"], n["entropy"], None, n["rank"], n["top_ids"],
+                      n["top_logp"], ws, wsb)
+    for name in ("logp", "entropy", "rank", "top_ids", "top_logp"):
+        assert torch.equal(n[name], o[name]), name
+    # and a few rows against 64 bits
+    some = torch.arange(0, rows, rows // 5)
+    logq, logp, ent, rank = reference(d[some.cuda()].cpu().float(), tok.cpu()[some], torch.tensor(0.7).item())
+    tol = tolerance(d[some.cuda()].cpu().float(), 0.7)
+    assert ((n["logp"].cpu().to(D)[some] - logp).abs() <= tol).all() and torch.equal(n["rank"].cpu().long()[some], rank)
+    assert ((n["entropy"].cpu().to(D)[some] - ent).abs() <= tol * (2 + math.log(vocab))).all()
+    assert torch.equal(n["top_ids"].cpu().long()[some], alternatives(d[some.cuda()].cpu().float(), 20))
