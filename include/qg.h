@@ -116,7 +116,7 @@ typedef enum {
   QG_A_MXFP4 = 2,
   QG_A_FP8_TOKEN = 3,
   QG_A_FP8_BLOCK = 4,
-  QG_A_INT8_TOKEN = 6 /* int8 with one fp32 scale per row (x_scales [rows]) */
+  QG_A_INT8_TOKEN = 6 /* int8 with one fp32 scale per row (x_scales [rows]); 5 is not assigned and refused */
 } qg_atype;
 typedef enum { QG_O_BF16 = 0, QG_O_F32 = 1 } qg_otype;
 /* Activation of a gated feed-forward block: v / (1 + e^-v), or
@@ -521,7 +521,8 @@ qg_status qg_gated_gemm(const qg_weight *w, const void *x, const void *x_scales,
  * and for training, in one kernel:
  *   g = x Wg^T, u = x Wu^T, h = act(g) u   (fp32, rounded once to bf16).
  *   x   device, bf16 [m][ldx]; w device, bf16 [2 * inter][ldw], the gate rows
- *       first; both 16-B aligned, ld >= k, ld % 8 == 0, ld <= 2^22, k % 8 == 0.
+ *       first; both 16-B aligned, ld >= k, ld % 8 == 0, ld <= 2^22, k % 8 == 0;
+ *       inter <= 2^24.
  *   h   device, bf16 [m][ldh], 16-B aligned, ldh >= inter.
  *   gu  device, [m][ldgu] of gu_type, 16-B aligned, ldgu >= 2 * inter, or NULL:
  *       g in columns 0 .. inter - 1 and u behind it, for the backward pass
@@ -538,7 +539,9 @@ qg_status qg_ffn_gated(const void *x, int64_t ldx, const void *w, int64_t ldw, i
 
 /* Backward pass of qg_ffn_gated: with dh the gradient of h,
  *   du = dh act(g), dg = dh u act'(g)      (fp32, rounded once to bf16; kept
- *       in two bf16 parts for dx up to 16 and for dw up to 32 tokens)
+ *       in two bf16 parts for dx up to 16 and for dw up to 32 tokens.  With more
+ *       tokens that rounding is in dx and dw, 1.7e-3 of their norm, whatever
+ *       dw_type is)
  *   dx = dg Wg + du Wu,  dw = [dg du]^T x  (summed in fp32, rounded once).
  *   x, w  as in the forward pass.  dh device, bf16 [m][lddh], lddh >= inter.
  *   dx    device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.

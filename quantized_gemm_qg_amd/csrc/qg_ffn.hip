@@ -7,12 +7,13 @@
 // [dg du] is rounded to bf16 once because the matrix cores take bf16 operands
 // (fp32 ones run at 1/16 of the rate): the rounding errors of its elements are
 // independent, so each gradient's relative error grows from the output
-// rounding's 1.7e-3 (2-norm) to sqrt(2) times that.  With few tokens single
+// rounding's 1.7e-3 (2-norm) to sqrt(2) times that, and an fp32 dW has 1.7e-3 from
+// it.  (Two parts for all tokens would double the products.)  With few tokens single
 // elements decide and nothing is bound by the matrix cores, so there [dg du] is
 // kept as the sum of two bf16 numbers (dx up to 16 tokens, dW up to 32: as far
 // as one tile or stage holds both parts).
-// 4096 tokens, 14336 x 4096: forward with pre-activations 801 us (1.20 PFLOP/s), the
-// elementwise pass 157, dx 724, dW 742.
+// 4096 tokens, 14336 x 4096: forward with pre-activations 794 us (1.21 PFLOP/s), the
+// elementwise pass 158, dx 725, dW 750.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"

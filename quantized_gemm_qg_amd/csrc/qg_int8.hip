@@ -16,8 +16,9 @@ namespace qg {
 // One row per workgroup, held in registers (VEC x 16 bytes per thread) between
 // its maximum and its codes, so it is read once; longer rows are read a second
 // time from L2.  The scale and the quotient are IEEE fp32 divisions, the code
-// the nearest integer, ties to even.  4096 x 4096: 50 MB in 13.6 us (10.0 at
-// the copy rate); a few rows: the launch and one read's latency.
+// the nearest integer, ties to even.  4096 x 4096: 50 MB in 13.4 us from memory
+// (10.0 at the copy's rate), 16384 rows 42.3 us (0.94 of it), 64 rows 2.9 us: a
+// launch of one round of rows and one read's latency, which only more rows hide.
 template <int THREADS, int VEC, bool LONG>
 __global__ __launch_bounds__(THREADS) void quantize_int8_kernel(const uint16_t *x, int64_t ldx, int64_t k, uint8_t *q,
                                                                 int64_t ldq, float *qs, int64_t rows) {
@@ -106,8 +107,8 @@ static MmArgs i8_args(const I8Call &c) {
   return a;
 }
 
-// Rows that the few-rows kernel quantizes for itself: one (14336 x 4096: 13.7 us,
-// 17.6 with a launch of its own for the quantization), or a few short ones
+// Rows that the few-rows kernel quantizes for itself: one (14336 x 4096: 3.9 us
+// less than with a launch of its own for the quantization), or a few short ones
 // (2 x 1024: 5.7 against 7.6 us; 2 x 4096: 10.6 against 8.5).
 bool i8_quantizes_in_kernel(int64_t m, int64_t k) {
   return m == 1 ? rows_pitch((int)k) <= 64 * 1024 : m <= 4 && m * k <= 2048;
@@ -125,7 +126,8 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
     return mm_dispatch<I8Cfg<true, 256, 256, 4, 2, 2, false>, I8Cfg<true, 192, 256, 4, 2, 2, false>,
                        I8Cfg<true, 128, 128, 4, 2, 2, true>, I8Cfg<true, 128, 128, 4, 2, 4, true>,
                        I8Cfg<true, 64, 128, 2, 4, 4, true>, I8Cfg<true, 32, 128, 1, 4, 4, true>>(a, budget, s, info);
-  // (224 columns: 14336 of them in 4096 rows are four whole rounds of the CUs)
+  // (224 columns, where the cost has fewer rounds of the CUs with them than with 256:
+  // 14336 of them in 4096 rows are four whole ones)
   return mm_dispatch<I8Cfg<false, 256, 256, 4, 2, 2, false>, I8Cfg<false, 256, 224, 4, 2, 2, false>,
                      I8Cfg<false, 192, 256, 4, 2, 2, false>, I8Cfg<false, 128, 128, 4, 2, 2, true>,
                      I8Cfg<false, 128, 128, 4, 2, 4, true>, I8Cfg<false, 64, 128, 2, 4, 4, true>,

@@ -28,9 +28,14 @@
 //
 // Many rows are bound by their bytes: 2048 x 131072 bf16 (537 MB) in 101 us
 // without alternatives and 114 us with 20 of them and a fifth of the tokens
-// masked.  One row of 131072 fp32 takes 11.4 us, a chain of latencies: 2.0 until
-// its logits are there, 3.4 for the alternatives and sums of a part, 0.7 to
-// publish them, 1.3 for the last workgroup to read the parts, 2.7 to join them.
+// masked.  Rows that are short, or a few hundred, are not: every chunk ends in the
+// chain that finds its alternatives before the next one is asked for, and a row a
+// little longer than a chunk has the chain twice (us without / with 20
+// alternatives, floor: 3963 x 4096 bf16 10.8 / 15.5, 6.4; 3963 x 4197 16.3 / 22.2,
+// 6.6; 1000 x 12000 11.2 / 14.7, 4.7; 2000 x 16000 19.7 / 31.3, 12.6; 256 x 131072
+// 21.7 / 29.7, 13.3).  One row of 131072 fp32 takes 11.4 us, a chain of latencies:
+// 2.0 until its logits are there, 3.4 for the alternatives and sums of a part, 0.7
+// to publish them, 1.3 for the last workgroup to read the parts, 2.7 to join them.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"

@@ -28,8 +28,9 @@
 //
 // Bounds and rates: large products by the matrix cores, which run into the power
 // limit (1.65-1.75 GHz; busy 65-72 % of the cycles in bf16, 55 % in int8): int8 4096
-// x 14336 x 4096 215 us (2.2 POP/s), bf16 4096 x 4096 x 28672 with one operand
-// transposed 724 us (1.33 PFLOP/s), with both 742 us.  128 x 128 tiles by LDS (96 KB
+// x 14336 x 4096 224 us (2.1 POP/s), bf16 4096 x 4096 x 28672 with one operand
+// transposed 725 us (1.33 PFLOP/s), with both 750 us.  (The int8 256 x 256 shapes
+// spill 14 to 20 registers, between the loop and the epilogue.)  128 x 128 tiles by LDS (96 KB
 // read and 32 KB written per stage, 1024 clocks for 512 of products), small
 // batches by the latency of their stages and of the join.
 //
@@ -540,8 +541,11 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
       const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * EL);
       uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * EL;
       if (col + PER <= a.n) {
-        // (a weight gradient is read once, much later: past the caches; the backward
-        // of one token through 14336 x 4096 124 -> 100 us, while the forward's
+        // (a weight gradient, of any size, is read once, much later: past the caches.
+        // Backward us through / past them, gradients in turn that no cache holds: 257
+        // tokens of 2817 x 1032 35.4 / 33.4 (11.6 MB bf16) and 37.0 / 35.3 (fp32), one
+        // of 4096 x 4096 44.1 / 43.0 and 62.9 / 58.0, of 14336 x 4096 126 / 106 and 171
+        // / 143; 257 of 4096 x 4096 75.6 / 76.6 and 86.3 / 89.9.  The forward's
         // outputs, read next, lose: 790 -> 810 us at 4096 tokens)
         if constexpr (C::AF == kCols)
           __builtin_nontemporal_store(v, (u32x4_any *)dst);

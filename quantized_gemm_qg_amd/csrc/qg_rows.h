@@ -6,14 +6,24 @@
 // 16 bytes per lane and load, all loads of a run in flight before its first
 // product, so nothing is staged and no barrier stands between loads.
 //
-// One token of 14336 x 4096: int8 12.7 us (4.6 TB/s of weights), int8 gated 20.8
-// us (5.6 TB/s), bf16 gated 43.2 us (5.4 TB/s); a copy reaches 5.1 TB/s.
+// One token of 14336 x 4096: int8 14.3 us from memory (4.1 TB/s of weights) and
+// 12.9 from the last-level cache (256 MB), int8 gated 20.8 us (5.6 TB/s), bf16
+// gated 43.2 us (5.4 TB/s); a copy reaches 5.1 TB/s.
 //
-// PAST (int8 weights from 64 MB on, which are no longer in the caches when their
-// layer's turn comes again): loads past the caches (one gated token of 14336 x 4096
-// 23.3 -> 21.7 us from memory, one of 8192 x 8192 ungated 15.9 -> 14.6; but 23 rows
-// of 4096 x 14336, which the caches hold, 18.3 -> 21.1).  Not bf16, whose lines take
-// two loads each (45.3 -> 48.2).
+// PAST (int8 weights of up to 16 rows, from 64 MB on): loads past the caches.  us
+// through the caches / past them, of layers in turn that no cache holds, and in
+// brackets of three layers in turn:
+//   1 row     8192 x 4096   10.1 / 9.6   [9.4 / 9.0]
+//             14336 x 4096  14.3 / 13.6  [12.9 / 12.9]
+//             28672 x 4096  23.9 / 21.8  [23.9 / 21.4], gated 23.0 / 21.1 [23.0 / 20.7]
+//   16 rows   8192 x 4096   9.6 / 9.3    [8.0 / 8.8]
+//             14336 x 4096  16.9 / 15.8  [13.1 / 15.1]
+//             28672 x 4096  30.6 / 29.0  [30.4 / 28.4]
+// What comes from memory gains 2 to 10 % at every size, what the last-level cache
+// holds loses up to 16 %.  From 64 MB on a few layers fill that cache; below,
+// whether they are found there is the program's, and the loads go through it.
+// Not 17 rows and more (23 rows of 4096 x 14336 17.1 / 16.5 [14.3 / 16.1]), nor
+// bf16, whose lines take two loads each (45.3 -> 48.2).
 //
 // FUSEQ (int8, the rows' codes fit in LDS): x is bf16 and every workgroup
 // quantizes it for itself while its first weights are on their way, which
