@@ -138,9 +138,8 @@ static hipError_t i8_tiled(const I8Call &c, hipStream_t s, MmInfo *info) {
 // that every workgroup reads (m k bytes) are not too long beside its 16 columns of
 // weights.  The bounds are where the two kernels cross, by N: with few columns the
 // tiled kernel's parts of k occupy more CUs; up to 4096 columns every workgroup
-// has a CU to itself; above, the second round on the CUs brings the crossing down,
-// the more so with two row blocks (17 rows and more), whose registers leave one
-// workgroup per CU.  us here / tiled, weights of layers in turn that no cache
+// has a CU to itself; above, some CUs have a second one and the others wait for
+// them, which brings the crossing down.  us here / tiled, weights of layers in turn that no cache
 // holds (bytes m k in brackets):
 //   N 1000   16 x 11264 [180 K] 11.0 / 11.0, 16 x 14336 [229 K] 13.4 / 12.0
 //   N 1536   24 x 8192 [197 K] 10.4 / 10.6, 28 x 8192 [229 K] 11.0 / 10.6
