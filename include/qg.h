@@ -601,6 +601,50 @@ qg_status qg_token_logprobs_backward(const void *logits, int32_t ltype, int64_t 
                                      const float *dlogp, const float *dentropy, void *dlogits, int64_t lddl,
                                      hipStream_t stream);
 
+/* Root-mean-square norm of rows with the residual's addition, to bf16 and / or
+ * to 8 bits with scales for the layer behind it:
+ *   s = x + residual, rounded to res_type (without residual and sum: s = x),
+ *   y[j] = s[j] w[j] / sqrt(mean_j(s[j]^2) + eps),
+ * in fp32, y and the codes each rounded once from there.
+ *   x        device, [rows][ldx] of x_type (QG_O_BF16 / QG_O_F32, a GEMM's output).
+ *   residual device, [rows][ldr] of res_type, or NULL.
+ *   sum      device, [rows][lds] of res_type, or NULL: s, for the next residual
+ *            and for the backward pass.  It may be x's or the residual's own
+ *            buffer (same pointer, stride and type).
+ *   weight   device, bf16 [k].  eps > 0.
+ *   y        device, bf16 [rows][ldy], or NULL.
+ *   q, q_scales, q_type  the codes of y and their scales, or NULL, NULL and
+ *            QG_A_BF16 (one of y and q is wanted): QG_A_INT8_TOKEN, QG_A_FP8_TOKEN,
+ *            QG_A_FP8_BLOCK or QG_A_MXFP8, layouts, scales and roundings as
+ *            qg_quantize_int8, qg_quantize_fp8 and qg_quantize_mxfp8 (fp32 scales
+ *            are at least 2^-126) but of the fp32 y; [rows][ldq] bytes.
+ * k % 8 == 0 (MXFP8: % 32), k <= 2^24; 16-B aligned rows (q: 8-B; a product that
+ * reads it wants 16).  Outputs other than sum overlap no input.  rows == 0 is a
+ * no-op.  A row with NaN, Inf or a mean square beyond fp32 gives unspecified
+ * values in that row.  Asynchronous on `stream`. */
+qg_status qg_rmsnorm(const void *x, int32_t x_type, int64_t ldx, const void *residual, int32_t res_type, int64_t ldr,
+                     void *sum, int64_t lds, const void *weight, float eps, int64_t rows, int64_t k, void *y,
+                     int64_t ldy, int32_t q_type, void *q, int64_t ldq, void *q_scales, hipStream_t stream);
+
+/* Backward pass of qg_rmsnorm: with s as the forward pass normed it (its sum, or x
+ * where there was none), r = 1 / sqrt(mean(s^2) + eps), g = dy w,
+ *   dx = r (g - s r^2 mean_j(g s)) + dsum,  dw = sum over the rows of dy s r
+ * (fp32, each rounded once).  dx is the gradient of x and of the residual alike.
+ *   s    device, [rows][lds] of s_type.  dy device, bf16 [rows][lddy].
+ *   dsum device, [rows][ldds] of s_type: the gradient that reaches s past the
+ *        norm, or NULL.
+ *   dx   device, [rows][lddx] of s_type, or NULL; it may be dsum's own buffer.
+ *   dw   device, [k] of dw_type, 16-B aligned, or NULL; overwritten (rows == 0:
+ *        zeros).
+ *   ws   qg_rmsnorm_backward_workspace_size bytes, 256-B aligned, any contents;
+ *        NULL without dw.
+ * Sums over the rows are in a fixed order.  Alignments and limits as above. */
+qg_status qg_rmsnorm_backward_workspace_size(int64_t rows, int64_t k, uint64_t *bytes);
+qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const void *weight, float eps, int64_t rows,
+                              int64_t k, const void *dy, int64_t lddy, const void *dsum, int64_t ldds, void *dx,
+                              int64_t lddx, void *dw, int32_t dw_type, void *ws, uint64_t ws_bytes,
+                              hipStream_t stream);
+
 /* Measurement utilities, used for roofline calibration and cold-cache timing.
  * qg_stream_read reads `bytes` (a multiple of 16; src 16-B aligned, device)
  * with 128-bit loads and folds them into `sink` (device, at least 16 KiB, any

@@ -38,6 +38,7 @@ EXPORTS = (
     "qg_quantize_int8", "qg_gated_gemm_workspace_size", "qg_gated_gemm",
     "qg_ffn_gated_workspace_size", "qg_ffn_gated", "qg_ffn_gated_backward_workspace_size", "qg_ffn_gated_backward",
     "qg_token_logprobs_workspace_size", "qg_token_logprobs", "qg_token_logprobs_backward",
+    "qg_rmsnorm", "qg_rmsnorm_backward_workspace_size", "qg_rmsnorm_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X = 1, 2
@@ -123,6 +124,9 @@ def _load():
         "qg_token_logprobs_workspace_size": (I32, [I64, I64, I32, ctypes.POINTER(U64)]),
         "qg_token_logprobs": (I32, [P, I32, I64, I64, I64, P, ctypes.c_float, I32, P, P, P, P, P, P, P, U64, P]),
         "qg_token_logprobs_backward": (I32, [P, I32, I64, I64, I64, P, ctypes.c_float, P, P, P, P, P, I64, P]),
+        "qg_rmsnorm": (I32, [P, I32, I64, P, I32, I64, P, I64, P, ctypes.c_float, I64, I64, P, I64, I32, P, I64, P, P]),
+        "qg_rmsnorm_backward_workspace_size": (I32, [I64, I64, ctypes.POINTER(U64)]),
+        "qg_rmsnorm_backward": (I32, [P, I32, I64, P, ctypes.c_float, I64, I64, P, I64, P, I64, P, I64, P, I32, P, U64, P]),
         "qg_autotune_reset": (None, []),
         "qg_set_override": (I32, [ctypes.c_char_p, ctypes.c_char_p]),
         "qg_clear_overrides": (None, []),
@@ -380,6 +384,27 @@ def token_logprobs_backward(logits, ltype: int, rows: int, vocab: int, ldl: int,
     _check(_lib.qg_token_logprobs_backward(_ptr(logits), ltype, rows, vocab, ldl, _ptr(tokens), scale, _ptr(stats),
                                            _ptr(entropy), _ptr(dlogp), _ptr(dentropy), _ptr(dlogits), lddl,
                                            _stream(stream)), "qg_token_logprobs_backward")
+
+
+def rmsnorm(x, x_type: int, ldx: int, weight, eps: float, rows: int, k: int, residual=None, res_type: int = O_BF16,
+            ldr: int = 0, sum=None, lds: int = 0, y=None, ldy: int = 0, q_type: int = A_BF16, q=None, ldq: int = 0,
+            q_scales=None, stream=None) -> None:
+    """s = x + residual (kept in sum), y = s w / sqrt(mean(s^2) + eps) as bf16 (y) and / or 8-bit codes (q, q_scales)
+    of q_type; outputs that are None are not written."""
+    _check(_lib.qg_rmsnorm(_ptr(x), x_type, ldx, _ptr(residual), res_type, ldr, _ptr(sum), lds, _ptr(weight), eps, rows, k,
+                           _ptr(y), ldy, q_type, _ptr(q), ldq, _ptr(q_scales), _stream(stream)), "qg_rmsnorm")
+
+
+def rmsnorm_backward_workspace_size(rows: int, k: int) -> int:
+    return _size(_lib.qg_rmsnorm_backward_workspace_size, "qg_rmsnorm_backward_workspace_size", rows, k)
+
+
+def rmsnorm_backward(s, s_type: int, lds: int, weight, eps: float, rows: int, k: int, dy, lddy: int, dx, lddx: int, dw,
+                     dw_type: int, ws=None, ws_bytes: int = 0, dsum=None, ldds: int = 0, stream=None) -> None:
+    """dx (of x and of the residual) and dw of rmsnorm (each may be None) from dy and dsum, the gradient of the sum."""
+    _check(_lib.qg_rmsnorm_backward(_ptr(s), s_type, lds, _ptr(weight), eps, rows, k, _ptr(dy), lddy, _ptr(dsum), ldds,
+                                    _ptr(dx), lddx, _ptr(dw), dw_type, _ptr(ws), ws_bytes, _stream(stream)),
+           "qg_rmsnorm_backward")
 
 
 def silu_mul(gu, gu_type: int, rows: int, inter: int, ldgu: int, h, h_type: int, ldh: int,

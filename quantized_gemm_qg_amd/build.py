@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqg.so")
 SOURCES = ["qg_api.cpp", "qg_ops.cpp", "qg_repack.cpp", "qg_kernels.hip", "qg_formats.hip", "qg_tiled.hip",
-           "qg_tiled_a16.hip", "qg_act.hip", "qg_int8.hip", "qg_ffn.hip", "qg_logprobs.hip"]
+           "qg_tiled_a16.hip", "qg_act.hip", "qg_int8.hip", "qg_ffn.hip", "qg_logprobs.hip", "qg_layer.cpp",
+           "qg_norm.hip"]
 ARCH = os.environ.get("QG_OFFLOAD_ARCH", "gfx950")
 
 

@@ -1638,7 +1638,6 @@ extern "C" qg_status qg_stream_copy(void *dst, const void *src, uint64_t bytes,
   return hip_status(launch_stream_copy(dst, src, bytes, stream));
 }
 
-static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 extern "C" qg_status qg_quantize_mxfp8(const void *x, int64_t rows, int64_t k, int64_t ldx, void *q,
                                        int64_t ldq, void *q_scales, hipStream_t stream) {

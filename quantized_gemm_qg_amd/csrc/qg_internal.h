@@ -188,6 +188,19 @@ inline qg_status hip_status(hipError_t e) {
   return QG_ERR_HIP;
 }
 
+// Argument checks that the entry points share.
+inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline int el_of(int otype) { return otype == QG_O_F32 ? 4 : 2; }
+inline bool out_type(int t) { return t == QG_O_BF16 || t == QG_O_F32; }
+
+// Checks a workspace of `need` bytes (0: none).
+inline qg_status ws_check(uint64_t need, const void *ws, uint64_t ws_bytes) {
+  if (need == 0) return QG_OK;
+  if (!ws) return QG_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
+  return aligned(ws, 256) ? QG_OK : QG_ERR_ALIGNMENT;
+}
+
 // Checks a bound weight against its descriptor; fills the layout.
 qg_status check_weight(const qg_weight *w, Layout *L);
 
@@ -419,6 +432,42 @@ struct LogprobArgs {
 uint64_t logprobs_ws_bytes(int64_t rows, int64_t vocab, int top);
 hipError_t launch_logprobs(const LogprobArgs &a, void *ws, hipStream_t s);
 hipError_t launch_logprobs_backward(const LogprobArgs &a, hipStream_t s);
+// root-mean-square norm (qg_norm.hip); strides in elements, sizes checked by the caller
+struct NormArgs {
+  const void *x;
+  int64_t ldx;
+  const void *res;
+  int64_t ldr;
+  void *sum;
+  int64_t lds;
+  const void *w;
+  float eps;
+  int64_t rows, k;
+  uint16_t *y;
+  int64_t ldy;
+  int32_t q_type;  // QG_A_BF16: no codes
+  uint8_t *q;
+  int64_t ldq;
+  void *qs;
+};
+struct NormBackArgs {
+  const void *s;
+  int64_t lds;
+  const void *w;
+  float eps;
+  int64_t rows, k;
+  const uint16_t *dy;
+  int64_t lddy;
+  const void *dsum;
+  int64_t ldds;
+  void *dx;
+  int64_t lddx;
+  float *partial;  // [rmsnorm_back_parts][k], NULL: no dw
+};
+// res: the type of the residual and the sum (0: neither, 1: bf16, 2: fp32)
+hipError_t launch_rmsnorm(const NormArgs &a, bool x_f32, int res, hipStream_t s);
+int64_t rmsnorm_back_parts(int64_t rows, int64_t k);
+hipError_t launch_rmsnorm_backward(const NormBackArgs &a, bool s_f32, void *dw, bool dw_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

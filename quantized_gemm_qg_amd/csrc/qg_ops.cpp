@@ -10,18 +10,6 @@
 
 namespace qg {
 
-static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-static int el_of(int otype) { return otype == QG_O_F32 ? 4 : 2; }
-static bool out_type(int t) { return t == QG_O_BF16 || t == QG_O_F32; }
-
-// Checks a workspace of `need` bytes (0: none).
-static qg_status ws_check(uint64_t need, const void *ws, uint64_t ws_bytes) {
-  if (need == 0) return QG_OK;
-  if (!ws) return QG_ERR_INVALID_ARGUMENT;
-  if (ws_bytes < need) return QG_ERR_BUFFER_TOO_SMALL;
-  return aligned(ws, 256) ? QG_OK : QG_ERR_ALIGNMENT;
-}
-
 // The tiled products address a tile's rows with 32-bit offsets from a 64-bit
 // base: 256 rows of this pitch stay below 2 GiB.  (The gradient of the
 // pre-activations has rows of up to 64 MiB, of which 64 are within reach: shapes

@@ -32,25 +32,9 @@
 #pragma once
 
 #include "qg_mm.h"
+#include "qg_quant.h"
 
 namespace qg {
-
-// scale of a row with largest magnitude `most`; code of v, IEEE division and
-// ties to even
-__device__ __forceinline__ float i8_scale(float most) { return most > 0.f ? most / 127.f : 1.f; }
-__device__ __forceinline__ uint32_t i8_codes4(const float *v, float s) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)rintf(v[i] / s) & 255u) << (8 * i);
-  return w;
-}
-__device__ __forceinline__ void unpack8(const u32x4 &w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
 
 // Bytes of a row's codes in LDS: whole blocks (what lies behind K meets zero
 // weights), and 16 more so that rows start on different banks.
