@@ -645,6 +645,46 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
                               int64_t lddx, void *dw, int32_t dw_type, void *ws, uint64_t ws_bytes,
                               hipStream_t stream);
 
+/* Softmax cross entropy of hidden states against a head's weights, for large
+ * vocabularies: the logits exist tile by tile and are never in memory.  With
+ * z = scale x W^T (fp32 sums of bf16 products),
+ *   lse[r] = log sum_v exp(z[r][v]),  loss[r] = lse[r] - z[r][t_r].
+ *   x       device, bf16 [m][ldx]; w device, bf16 [vocab][ldw]; 16-B aligned, ld
+ *           >= k, ld % 8 == 0, ld <= 2^22, k % 8 == 0; vocab <= 2^24.
+ *   targets device int32 [m]; a target outside 0 .. vocab - 1 is ignored: loss 0
+ *           and no gradient (its lse is that of its logits).  NULL without loss.
+ *   scale   > 0: 1, or one over the temperature.
+ *   loss, lse  device fp32 [m], one of them may be NULL; lse is for the backward
+ *           pass.
+ *   ws      qg_linear_xent_workspace_size bytes, 256-B aligned, zero-filled once
+ *           (its first 64 KiB suffice).
+ * NaN in a row of x, or an infinite logit, gives NaN in that row alone.  m == 0 is
+ * a no-op.  Sums are in a fixed order.  Asynchronous on `stream`. */
+qg_status qg_linear_xent_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);
+qg_status qg_linear_xent(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k, int64_t vocab,
+                         const int32_t *targets, float scale, float *loss, float *lse, void *ws, uint64_t ws_bytes,
+                         hipStream_t stream);
+
+/* Gradients of qg_linear_xent from that of the losses (dloss, fp32 [m]), with lse
+ * of the forward pass on the same x, w and scale:
+ *   d[r][v] = dloss[r] (exp(z[r][v] - lse[r]) - 1{v = t_r}),
+ *   dx = scale d W,  dw = scale d^T x.
+ * The vocabulary goes in pieces: d exists for one piece, in bf16 (two bf16 parts
+ * for dx up to 16 and for dw up to 32 tokens; with more that rounding, 1.7e-3 of
+ * the norm, is in dx and dw whatever dw_type is), relative to the largest |dloss|.
+ *   dx   device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.
+ *   dw   device, [vocab][lddw] of dw_type, 16-B aligned, lddw >= k, or NULL; it is
+ *        overwritten; m == 0 fills it with zeros.
+ *   ws   qg_linear_xent_backward_workspace_size bytes (some 130 MB and 4 m k, or
+ *        16384 m + 4 m k where that is more), 256-B aligned, zero-filled once.
+ * An ignored row's dx is 0, and it adds nothing to dw as long as its x is finite.
+ * Asynchronous on `stream`. */
+qg_status qg_linear_xent_backward_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);
+qg_status qg_linear_xent_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k,
+                                  int64_t vocab, const int32_t *targets, float scale, const float *lse,
+                                  const float *dloss, void *dx, int64_t lddx, void *dw, int32_t dw_type, int64_t lddw,
+                                  void *ws, uint64_t ws_bytes, hipStream_t stream);
+
 /* Measurement utilities, used for roofline calibration and cold-cache timing.
  * qg_stream_read reads `bytes` (a multiple of 16; src 16-B aligned, device)
  * with 128-bit loads and folds them into `sink` (device, at least 16 KiB, any

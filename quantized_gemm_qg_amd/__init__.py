@@ -39,6 +39,7 @@ EXPORTS = (
     "qg_ffn_gated_workspace_size", "qg_ffn_gated", "qg_ffn_gated_backward_workspace_size", "qg_ffn_gated_backward",
     "qg_token_logprobs_workspace_size", "qg_token_logprobs", "qg_token_logprobs_backward",
     "qg_rmsnorm", "qg_rmsnorm_backward_workspace_size", "qg_rmsnorm_backward",
+    "qg_linear_xent_workspace_size", "qg_linear_xent", "qg_linear_xent_backward_workspace_size", "qg_linear_xent_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X = 1, 2
@@ -127,6 +128,11 @@ def _load():
         "qg_rmsnorm": (I32, [P, I32, I64, P, I32, I64, P, I64, P, ctypes.c_float, I64, I64, P, I64, I32, P, I64, P, P]),
         "qg_rmsnorm_backward_workspace_size": (I32, [I64, I64, ctypes.POINTER(U64)]),
         "qg_rmsnorm_backward": (I32, [P, I32, I64, P, ctypes.c_float, I64, I64, P, I64, P, I64, P, I64, P, I32, P, U64, P]),
+        "qg_linear_xent_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
+        "qg_linear_xent": (I32, [P, I64, P, I64, I64, I64, I64, P, ctypes.c_float, P, P, P, U64, P]),
+        "qg_linear_xent_backward_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
+        "qg_linear_xent_backward": (I32, [P, I64, P, I64, I64, I64, I64, P, ctypes.c_float, P, P, P, I64, P, I32, I64, P, U64,
+                                          P]),
         "qg_autotune_reset": (None, []),
         "qg_set_override": (I32, [ctypes.c_char_p, ctypes.c_char_p]),
         "qg_clear_overrides": (None, []),
@@ -405,6 +411,30 @@ def rmsnorm_backward(s, s_type: int, lds: int, weight, eps: float, rows: int, k:
     _check(_lib.qg_rmsnorm_backward(_ptr(s), s_type, lds, _ptr(weight), eps, rows, k, _ptr(dy), lddy, _ptr(dsum), ldds,
                                     _ptr(dx), lddx, _ptr(dw), dw_type, _ptr(ws), ws_bytes, _stream(stream)),
            "qg_rmsnorm_backward")
+
+
+def linear_xent_workspace_size(m: int, k: int, vocab: int) -> int:
+    return _size(_lib.qg_linear_xent_workspace_size, "qg_linear_xent_workspace_size", m, k, vocab)
+
+
+def linear_xent(x, ldx: int, w, ldw: int, m: int, k: int, vocab: int, targets, scale: float, loss, lse, ws, ws_bytes: int,
+                stream=None) -> None:
+    """Cross entropy of bf16 x [m][ldx] against a head's w [vocab][ldw] without logits in memory: loss and log-sum [m]
+    (either may be None); targets outside the vocabulary are ignored."""
+    _check(_lib.qg_linear_xent(_ptr(x), ldx, _ptr(w), ldw, m, k, vocab, _ptr(targets), scale, _ptr(loss), _ptr(lse), _ptr(ws),
+                               ws_bytes, _stream(stream)), "qg_linear_xent")
+
+
+def linear_xent_backward_workspace_size(m: int, k: int, vocab: int) -> int:
+    return _size(_lib.qg_linear_xent_backward_workspace_size, "qg_linear_xent_backward_workspace_size", m, k, vocab)
+
+
+def linear_xent_backward(x, ldx: int, w, ldw: int, m: int, k: int, vocab: int, targets, scale: float, lse, dloss, dx, lddx: int,
+                         dw, dw_type: int, lddw: int, ws, ws_bytes: int, stream=None) -> None:
+    """dx and dw (each may be None) of linear_xent from dloss [m] and the forward pass's lse."""
+    _check(_lib.qg_linear_xent_backward(_ptr(x), ldx, _ptr(w), ldw, m, k, vocab, _ptr(targets), scale, _ptr(lse), _ptr(dloss),
+                                        _ptr(dx), lddx, _ptr(dw), dw_type, lddw, _ptr(ws), ws_bytes, _stream(stream)),
+           "qg_linear_xent_backward")
 
 
 def silu_mul(gu, gu_type: int, rows: int, inter: int, ldgu: int, h, h_type: int, ldh: int,

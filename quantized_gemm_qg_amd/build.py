@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqg.so")
 SOURCES = ["qg_api.cpp", "qg_ops.cpp", "qg_repack.cpp", "qg_kernels.hip", "qg_formats.hip", "qg_tiled.hip",
            "qg_tiled_a16.hip", "qg_act.hip", "qg_int8.hip", "qg_ffn.hip", "qg_logprobs.hip", "qg_layer.cpp",
-           "qg_norm.hip"]
+           "qg_norm.hip", "qg_xent.hip"]
 ARCH = os.environ.get("QG_OFFLOAD_ARCH", "gfx950")
 
 
@@ -45,7 +45,7 @@ def _flags():
 # (the integer formats' feed fp32 FMAs right away); left to its heuristics the
 # compiler puts them in AGPRs and copies them back.
 VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA = {"qg_tiled_a16.hip": VGPR_MFMA, "qg_int8.hip": VGPR_MFMA, "qg_ffn.hip": VGPR_MFMA}
+EXTRA = {"qg_tiled_a16.hip": VGPR_MFMA, "qg_int8.hip": VGPR_MFMA, "qg_ffn.hip": VGPR_MFMA, "qg_xent.hip": VGPR_MFMA}
 
 
 def _compile(src: str, verbose: bool) -> str:

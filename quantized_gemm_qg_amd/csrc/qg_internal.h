@@ -201,6 +201,14 @@ inline qg_status ws_check(uint64_t need, const void *ws, uint64_t ws_bytes) {
   return aligned(ws, 256) ? QG_OK : QG_ERR_ALIGNMENT;
 }
 
+// The tiled products address a tile's rows with 32-bit offsets from a 64-bit
+// base: 256 rows of this pitch stay below 2 GiB.  (The gradient of the gated
+// block's pre-activations has rows of up to 64 MiB, of which 64 are within reach:
+// shapes of more rows are left out where theirs are not.)
+constexpr int64_t kMaxPitchBytes = 1 << 23;
+// Tiles are numbered in 32 bits (the smallest tile is 32 x 64 outputs).
+inline bool tiles_fit(int64_t m, int64_t n) { return ((m + 31) / 32) * ((n + 63) / 64) < (1ll << 31) - 8; }
+
 // Checks a bound weight against its descriptor; fills the layout.
 qg_status check_weight(const qg_weight *w, Layout *L);
 
@@ -468,6 +476,33 @@ struct NormBackArgs {
 hipError_t launch_rmsnorm(const NormArgs &a, bool x_f32, int res, hipStream_t s);
 int64_t rmsnorm_back_parts(int64_t rows, int64_t k);
 hipError_t launch_rmsnorm_backward(const NormBackArgs &a, bool s_f32, void *dw, bool dw_f32, hipStream_t s);
+// cross entropy of a head (qg_xent.hip); strides in elements
+struct XentCall {
+  const void *x;
+  int64_t ldx;
+  const void *w;
+  int64_t ldw;
+  int64_t m, k, vocab;
+  const int32_t *targets;
+  float scale;
+  float *loss, *lse;
+  uint32_t *counters;  // split-K counters and partial tiles
+  void *partials;
+  float *stats, *at_target;  // forward: [tiles of columns][m][2], [m]
+  float *weight, *alpha;     // backward: [m], [1]
+  void *d;                   // backward: bf16 [xent_d_rows][ldd], one piece
+  int64_t ldd;
+};
+int64_t xent_d_rows(int64_t m);
+int64_t xent_piece(int64_t m, int64_t vocab);
+// info: NULL, or nothing is launched and the choice reported
+hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info = nullptr);
+hipError_t launch_xent_weights(const XentCall &c, const float *dloss, hipStream_t s);
+hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info = nullptr);
+hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, const float *add, int64_t ldadd, void *out,
+                          int out_type, int64_t ldout, hipStream_t s, MmInfo *info = nullptr);
+hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, void *dw, int dw_type, int64_t lddw,
+                          hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

@@ -82,3 +82,160 @@ extern "C" qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t 
   const NormBackArgs a{s, lds, weight, eps, rows, k, (const uint16_t *)dy, lddy, dsum, ldds, dx, lddx, dw ? (float *)ws : nullptr};
   return hip_status(launch_rmsnorm_backward(a, s_type == QG_O_F32, dw, dw_type == QG_O_F32, stream));
 }
+
+namespace qg {
+
+// Forward workspace: [split-K counters][partial tiles][statistics of the
+// tiles][the targets' logits].
+struct XentSpace {
+  uint64_t partials = 0, stats = 0, at_target = 0;  // bytes
+  uint64_t total() const { return kSplitCounterBytes + partials + stats + at_target; }
+};
+// Backward: [split-K counters][partial tiles][row weights][alpha][d of a
+// piece][dx in fp32, where there are several pieces].
+struct XentBackSpace {
+  int64_t piece = 0;
+  uint64_t partials = 0, weight = 0, d = 0, dx = 0;
+  static constexpr uint64_t alpha = 256;
+  uint64_t total() const { return kSplitCounterBytes + partials + weight + alpha + d + dx; }
+};
+
+static bool xent_in_range(int64_t m, int64_t k, int64_t vocab) {
+  return m <= (1ll << 30) && k <= (1 << 22) && vocab <= (1 << 24) && tiles_fit(m, vocab) && tiles_fit(m, k) &&
+         tiles_fit(vocab, k);
+}
+
+static XentSpace xent_space(const XentCall &c) {
+  MmInfo i;
+  (void)launch_xent(c, nullptr, &i);
+  XentSpace sp;
+  sp.partials = align_up(i.bytes, 256);
+  sp.stats = align_up((uint64_t)((c.vocab + i.bn - 1) / i.bn) * c.m * 8, 256);
+  sp.at_target = align_up((uint64_t)c.m * 4, 256);
+  return sp;
+}
+
+static XentBackSpace xent_back_space(const XentCall &c) {
+  XentBackSpace sp;
+  sp.piece = xent_piece(c.m, c.vocab);
+  // the last piece may be shorter, and its products split otherwise
+  const int64_t last = c.vocab - (c.vocab - 1) / sp.piece * sp.piece;
+  for (int64_t columns : {std::min(sp.piece, c.vocab), last}) {
+    MmInfo i;
+    (void)launch_xent_d(c, 0, columns, nullptr, &i);
+    sp.partials = std::max(sp.partials, i.bytes);
+    (void)launch_xent_dx(c, 0, columns, nullptr, 0, nullptr, 0, 0, nullptr, &i);
+    sp.partials = std::max(sp.partials, i.bytes);
+    (void)launch_xent_dw(c, 0, columns, nullptr, 0, 0, nullptr, &i);
+    sp.partials = std::max(sp.partials, i.bytes);
+  }
+  sp.partials = align_up(sp.partials, 256);
+  sp.weight = align_up((uint64_t)c.m * 4, 256);
+  sp.d = align_up((uint64_t)xent_d_rows(c.m) * sp.piece * 2, 256);
+  if (sp.piece < c.vocab) sp.dx = align_up((uint64_t)c.m * c.k * 4, 256);
+  return sp;
+}
+
+// Checks that the two directions of the cross entropy share.
+static qg_status xent_check(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k, int64_t vocab,
+                            const int32_t *targets, float scale) {
+  if (m < 0 || k < 0 || vocab < 0 || !std::isfinite(scale) || !(scale > 0.f)) return QG_ERR_INVALID_ARGUMENT;
+  if (k == 0 || k % 8 != 0 || vocab == 0) return QG_ERR_SHAPE;
+  if (!xent_in_range(m, k, vocab) || 2 * ldx > kMaxPitchBytes || 2 * ldw > kMaxPitchBytes) return QG_ERR_UNSUPPORTED;
+  if (m > 0 && (!x || !w)) return QG_ERR_INVALID_ARGUMENT;
+  QG_TRY(matrix_check(x, ldx, k, 2));
+  QG_TRY(matrix_check(w, ldw, k, 2));
+  return aligned(targets, 4) ? QG_OK : QG_ERR_ALIGNMENT;
+}
+
+static XentCall xent_call(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k, int64_t vocab,
+                          const int32_t *targets, float scale) {
+  XentCall c = {};
+  c.x = x;
+  c.ldx = ldx;
+  c.w = w;
+  c.ldw = ldw;
+  c.m = m;
+  c.k = k;
+  c.vocab = vocab;
+  c.targets = targets;
+  c.scale = scale;
+  return c;
+}
+
+// Bytes of either workspace; 0 for sizes that the calls refuse or that need none.
+static qg_status xent_bytes(int64_t m, int64_t k, int64_t vocab, bool backward, uint64_t *bytes) {
+  if (!bytes || m < 0 || k < 0 || vocab < 0) return QG_ERR_INVALID_ARGUMENT;
+  const XentCall c = xent_call(nullptr, k, nullptr, k, m, k, vocab, nullptr, 1.f);
+  const bool some = m > 0 && k > 0 && vocab > 0 && xent_in_range(m, k, vocab);
+  *bytes = !some ? 0 : backward ? xent_back_space(c).total() : xent_space(c).total();
+  return QG_OK;
+}
+
+}  // namespace qg
+
+extern "C" qg_status qg_linear_xent_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes) {
+  return xent_bytes(m, k, vocab, false, bytes);
+}
+
+extern "C" qg_status qg_linear_xent(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k,
+                                    int64_t vocab, const int32_t *targets, float scale, float *loss, float *lse,
+                                    void *ws, uint64_t ws_bytes, hipStream_t stream) {
+  QG_TRY(xent_check(x, ldx, w, ldw, m, k, vocab, targets, scale));
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return QG_ERR_ALIGNMENT;
+  if (m == 0) return QG_OK;
+  if ((!loss && !lse) || (loss && !targets)) return QG_ERR_INVALID_ARGUMENT;
+  XentCall c = xent_call(x, ldx, w, ldw, m, k, vocab, targets, scale);
+  const XentSpace sp = xent_space(c);
+  QG_TRY(ws_check(sp.total(), ws, ws_bytes));
+  c.loss = loss;
+  c.lse = lse;
+  uint8_t *p = (uint8_t *)ws;
+  c.counters = (uint32_t *)p;
+  c.partials = p += kSplitCounterBytes;
+  c.stats = (float *)(p += sp.partials);
+  c.at_target = (float *)(p + sp.stats);
+  return hip_status(launch_xent(c, stream));
+}
+
+extern "C" qg_status qg_linear_xent_backward_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes) {
+  return xent_bytes(m, k, vocab, true, bytes);
+}
+
+extern "C" qg_status qg_linear_xent_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k,
+                                             int64_t vocab, const int32_t *targets, float scale, const float *lse,
+                                             const float *dloss, void *dx, int64_t lddx, void *dw, int32_t dw_type,
+                                             int64_t lddw, void *ws, uint64_t ws_bytes, hipStream_t stream) {
+  QG_TRY(xent_check(x, ldx, w, ldw, m, k, vocab, targets, scale));
+  if (dw && !out_type(dw_type)) return QG_ERR_INVALID_ARGUMENT;
+  if ((dx && lddx < k) || (dw && lddw < k)) return QG_ERR_SHAPE;
+  if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16)) return QG_ERR_ALIGNMENT;
+  if (m == 0)  // a sum over no tokens
+    return dw ? hip_status(launch_ffn_zero(dw, lddw * el_of(dw_type), k * el_of(dw_type), vocab, stream)) : QG_OK;
+  if (!targets || !lse || !dloss) return QG_ERR_INVALID_ARGUMENT;
+  if (!dx && !dw) return QG_OK;
+  XentCall c = xent_call(x, ldx, w, ldw, m, k, vocab, targets, scale);
+  const XentBackSpace sp = xent_back_space(c);
+  QG_TRY(ws_check(sp.total(), ws, ws_bytes));
+  c.lse = const_cast<float *>(lse);
+  uint8_t *p = (uint8_t *)ws;
+  c.counters = (uint32_t *)p;
+  c.partials = p += kSplitCounterBytes;
+  c.weight = (float *)(p += sp.partials);
+  c.alpha = (float *)(p += sp.weight);
+  c.d = p += sp.alpha;
+  c.ldd = sp.piece;
+  float *sum = (float *)(p + sp.d);
+  hipError_t e = launch_xent_weights(c, dloss, stream);
+  for (int64_t first = 0; e == hipSuccess && first < vocab; first += sp.piece) {
+    const int64_t columns = std::min(sp.piece, vocab - first);
+    e = launch_xent_d(c, first, columns, stream);
+    const float *add = first > 0 ? sum : nullptr;
+    if (e == hipSuccess && dx && first + columns < vocab)
+      e = launch_xent_dx(c, first, columns, add, k, sum, QG_O_F32, k, stream);
+    else if (e == hipSuccess && dx)
+      e = launch_xent_dx(c, first, columns, add, k, dx, QG_O_BF16, lddx, stream);
+    if (e == hipSuccess && dw) e = launch_xent_dw(c, first, columns, dw, dw_type, lddw, stream);
+  }
+  return hip_status(e);
+}

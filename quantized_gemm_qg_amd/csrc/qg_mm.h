@@ -103,7 +103,22 @@ struct MmArgs {
   int32_t splits, per;
   uint32_t *counters;
   uint64_t *partials;
+  // cross entropy of a head (kXentStats, kXentGrad): y's columns are the logits of
+  // tokens first_token ..; kXentStats leaves the largest logit and the sum of
+  // exponentials of every row and tile in stats [tile][m] and the target's logit
+  // in at_target; kXentGrad writes row_weight (softmax - target)
+  const int32_t *targets;
+  int32_t first_token;
+  float scale;
+  float *stats, *at_target;
+  const float *lse, *row_weight;
+  // kScaled: y = alpha[0] times the product, plus `add` (fp32 [m][ldadd]) where given
+  const float *alpha, *add;
+  int64_t ldadd;
 };
+
+// What is done with a tile's sums besides storing them.
+enum { kPlain = 0, kXentStats = 1, kXentGrad = 2, kScaled = 3 };
 
 // Partial tiles of a call take at most this much.
 constexpr uint64_t kMmPartialBytes = 48u << 20;
@@ -112,8 +127,10 @@ constexpr uint64_t kMmPartialBytes = 48u << 20;
 static __device__ const uint32_t mm_zeros[4] = {0u, 0u, 0u, 0u};
 
 // SPLIT: the tile's k may be shared by several workgroups.
-template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, int WN_, int ST_, bool SPLIT_>
+template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, int WN_, int ST_, bool SPLIT_,
+          int EPI_ = kPlain>
 struct MmCfg {
+  static constexpr int EPI = EPI_;
   static constexpr bool I8 = I8_, GATED = GATED_;
   static constexpr bool SPLIT = SPLIT_;
   static constexpr int AF = AF_, BF = BF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = 128, ST = ST_;
@@ -136,6 +153,7 @@ struct MmCfg {
   static_assert(AF != kCols || BM >= 128, "column units for the swizzle");
   static_assert(BF != kCols || BN >= 128, "column units for the swizzle");
   static_assert(LDS <= 160 * 1024 && ST >= 2 && ST <= 4, "LDS ring");
+  static_assert(EPI == kPlain || (!I8 && !GATED), "epilogues of the bf16 products");
 };
 
 // Waits until at most `stages` (0 .. 3) stages of LOADS loads each are out.
@@ -501,9 +519,101 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   uint8_t *slab = smem + wave * C::SLAB;
   const int row_w = m0 + wm * C::MB * 16;           // first row of the wave
   const int col_w = n0 + wn * C::OUT_NB * 16;       // first output column of the wave
+  if constexpr (C::EPI == kXentStats) {
+    // Largest logit and sum of exp(scale (z - largest)) of every row over the wave's
+    // columns, over its 4 quarters of lanes, then over the waves side by side.  (z -
+    // largest) before the product with the scale: the difference is exact where it
+    // counts.
+    float *red = (float *)smem;  // [WN][BM][2]
+    const float base2 = a.scale * 1.4426950408889634f;
+    const bool edge = col_w + 16 * C::NB > a.n;
+#pragma unroll
+    for (int i = 0; i < C::MB; ++i) {
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col_w + 16 * j + 4 * q + e >= a.n) acc[i][j][e] = -INFINITY;
+      }
+      float most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, acc[i][j][e]);
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const float from = most == -INFINITY ? 0.f : most;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - from) * base2);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (q == 0) *(float2 *)(red + 2 * ((wn * C::BM) + (wm * C::MB + i) * 16 + r16)) = float2{most, sum};
+      const int row = row_w + 16 * i + r16;
+      const int at = row < a.m && a.targets ? a.targets[row] - a.first_token - col_w : -1;
+      if (__any(at >= 0 && at < 16 * C::NB)) {
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at == 16 * j + 4 * q + e && col_w + at < a.n) a.at_target[row] = acc[i][j][e];
+      }
+    }
+    mm_barrier();
+    for (int r = threadIdx.x; r < rows; r += C::THREADS) {
+      float2 v[C::WN];
+      float most = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) {
+        v[w] = *(const float2 *)(red + 2 * (w * C::BM + r));
+        most = fmaxf(most, v[w].x);
+      }
+      const float from = most == -INFINITY ? 0.f : most;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) sum += v[w].y * __builtin_amdgcn_exp2f((v[w].x - from) * base2);
+      *(float2 *)(a.stats + 2 * ((int64_t)tn * a.m + m0 + r)) = float2{most, sum};
+    }
+    return;
+  }
+  // columns that are stored (the gradient of the logits is padded with zeros to
+  // whole 16-byte units: the products that read it take units whole)
+  const int n_out = C::EPI == kXentGrad ? (a.n + 7) & ~7 : a.n;
+  // kXentGrad: per row its weight, the logarithm (base 2) of its sum and its target
+  float weight[C::EPI == kXentGrad ? C::MB : 1], log_sum[C::EPI == kXentGrad ? C::MB : 1];
+  int target[C::EPI == kXentGrad ? C::MB : 1];
+  if constexpr (C::EPI == kXentGrad) {
+#pragma unroll
+    for (int i = 0; i < C::MB; ++i) {
+      const int row = min(row_w + 16 * i + r16, a.m - 1);
+      weight[i] = a.row_weight[row];
+      log_sum[i] = a.lse[row] * 1.4426950408889634f;
+      target[i] = a.targets[row] - a.first_token;
+    }
+  }
+  const float alpha = C::EPI == kScaled ? a.alpha[0] : 1.f;
   // fp32 values of block (i, j), scales applied
   auto value = [&](int i, int j) {
     f32x4 v;
+    if constexpr (C::EPI == kXentGrad) {
+      const float base2 = a.scale * 1.4426950408889634f;
+      const int col = col_w + 16 * j + 4 * q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], base2, -log_sum[i]));
+        // (a weight of 0: nothing, whatever the logits are)
+        v[e] = weight[i] == 0.f || col + e >= a.n ? 0.f : weight[i] * (col + e == target[i] ? p - 1.f : p);
+      }
+      return v;
+    }
+    if constexpr (C::EPI == kScaled) {
+      v = acc[i][j] * alpha;
+      const int row = row_w + 16 * i + r16, col = col_w + 16 * j + 4 * q;
+      if (a.add && row < m_out && col < a.n) v += *(const f32x4 *)(a.add + row * a.ldadd + col);
+      return v;
+    }
     if constexpr (C::I8) {
       bool up;
       int col = b_col(wn * C::NB + j, 4 * q, &up);
@@ -537,10 +647,10 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
 #pragma unroll
     for (int r0 = 0; r0 < 16; r0 += ROWS) {
       const int rr = r0 + lane / CHUNKS, row = row_w + 16 * i + rr;
-      if (lane >= ROWS * CHUNKS || row >= m_out || col >= a.n) continue;
+      if (lane >= ROWS * CHUNKS || row >= m_out || col >= n_out) continue;
       const u32x4 v = *(const u32x4 *)(slab + rr * C::PITCH + c * EL);
       uint8_t *dst = (uint8_t *)out + (row * ld + shift + col) * EL;
-      if (col + PER <= a.n) {
+      if (col + PER <= n_out) {
         // (a weight gradient, of any size, is read once, much later: past the caches.
         // Backward us through / past them, gradients in turn that no cache holds: 257
         // tokens of 2817 x 1032 35.4 / 33.4 (11.6 MB bf16) and 37.0 / 35.3 (fp32), one
@@ -590,6 +700,20 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
               a.y, a.ldy, a.otype, 0);
     } else {
       store(i, [&](int j) { return value(i, j); }, a.y, a.ldy, a.otype, 0);
+      if constexpr (C::EPI == kXentGrad && C::BM == 32) {
+        if (a.halves > 0)  // what the rounding left
+          store(i,
+                [&](int j) {
+                  f32x4 v = value(i, j);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float rest = v[e] - bf16_bits_to_f32(bf16_rne(v[e]));
+                    v[e] = fabsf(v[e]) <= 3.3e38f ? rest : 0.f;  // (nothing of an infinity or a NaN)
+                  }
+                  return v;
+                },
+                (uint16_t *)a.y + a.halves * a.ldy, a.ldy, a.otype, 0);
+      }
     }
   }
 }

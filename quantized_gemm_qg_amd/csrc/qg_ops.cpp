@@ -10,14 +10,6 @@
 
 namespace qg {
 
-// The tiled products address a tile's rows with 32-bit offsets from a 64-bit
-// base: 256 rows of this pitch stay below 2 GiB.  (The gradient of the
-// pre-activations has rows of up to 64 MiB, of which 64 are within reach: shapes
-// of more rows are left out where theirs are not.)
-constexpr int64_t kMaxPitchBytes = 1 << 23;
-// Tiles are numbered in 32 bits (the smallest tile is 32 x 64 outputs).
-static bool tiles_fit(int64_t m, int64_t n) { return ((m + 31) / 32) * ((n + 63) / 64) < (1ll << 31) - 8; }
-
 // Int8 workspace: [split-K counters][partial tiles][codes of the quantized
 // rows][their scales]; nothing where none of them is needed.
 struct I8Space {

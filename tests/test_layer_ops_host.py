@@ -71,3 +71,58 @@ def test_norm_backward_without_outputs():
     assert qg.rmsnorm_backward_workspace_size(1 << 20, 1 << 24) <= 64 << 20
     assert qg._lib.qg_rmsnorm_backward_workspace_size(1, 64, None) == INVALID
     assert qg._lib.qg_rmsnorm_backward_workspace_size(1, -64, ctypes.byref(ctypes.c_uint64())) == INVALID
+
+
+def xent(x=DEV, ldx=64, w=DEV, ldw=64, m=4, k=64, vocab=100, targets=DEV, scale=1.0, loss=DEV, lse=DEV, ws=DEV, wsb=1 << 40):
+    qg.linear_xent(x, ldx, w, ldw, m, k, vocab, targets, scale, loss, lse, ws, wsb, stream=0)
+
+
+def xent_back(x=DEV, ldx=64, w=DEV, ldw=64, m=4, k=64, vocab=100, targets=DEV, scale=1.0, lse=DEV, dloss=DEV, dx=DEV, lddx=64, dw=DEV,
+              dw_type=qg.O_F32, lddw=64, ws=DEV, wsb=1 << 40):
+    qg.linear_xent_backward(x, ldx, w, ldw, m, k, vocab, targets, scale, lse, dloss, dx, lddx, dw, dw_type, lddw, ws, wsb, stream=0)
+
+
+@pytest.mark.parametrize("fn", [xent, xent_back])
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(x=None)), (INVALID, dict(w=None)), (INVALID, dict(m=-1)), (INVALID, dict(k=-8)), (INVALID, dict(vocab=-1)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-1.0)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(scale=float("inf"))),
+    (INVALID, dict(targets=None)), (SHAPE, dict(k=60)), (SHAPE, dict(k=0)), (SHAPE, dict(vocab=0)), (SHAPE, dict(ldx=56)),
+    (SHAPE, dict(ldw=56)), (ALIGNMENT, dict(x=DEV + 8)), (ALIGNMENT, dict(w=DEV + 2)), (ALIGNMENT, dict(ldx=68)),
+    (ALIGNMENT, dict(ldw=68)), (ALIGNMENT, dict(targets=DEV + 2)), (ALIGNMENT, dict(lse=DEV + 2)), (INVALID, dict(ws=None)),
+    (SMALL, dict(wsb=1 << 16)), (ALIGNMENT, dict(ws=DEV + 64)), (UNSUPPORTED, dict(ldx=1 << 23)), (UNSUPPORTED, dict(ldw=1 << 23)),
+    (UNSUPPORTED, dict(vocab=(1 << 24) + 1)), (UNSUPPORTED, dict(m=(1 << 30) + 1)),
+])
+def test_xent_refusals(fn, status, kw):
+    refuses(status, fn, **kw)
+
+
+@pytest.mark.parametrize("status,kw", [(INVALID, dict(loss=None, lse=None)), (ALIGNMENT, dict(loss=DEV + 1))])
+def test_xent_forward_refusals(status, kw):
+    refuses(status, xent, **kw)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(lse=None)), (INVALID, dict(dloss=None)), (INVALID, dict(dw_type=2)), (SHAPE, dict(lddx=56)), (SHAPE, dict(lddw=63)),
+    (ALIGNMENT, dict(dx=DEV + 2)), (ALIGNMENT, dict(dw=DEV + 4)), (ALIGNMENT, dict(dloss=DEV + 2)),
+])
+def test_xent_backward_refusals(status, kw):
+    refuses(status, xent_back, **kw)
+
+
+def test_xent_without_work():
+    xent(m=0, x=None, w=None, targets=None, loss=None, lse=None, ws=None, wsb=0)
+    xent_back(m=0, dw=None, x=None, w=None, targets=None, lse=None, dloss=None, ws=None, wsb=0)
+    xent_back(dx=None, dw=None, ws=None, wsb=0)
+    for size in (qg.linear_xent_workspace_size, qg.linear_xent_backward_workspace_size):
+        assert size(0, 64, 100) == size(4, 0, 100) == size(4, 64, 0) == 0
+    for fn in (qg._lib.qg_linear_xent_workspace_size, qg._lib.qg_linear_xent_backward_workspace_size):
+        assert fn(4, 64, 100, None) == INVALID and fn(-1, 64, 100, ctypes.byref(ctypes.c_uint64())) == INVALID
+
+
+def test_xent_memory_does_not_grow_with_the_vocabulary():
+    """The logits' gradient of a piece, whatever the vocabulary; many tokens: at
+    least 8192 columns of it."""
+    m, k = 4096, 4096
+    fixed = 48 << 20   # partial tiles at most
+    assert qg.linear_xent_backward_workspace_size(m, k, 1 << 24) <= (128 << 20) + 4 * m * k + fixed + (1 << 20)
+    assert qg.linear_xent_backward_workspace_size(1 << 20, 64, 1 << 20) <= (1 << 20) * (8192 * 2 + 4 * 64 + 4) + fixed + (1 << 20)
