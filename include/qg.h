@@ -645,6 +645,37 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
                               int64_t lddx, void *dw, int32_t dw_type, void *ws, uint64_t ws_bytes,
                               hipStream_t stream);
 
+/* Low-rank adapters of many requests added in place to the output of a projection
+ * that they share: for every row r of adapter a
+ *   y[r] += scales[a] (x[r] A_a^T) B_a^T
+ * (fp32 sums; the low-rank row enters the second product as two bf16 parts for a
+ * bf16 y, three for an fp32 one; y is rounded once).  Rows of no adapter keep
+ * their bits.
+ *   x       device, bf16 [m][ldx]: the projection's input before any quantization.
+ *   a, b    device, bf16 [num_adapters][rank][lda] and [num_adapters][n][ldb], lda
+ *           >= k, ldb >= rank; adapters of a lower rank are padded with zeros.  x,
+ *           a and b 16-B aligned, their strides multiples of 8, k % 8 == 0, rank %
+ *           8 == 0, rank <= QG_LORA_MAX_RANK, num_adapters <= 1024, m <= 2^21.
+ *   scales  device, fp32 [num_adapters], or NULL: 1.
+ *   sorted_rows, offsets  device, the rows grouped by adapter, as qg_moe_sort
+ *           gives them for the rows' adapter ids (topk 1, num_experts =
+ *           num_adapters; ids outside, such as -1, are rows of no adapter): one
+ *           call serves every projection of a batch.  A row is listed once at most;
+ *           entries that name no row are skipped.
+ *   y       device, [m][ldy] of y_type (QG_O_BF16 / QG_O_F32), ldy >= n, any element
+ *           alignment (rows on 16 bytes are faster); some columns of a fused
+ *           projection are y + their first column.  It overlaps no input.
+ *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents.
+ * m == 0 is a no-op.  A row's result does not depend on the other rows' values.
+ * Asynchronous on `stream`. */
+#define QG_LORA_MAX_RANK 256
+qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank,
+                                 uint64_t *bytes);
+qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t lda, const void *b, int64_t ldb,
+                  const float *scales, int32_t num_adapters, int32_t rank, const int32_t *sorted_rows,
+                  const int32_t *offsets, int64_t m, int64_t k, int64_t n, void *y, int32_t y_type, int64_t ldy,
+                  void *ws, uint64_t ws_bytes, hipStream_t stream);
+
 /* Softmax cross entropy of hidden states against a head's weights, for large
  * vocabularies: the logits exist tile by tile and are never in memory.  With
  * z = scale x W^T (fp32 sums of bf16 products),

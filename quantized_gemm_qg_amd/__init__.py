@@ -39,11 +39,13 @@ EXPORTS = (
     "qg_ffn_gated_workspace_size", "qg_ffn_gated", "qg_ffn_gated_backward_workspace_size", "qg_ffn_gated_backward",
     "qg_token_logprobs_workspace_size", "qg_token_logprobs", "qg_token_logprobs_backward",
     "qg_rmsnorm", "qg_rmsnorm_backward_workspace_size", "qg_rmsnorm_backward",
+    "qg_lora_workspace_size", "qg_lora",
     "qg_linear_xent_workspace_size", "qg_linear_xent", "qg_linear_xent_backward_workspace_size", "qg_linear_xent_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X = 1, 2
 MAX_ALTERNATIVES = 32
+LORA_MAX_RANK = 256
 
 
 class QGError(RuntimeError):
@@ -128,6 +130,8 @@ def _load():
         "qg_rmsnorm": (I32, [P, I32, I64, P, I32, I64, P, I64, P, ctypes.c_float, I64, I64, P, I64, I32, P, I64, P, P]),
         "qg_rmsnorm_backward_workspace_size": (I32, [I64, I64, ctypes.POINTER(U64)]),
         "qg_rmsnorm_backward": (I32, [P, I32, I64, P, ctypes.c_float, I64, I64, P, I64, P, I64, P, I64, P, I32, P, U64, P]),
+        "qg_lora_workspace_size": (I32, [I64, I64, I64, I32, I32, ctypes.POINTER(U64)]),
+        "qg_lora": (I32, [P, I64, P, I64, P, I64, P, I32, I32, P, P, I64, I64, I64, P, I32, I64, P, U64, P]),
         "qg_linear_xent_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
         "qg_linear_xent": (I32, [P, I64, P, I64, I64, I64, I64, P, ctypes.c_float, P, P, P, U64, P]),
         "qg_linear_xent_backward_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
@@ -411,6 +415,17 @@ def rmsnorm_backward(s, s_type: int, lds: int, weight, eps: float, rows: int, k:
     _check(_lib.qg_rmsnorm_backward(_ptr(s), s_type, lds, _ptr(weight), eps, rows, k, _ptr(dy), lddy, _ptr(dsum), ldds,
                                     _ptr(dx), lddx, _ptr(dw), dw_type, _ptr(ws), ws_bytes, _stream(stream)),
            "qg_rmsnorm_backward")
+
+
+def lora_workspace_size(m: int, k: int, n: int, num_adapters: int, rank: int) -> int:
+    return _size(_lib.qg_lora_workspace_size, "qg_lora_workspace_size", m, k, n, num_adapters, rank)
+
+
+def lora(x, ldx: int, a, lda: int, b, ldb: int, scales, num_adapters: int, rank: int, sorted_rows, offsets, m: int, k: int, n: int,
+         y, y_type: int, ldy: int, ws, ws_bytes: int, stream=None) -> None:
+    """y[r] += scales[i] (x[r] a[i]^T) b[i]^T for the rows of every adapter i, grouped by moe_sort of their adapter ids."""
+    _check(_lib.qg_lora(_ptr(x), ldx, _ptr(a), lda, _ptr(b), ldb, _ptr(scales), num_adapters, rank, _ptr(sorted_rows),
+                        _ptr(offsets), m, k, n, _ptr(y), y_type, ldy, _ptr(ws), ws_bytes, _stream(stream)), "qg_lora")
 
 
 def linear_xent_workspace_size(m: int, k: int, vocab: int) -> int:

@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqg.so")
 SOURCES = ["qg_api.cpp", "qg_ops.cpp", "qg_repack.cpp", "qg_kernels.hip", "qg_formats.hip", "qg_tiled.hip",
            "qg_tiled_a16.hip", "qg_act.hip", "qg_int8.hip", "qg_ffn.hip", "qg_logprobs.hip", "qg_layer.cpp",
-           "qg_norm.hip", "qg_xent.hip"]
+           "qg_norm.hip", "qg_lora.hip", "qg_xent.hip"]
 ARCH = os.environ.get("QG_OFFLOAD_ARCH", "gfx950")
 
 

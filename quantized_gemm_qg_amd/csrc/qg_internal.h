@@ -503,6 +503,25 @@ hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, con
                           int out_type, int64_t ldout, hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, void *dw, int dw_type, int64_t lddw,
                           hipStream_t s, MmInfo *info = nullptr);
+// low-rank adapters (qg_lora.hip); strides in elements
+struct LoraArgs {
+  const uint16_t *x;
+  int64_t ldx;
+  const uint16_t *a;  // [adapters][rank][lda]
+  int64_t lda;
+  const uint16_t *b;  // [adapters][n][ldb]
+  int64_t ldb;
+  const float *scales;  // [adapters] or NULL
+  const int32_t *sorted, *offsets;
+  int32_t adapters, rank, m, k, n;
+  void *y;
+  int64_t ldy;
+  bool y_vectors;  // y's rows are 16-byte aligned
+  float *t;        // [splits][m][rank]
+  int32_t splits;
+};
+int lora_splits(int64_t m, int64_t k, int adapters);
+hipError_t launch_lora(const LoraArgs &a, bool y_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

@@ -83,6 +83,46 @@ extern "C" qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t 
   return hip_status(launch_rmsnorm_backward(a, s_type == QG_O_F32, dw, dw_type == QG_O_F32, stream));
 }
 
+static qg_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t adapters, int32_t rank) {
+  if (m < 0 || k < 0 || n < 0 || adapters <= 0 || rank <= 0) return QG_ERR_INVALID_ARGUMENT;
+  if (k == 0 || n == 0 || k % 8 != 0 || rank % 8 != 0) return QG_ERR_SHAPE;
+  if (rank > QG_LORA_MAX_RANK || adapters > kMaxExperts || m > (1 << 21) || k > (1 << 24) || n > (1 << 24))
+    return QG_ERR_UNSUPPORTED;
+  return QG_OK;
+}
+
+extern "C" qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank,
+                                            uint64_t *bytes) {
+  if (!bytes) return QG_ERR_INVALID_ARGUMENT;
+  QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
+  *bytes = m == 0 ? 0 : align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
+  return QG_OK;
+}
+
+extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t lda, const void *b, int64_t ldb,
+                             const float *scales, int32_t num_adapters, int32_t rank, const int32_t *sorted_rows,
+                             const int32_t *offsets, int64_t m, int64_t k, int64_t n, void *y, int32_t y_type,
+                             int64_t ldy, void *ws, uint64_t ws_bytes, hipStream_t stream) {
+  QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
+  if (!out_type(y_type)) return QG_ERR_INVALID_ARGUMENT;
+  if (m > 0 && (!x || !a || !b || !sorted_rows || !offsets || !y)) return QG_ERR_INVALID_ARGUMENT;
+  QG_TRY(matrix_check(x, ldx, k, 2));
+  QG_TRY(matrix_check(a, lda, k, 2));
+  QG_TRY(matrix_check(b, ldb, rank, 2));
+  if (ldy < n) return QG_ERR_SHAPE;
+  if (!aligned(y, el_of(y_type)) || !aligned(scales, 4) || !aligned(sorted_rows, 4) || !aligned(offsets, 4))
+    return QG_ERR_ALIGNMENT;
+  if (m == 0) return QG_OK;
+  uint64_t need = 0;
+  (void)qg_lora_workspace_size(m, k, n, num_adapters, rank, &need);
+  QG_TRY(ws_check(need, ws, ws_bytes));
+  const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
+  const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
+                      num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors, (float *)ws,
+                      lora_splits(m, k, num_adapters)};
+  return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
+}
+
 namespace qg {
 
 // Forward workspace: [split-K counters][partial tiles][statistics of the

@@ -126,3 +126,33 @@ def test_xent_memory_does_not_grow_with_the_vocabulary():
     fixed = 48 << 20   # partial tiles at most
     assert qg.linear_xent_backward_workspace_size(m, k, 1 << 24) <= (128 << 20) + 4 * m * k + fixed + (1 << 20)
     assert qg.linear_xent_backward_workspace_size(1 << 20, 64, 1 << 20) <= (1 << 20) * (8192 * 2 + 4 * 64 + 4) + fixed + (1 << 20)
+
+
+def lora(x=DEV, ldx=64, a=DEV, lda=64, b=DEV, ldb=16, scales=DEV, adapters=3, rank=16, rows=DEV, offsets=DEV, m=4, k=64, n=100, y=DEV,
+         y_type=qg.O_BF16, ldy=100, ws=DEV, wsb=1 << 30):
+    qg.lora(x, ldx, a, lda, b, ldb, scales, adapters, rank, rows, offsets, m, k, n, y, y_type, ldy, ws, wsb, stream=0)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (INVALID, dict(x=None)), (INVALID, dict(a=None)), (INVALID, dict(b=None)), (INVALID, dict(rows=None)), (INVALID, dict(offsets=None)),
+    (INVALID, dict(y=None)), (INVALID, dict(y_type=2)), (INVALID, dict(m=-1)), (INVALID, dict(k=-8)), (INVALID, dict(n=-1)),
+    (INVALID, dict(adapters=0)), (INVALID, dict(rank=0)), (SHAPE, dict(k=60)), (SHAPE, dict(k=0)), (SHAPE, dict(n=0)),
+    (SHAPE, dict(rank=12, ldb=16)), (SHAPE, dict(ldx=56)), (SHAPE, dict(lda=56)), (SHAPE, dict(ldb=8)), (SHAPE, dict(ldy=99)),
+    (UNSUPPORTED, dict(rank=264, ldb=264)), (UNSUPPORTED, dict(adapters=1025)), (UNSUPPORTED, dict(m=(1 << 21) + 1)),
+    (UNSUPPORTED, dict(n=(1 << 24) + 1, ldy=1 << 25)), (ALIGNMENT, dict(x=DEV + 8)), (ALIGNMENT, dict(a=DEV + 8)),
+    (ALIGNMENT, dict(b=DEV + 8)), (ALIGNMENT, dict(ldx=68)), (ALIGNMENT, dict(lda=68)), (ALIGNMENT, dict(ldb=20)),
+    (ALIGNMENT, dict(y=DEV + 1)), (ALIGNMENT, dict(y=DEV + 2, y_type=qg.O_F32)), (ALIGNMENT, dict(scales=DEV + 2)),
+    (ALIGNMENT, dict(rows=DEV + 2)), (ALIGNMENT, dict(offsets=DEV + 1)), (INVALID, dict(ws=None)), (SMALL, dict(wsb=16)),
+    (ALIGNMENT, dict(ws=DEV + 64)),
+])
+def test_lora_refusals(status, kw):
+    refuses(status, lora, **kw)
+
+
+def test_lora_sizes():
+    lora(m=0, x=None, a=None, b=None, rows=None, offsets=None, y=None, ws=None, wsb=0)
+    out = ctypes.c_uint64()
+    size = lambda m, k, n, adapters, rank: qg._lib.qg_lora_workspace_size(m, k, n, adapters, rank, ctypes.byref(out))  # noqa: E731
+    assert qg._lib.qg_lora_workspace_size(1, 64, 8, 1, 8, None) == INVALID
+    assert size(-1, 64, 8, 1, 8) == INVALID and size(1, 64, 8, 0, 8) == INVALID and size(1, 60, 8, 1, 8) == SHAPE
+    assert size(1, 64, 8, 1, 264) == UNSUPPORTED
