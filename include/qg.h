@@ -654,8 +654,9 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
  *   x       device, bf16 [m][ldx]: the projection's input before any quantization.
  *   a, b    device, bf16 [num_adapters][rank][lda] and [num_adapters][n][ldb], lda
  *           >= k, ldb >= rank; adapters of a lower rank are padded with zeros.  x,
- *           a and b 16-B aligned, their strides multiples of 8, k % 8 == 0, rank %
- *           8 == 0, rank <= QG_LORA_MAX_RANK, num_adapters <= 1024, m <= 2^21.
+ *           a and b 16-B aligned, their strides multiples of 8, lda and ldb <=
+ *           2^22, k % 8 == 0, rank % 8 == 0, rank <= QG_LORA_MAX_RANK, num_adapters
+ *           <= 1024, m <= 2^21, n <= 2^24.
  *   scales  device, fp32 [num_adapters], or NULL: 1.
  *   sorted_rows, offsets  device, the rows grouped by adapter, as qg_moe_sort
  *           gives them for the rows' adapter ids (topk 1, num_experts =

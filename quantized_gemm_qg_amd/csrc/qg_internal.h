@@ -519,9 +519,10 @@ struct LoraArgs {
   bool y_vectors;  // y's rows are 16-byte aligned
   float *t;        // [splits][m][rank]
   int32_t splits;
+  int32_t chunks;  // (set by the launch) 256-column chunks of a workgroup
 };
 int lora_splits(int64_t m, int64_t k, int adapters);
-hipError_t launch_lora(const LoraArgs &a, bool y_f32, hipStream_t s);
+hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

@@ -86,7 +86,7 @@ extern "C" qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t 
 static qg_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t adapters, int32_t rank) {
   if (m < 0 || k < 0 || n < 0 || adapters <= 0 || rank <= 0) return QG_ERR_INVALID_ARGUMENT;
   if (k == 0 || n == 0 || k % 8 != 0 || rank % 8 != 0) return QG_ERR_SHAPE;
-  if (rank > QG_LORA_MAX_RANK || adapters > kMaxExperts || m > (1 << 21) || k > (1 << 24) || n > (1 << 24))
+  if (rank > QG_LORA_MAX_RANK || adapters > kMaxExperts || m > (1 << 21) || k > (1 << 22) || n > (1 << 24))
     return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
@@ -109,6 +109,7 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   QG_TRY(matrix_check(x, ldx, k, 2));
   QG_TRY(matrix_check(a, lda, k, 2));
   QG_TRY(matrix_check(b, ldb, rank, 2));
+  if (2 * lda > kMaxPitchBytes || 2 * ldb > kMaxPitchBytes) return QG_ERR_UNSUPPORTED;
   if (ldy < n) return QG_ERR_SHAPE;
   if (!aligned(y, el_of(y_type)) || !aligned(scales, 4) || !aligned(sorted_rows, 4) || !aligned(offsets, 4))
     return QG_ERR_ALIGNMENT;
@@ -119,7 +120,7 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
   const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
                       num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors, (float *)ws,
-                      lora_splits(m, k, num_adapters)};
+                      lora_splits(m, k, num_adapters), 0};
   return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
 }
 

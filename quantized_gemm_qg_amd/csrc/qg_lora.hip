@@ -16,6 +16,7 @@
 
 #include "qg_device.h"
 #include "qg_internal.h"
+#include "qg_mm.h"
 #include "qg_quant.h"
 
 namespace qg {
@@ -39,8 +40,11 @@ __device__ __forceinline__ LoraItem lora_item(const LoraArgs &a, int item) {
     *begin = min(max(a.offsets[e], 0), a.m);
     return max(min(a.offsets[e + 1], a.m) - *begin, 0);
   };
-  int mine = 0, begin;
-  for (int e = first; e < last; ++e) mine += (span(e, &begin) + ROWS - 1) / ROWS;
+  int mine = 0, begin = 0, count = 0;
+  for (int e = first; e < last; ++e) {
+    count = span(e, &begin);
+    mine += (count + ROWS - 1) / ROWS;
+  }
   int upto = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -50,22 +54,16 @@ __device__ __forceinline__ LoraItem lora_item(const LoraArgs &a, int item) {
   const uint64_t behind = __ballot(upto > item);
   if (behind == 0) return LoraItem{-1, 0, 0};
   const int owner = __ffsll((unsigned long long)behind) - 1;
-  LoraItem found = {-1, 0, 0};
-  if (lane == owner) {
-    int at = item - (upto - mine);
-    for (int e = first; e < last; ++e) {
-      const int count = span(e, &begin), items = (count + ROWS - 1) / ROWS;
-      if (at < items) {
-        found = LoraItem{e, begin + at * ROWS, min(ROWS, count - at * ROWS)};
-        break;
-      }
+  int at = item - (upto - mine), e = first;
+  if (per > 1 && lane == owner)  // (with one adapter per lane its offsets are at hand)
+    for (;; ++e) {
+      count = span(e, &begin);
+      const int items = (count + ROWS - 1) / ROWS;
+      if (at < items) break;
       at -= items;
     }
-  }
-  found.adapter = __builtin_amdgcn_readlane(found.adapter, owner);
-  found.pos = __builtin_amdgcn_readlane(found.pos, owner);
-  found.rows = __builtin_amdgcn_readlane(found.rows, owner);
-  return found;
+  return LoraItem{__builtin_amdgcn_readlane(e, owner), __builtin_amdgcn_readlane(begin + at * ROWS, owner),
+                  __builtin_amdgcn_readlane(min(ROWS, count - at * ROWS), owner)};
 }
 
 // The row of sorted position pos, -1 for an entry that names none
@@ -76,119 +74,183 @@ __device__ __forceinline__ int lora_row(const LoraArgs &a, int pos) {
 
 }  // namespace
 
-// t[split][position][rank] = x A^T over the split's part of k.  A wave computes 16
-// rows x 16 NB columns with operands straight from memory (16 bytes per lane, U
-// steps of 32 k in flight).  RW waves take 16 rows each; the KW waves of a row block
-// share the part of k and join in LDS.
-template <int NB, int RW, int KW>
-__global__ __launch_bounds__(64 * RW *KW) void lora_down_kernel(LoraArgs a) {
-  constexpr int U = NB <= 2 ? 8 : NB <= 4 ? 4 : 2;
-  __shared__ f32x4 join[KW > 1 ? RW * (KW - 1) * NB * 64 : 1];
-  const LoraItem it = lora_item<16 * RW>(a, blockIdx.x);
+// t[split][position][rank] = x A^T over the split's part of k, for an item of 16
+// rows: KW waves share the part of k and join in LDS.  The operand layout of the
+// matrix instruction has neighbouring lanes in different rows, which the memory path
+// takes at 16 bytes per clock and CU (51 with four lanes to 64 bytes of a row; L1
+// hits, 4 waves per SIMD), and every workgroup reads its whole adapter: so whole
+// cache lines go to a ring of ST stages of 64 k in LDS (16-byte chunks of a row at
+// slot chunk ^ row % 8), one ring per wave, without barriers.  4096 rows, rank 64, k
+// 4096: 16 us (operands straight to registers 24), 44 rows of 35 adapters of rank
+// 16: 4.1 us (6.2), one row 3.7 us (5.4).
+template <int NB, int KW, int ST>
+__global__ __launch_bounds__(64 * KW) void lora_down_kernel(LoraArgs a) {
+  constexpr int COPIES = 2 * (1 + NB), STAGE = COPIES * 1024, RING = ST * STAGE;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const LoraItem it = lora_item<16>(a, blockIdx.x);
   if (it.adapter < 0) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rw = wave % RW, kw = wave / RW;
+  const int lane = threadIdx.x & 63, kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
-  const bool any = 16 * rw < it.rows;
-  const int pos = it.pos + min(16 * rw + r16, it.rows - 1);
-  const int row = max(lora_row(a, pos), 0);
-  const uint16_t *xp = a.x + row * a.ldx + 8 * q;
-  const uint16_t *ap[NB];
+  // a copy: 8 rows of 128 bytes, this lane's 16 of row 8 c + lane / 8
+  const int chunk = (lane & 7) ^ ((lane >> 3) & 7);
+  const uint8_t *src[COPIES];
 #pragma unroll
-  for (int j = 0; j < NB; ++j)
-    ap[j] = a.a + ((int64_t)it.adapter * a.rank + min(16 * j + r16, a.rank - 1)) * a.lda + 8 * q;
-  // steps of 32 k: of the split, then of the wave
-  const int steps = (a.k + 31) / 32, per_split = (steps + a.splits - 1) / a.splits;
-  const int s0 = blockIdx.y * per_split, s1 = min(s0 + per_split, steps);
-  const int per_wave = (max(s1 - s0, 0) + KW - 1) / KW;
-  const int begin = s0 + kw * per_wave, end = any ? min(begin + per_wave, s1) : begin;
+  for (int c = 0; c < 2; ++c) {
+    const int row = a.sorted[it.pos + min(8 * c + (lane >> 3), it.rows - 1)];
+    src[c] = (const uint8_t *)(a.x + (row >= 0 && row < a.m ? row : 0) * a.ldx) + 16 * chunk;
+  }
+#pragma unroll
+  for (int c = 2; c < COPIES; ++c)
+    src[c] = (const uint8_t *)(a.a + ((int64_t)it.adapter * a.rank + min(8 * (c - 2) + (lane >> 3), a.rank - 1)) * a.lda) +
+             16 * chunk;
+  // stages of 64 k: of the split, then of the wave
+  const int steps = (a.k + 63) / 64, per_split = (steps + a.splits - 1) / a.splits;
+  const int s0 = min((int)blockIdx.y * per_split, steps), s1 = min(s0 + per_split, steps);
+  const int per_wave = (s1 - s0 + KW - 1) / KW;
+  const int begin = min(s0 + kw * per_wave, s1), end = min(begin + per_wave, s1);
+  const uint8_t *mine = smem + kw * RING;
+  const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)mine;
+  auto issue = [&](int s) {
+    const uint32_t st = ring + (s - begin) % ST * STAGE;
+    const bool in = 64 * s + 8 * chunk < a.k;  // (behind k: zeros)
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c)
+      mm_copy16_at(in ? src[c] + 128 * (int64_t)s : (const uint8_t *)mm_zeros, st + c * 1024);
+  };
   f32x4 acc[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (int s = begin; s < end; s += U) {
-    u32x4 xv[U], av[U][NB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // (steps behind the wave's last one are loaded again and multiplied by zeros;
-      // so are the units behind k)
-      const int at = min(s + u, end - 1);
-      const bool in = 32 * at + 8 * q < a.k;
-      const int64_t off = in ? 32 * (int64_t)at : 0;
-      xv[u] = *(const u32x4 *)(xp + (in ? off : -8 * q));
-#pragma unroll
-      for (int j = 0; j < NB; ++j) av[u][j] = *(const u32x4 *)(ap[j] + (in ? off : -8 * q));
+  for (int s = 0; s < ST - 1; ++s)
+    if (begin + s < end) issue(begin + s);
+  for (int s = begin; s < end; ++s) {
+    // (into the stage that was read last time: its reads are in registers)
+    if (s + ST - 1 < end) {
+      issue(s + ST - 1);
+      QG_WAIT_VMCNT((ST - 1) * COPIES);
+    } else if (ST > 2 && s + 1 < end) {
+      QG_WAIT_VMCNT(COPIES);
+    } else {
+      QG_WAIT_VMCNT(0);
     }
+    asm volatile("" ::: "memory");
+    const uint8_t *st = mine + (s - begin) % ST * STAGE;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = s + u < end && 32 * (s + u) + 8 * q < a.k;
+    for (int u = 0; u < 2; ++u) {
+      const int at = r16 * 128 + 16 * ((4 * u + q) ^ (r16 & 7));
+      const u32x4 xv = *(const u32x4 *)(st + at);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[j] = mfma_bf16(in ? av[u][j] : zero, in ? xv[u] : zero, acc[j]);
+      for (int j = 0; j < NB; ++j) acc[j] = mfma_bf16(*(const u32x4 *)(st + 2048 * (1 + j) + at), xv, acc[j]);
     }
+    QG_WAIT_LGKMCNT0();
+    asm volatile("" ::: "memory");
   }
-  if constexpr (KW > 1) {
-    if (kw > 0) {
+  f32x4 *join = (f32x4 *)smem;
+  __syncthreads();  // every wave is done with its ring
+  if (kw > 0) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) join[((rw * (KW - 1) + kw - 1) * NB + j) * 64 + lane] = acc[j];
-    }
-    __syncthreads();
-    if (kw > 0) return;
-#pragma unroll
-    for (int o = 0; o < KW - 1; ++o)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[j] += join[((rw * (KW - 1) + o) * NB + j) * 64 + lane];
+    for (int j = 0; j < NB; ++j) join[((kw - 1) * NB + j) * 64 + lane] = acc[j];
   }
-  if (16 * rw + r16 >= it.rows) return;
-  float *t = a.t + ((int64_t)blockIdx.y * a.m + it.pos + 16 * rw + r16) * a.rank;
+  __syncthreads();
+  if (kw > 0 || r16 >= it.rows) return;
+#pragma unroll
+  for (int o = 0; o < KW - 1; ++o)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[j] += join[(o * NB + j) * 64 + lane];
+  float *t = a.t + ((int64_t)blockIdx.y * a.m + it.pos + r16) * a.rank;
 #pragma unroll
   for (int j = 0; j < NB; ++j)
     if (16 * j + 4 * q < a.rank) *(f32x4 *)(t + 16 * j + 4 * q) = acc[j];
 }
 
-// y += scale t B^T for one item and 256 columns, 64 per wave.  Which column of B a
-// lane brings is arbitrary: block j's column c is 16 (c / 4) + 4 j + c % 4, so a lane
-// ends with 16 neighbouring columns of one row, and four lanes with a cache line.
-// The parts of t stand in LDS as units of 8 along the contraction: [unit][row].
-template <int RB, bool F32>
+// y += scale t B^T for one item of 16 RB rows and `chunks` times 256 columns, 64 of
+// them per wave.  The parts of t stand in LDS as units of 8 along the contraction,
+// [unit][row].  SD x 32 of the rank are in registers at a time, used for every part
+// in turn; ranks of 8 and 16 have their parts side by side in one step.  y is loaded
+// and stored along its rows, 16 bytes per lane (the sums go through LDS for that),
+// and asked for before t.
+template <int RB, int SD, bool F32>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   constexpr int ROWS = 16 * RB, PARTS = F32 ? 3 : 2, EL = F32 ? 4 : 2;
+  constexpr int VC = 16 / EL, LPR = 64 / VC, RPP = 64 / LPR, PASSES = 16 / RPP;  // columns per lane, lanes per row, rows per pass
+  constexpr int UNIT = ROWS + 1;           // 16-byte rows of a unit (one more: banks)
+  constexpr int PITCH = 64 * 4 + 16;       // bytes of a row of the sums
   const LoraItem it = lora_item<ROWS>(a, blockIdx.y);
   if (it.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
-  const int col0 = blockIdx.x * 256 + 64 * wave;
-  const int units = a.rank / 8, steps = (PARTS * units + 3) / 4;
-  u32x4 *parts = (u32x4 *)smem;  // [4 steps][ROWS]
+  const int units = a.rank / 8;
+  const bool side = units <= 2;  // parts side by side
+  const int groups = (units + 4 * SD - 1) / (4 * SD), pitch = side ? 4 : groups * 4 * SD;  // units of a part
+  const int lds_steps = side ? (PARTS * units + 3) / 4 : PARTS;
+  u32x4 *parts = (u32x4 *)smem;  // [lds_steps * pitch][UNIT]
+  uint8_t *slab = smem + lds_steps * pitch * UNIT * 16 + wave * 16 * PITCH;
 
-  // this lane's 16 columns of its row in each block of 16 rows
-  const int col = col0 + 16 * q;
-  uint8_t *yp[RB];
-  bool store[RB];
+  // this lane's row in each pass of each block of 16 rows, and its first column
+  int row[RB][PASSES];
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int p = 16 * i + r16, row = lora_row(a, it.pos + min(p, it.rows - 1));
-    store[i] = p < it.rows && row >= 0 && col < a.n;
-    yp[i] = (uint8_t *)a.y + (max(row, 0) * a.ldy + min(col, a.n - 1)) * EL;
-  }
-  const bool whole = a.y_vectors && col + 16 <= a.n;
-  u32x4 yv[RB][EL];
-  if (whole) {
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int at = 16 * i + p * RPP + lane / LPR, r = a.sorted[it.pos + min(at, it.rows - 1)];
+      row[i][p] = at < it.rows && r >= 0 && r < a.m ? r : -1;
+    }
+  const int ycol = lane % LPR * VC;
+
+  const uint8_t *bbase = (const uint8_t *)(a.b + (int64_t)it.adapter * a.n * a.ldb);
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  u32x4 bv[SD][4];
+  auto load_b = [&](int col0, int group) {
+    const uint8_t *p = bbase + (int64_t)col0 * a.ldb * 2;
+    uint32_t boff[4];  // (64 rows of B span less than 4 GiB; columns behind the last one bring it)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) boff[j] = (uint32_t)(min(16 * j + r16, a.n - 1 - col0) * a.ldb * 2);
+#pragma unroll
+    for (int d = 0; d < SD; ++d) {
+      const int unit = side ? q % units : 4 * (group * SD + d) + q;
+      const uint32_t at = 16 * min(unit, units - 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bv[d][j] = *(const u32x4 *)(p + (boff[j] + at));
+        if (unit >= units) bv[d][j] = zero;
+      }
+    }
+  };
+  u32x4 yv[RB][PASSES], next[RB][PASSES];
+  auto y_at = [&](int i, int p, int col0) {
+    return (uint8_t *)a.y + (max(row[i][p], 0) * a.ldy + col0 + ycol) * EL;
+  };
+  auto load_y = [&](int col0, u32x4 (&yv)[RB][PASSES]) {
+    if (!a.y_vectors || col0 + 64 > a.n) return;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int h = 0; h < EL; ++h) yv[i][h] = ((const u32x4 *)yp[i])[h];
-  }
+      for (int p = 0; p < PASSES; ++p) yv[i][p] = *(const u32x4 *)y_at(i, p, col0);
+  };
+  const int first_col = blockIdx.x * 256 + 64 * wave, stride = gridDim.x * 256;
+  if (first_col < a.n) load_b(first_col, 0);
+  load_y(first_col, yv);
 
   const float scale = a.scales ? a.scales[it.adapter] : 1.f;
   for (int u = threadIdx.x; u < units * ROWS; u += 256) {
-    const int row = u % ROWS, unit = u / ROWS;
-    const float *t = a.t + ((int64_t)it.pos + min(row, it.rows - 1)) * a.rank + 8 * unit;
+    const int r = u / units, unit = u % units;
+    const float *t = a.t + ((int64_t)it.pos + min(r, it.rows - 1)) * a.rank + 8 * unit;
     f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-    for (int s = 0; s < a.splits; ++s) {
-      const f32x4 *p = (const f32x4 *)(t + (int64_t)s * a.m * a.rank);
-      v0 += p[0];
-      v1 += p[1];
+    for (int s0 = 0; s0 < a.splits; s0 += 4) {  // (the loads of four parts go out together)
+      f32x4 w[4][2];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 *p = (const f32x4 *)(t + (int64_t)min(s0 + g, a.splits - 1) * a.m * a.rank);
+        w[g][0] = p[0];
+        w[g][1] = p[1];
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (s0 + g >= a.splits) continue;
+        v0 += w[g][0];
+        v1 += w[g][1];
+      }
     }
     float v[8];
 #pragma unroll
@@ -198,7 +260,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       u32x4 w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
-      parts[(part * units + unit) * ROWS + row] = w;
+      parts[(part * (side ? units : pitch) + unit) * UNIT + r] = w;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {  // what the part left (nothing of an infinity or a NaN)
         const float f = __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
@@ -206,112 +268,167 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       }
     }
   }
-  for (int u = PARTS * units * ROWS + threadIdx.x; u < 4 * steps * ROWS; u += 256) parts[u] = u32x4{0u, 0u, 0u, 0u};
+  // zeros in the units that no part fills
+  if (side) {
+    for (int u = PARTS * units * UNIT + threadIdx.x; u < lds_steps * 4 * UNIT; u += 256) parts[u] = zero;
+  } else {
+    for (int u = threadIdx.x; u < PARTS * (pitch - units) * ROWS; u += 256) {
+      const int r = u % ROWS, unit = u / ROWS;
+      parts[(unit / (pitch - units) * pitch + units + unit % (pitch - units)) * UNIT + r] = zero;
+    }
+  }
   __syncthreads();
 
-  const uint16_t *bp[4];
+  for (int chunk = 0; chunk < a.chunks; ++chunk) {
+    const int col0 = first_col + stride * chunk;
+    if (col0 >= a.n) break;  // (whole waves: the matrix instructions take every lane)
+    const bool whole = a.y_vectors && col0 + 64 <= a.n, more = chunk + 1 < a.chunks && col0 + stride < a.n;
+    if (more) load_y(col0 + stride, next);
+    f32x4 acc[RB][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    bp[j] = a.b + ((int64_t)it.adapter * a.n + min(col0 + 16 * (r16 >> 2) + 4 * j + (r16 & 3), a.n - 1)) * a.ldb;
-  f32x4 acc[RB][4];
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int group = 0; group < groups; ++group) {
+      if (group > 0) load_b(col0, group);
+      for (int st = 0; st < lds_steps; ++st)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (col0 < a.n)  // (whole waves only: the matrix instructions take every lane)
-    for (int s = 0; s < steps; ++s) {
-      const int unit = 4 * s + q;
-      // (units behind the last part: zeros in LDS, any finite or not values of B must not meet them)
-      const int at = unit % units;
-      u32x4 bv[4];
+        for (int d = 0; d < SD; ++d)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bv[j] = *(const u32x4 *)(bp[j] + 8 * at);
-        if (unit >= PARTS * units) bv[j] = u32x4{0u, 0u, 0u, 0u};
+          for (int i = 0; i < RB; ++i) {
+            const u32x4 tv = parts[(st * pitch + 4 * (group * SD + d) + q) * UNIT + 16 * i + r16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma_bf16(bv[d][j], tv, acc[i][j]);
+          }
+    }
+    if (more) load_b(col0 + stride, 0);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(f32x4 *)(slab + r16 * PITCH + (16 * j + 4 * q) * 4) = acc[i][j];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, before its reads
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const f32x4 *sum = (const f32x4 *)(slab + (p * RPP + lane / LPR) * PITCH + ycol * 4);
+        float d[VC];
+#pragma unroll
+        for (int e = 0; e < VC; ++e) d[e] = sum[e / 4][e % 4];
+        if (row[i][p] < 0) continue;
+        uint8_t *dst = y_at(i, p, col0);
+        if (whole) {
+          u32x4 w = yv[i][p];
+          if constexpr (F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + d[e]);
+          } else {
+            float v[8];
+            unpack8(w, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = bf16_pair(v[2 * e] + d[2 * e], v[2 * e + 1] + d[2 * e + 1]);
+          }
+          *(u32x4 *)dst = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < VC; ++e) {
+            if (col0 + ycol + e >= a.n) continue;
+            if constexpr (F32)
+              ((float *)dst)[e] += d[e];
+            else
+              ((uint16_t *)dst)[e] = (uint16_t)bf16_pair(bf16_bits_to_f32(((uint16_t *)dst)[e]) + d[e], 0.f);
+          }
+        }
       }
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const u32x4 tv = parts[unit * ROWS + 16 * i + r16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_bf16(bv[j], tv, acc[i][j]);
-      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the reads, before the slab's next writes
     }
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    if (!store[i]) continue;
-    if (whole) {
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int h = 0; h < EL; ++h) {
-        u32x4 w = yv[i][h];
-        if constexpr (F32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + acc[i][h][e]);
-        } else {
-          float v[8];
-          unpack8(w, v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = bf16_pair(v[2 * e] + acc[i][2 * h + e / 2][2 * (e % 2)], v[2 * e + 1] + acc[i][2 * h + e / 2][2 * (e % 2) + 1]);
-        }
-        ((u32x4 *)yp[i])[h] = w;
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        if (col + c >= a.n) continue;
-        if constexpr (F32) {
-          ((float *)yp[i])[c] += acc[i][c / 4][c % 4];
-        } else {
-          uint16_t *p = (uint16_t *)yp[i] + c;
-          *p = (uint16_t)bf16_pair(bf16_bits_to_f32(*p) + acc[i][c / 4][c % 4], 0.f);
-        }
-      }
-    }
+      for (int p = 0; p < PASSES; ++p) yv[i][p] = next[i][p];
   }
 }
 
-// Rows of an item: 64 where the adapters have that many on average, so that a
-// workgroup reads its adapter's columns once for more rows.
-static int lora_rows(int64_t m, int adapters) { return m >= 32ll * adapters ? 64 : 16; }
-static int64_t lora_items(int64_t m, int adapters) {
-  return std::min<int64_t>(adapters, m) + m / lora_rows(m, adapters);
-}
+template <int V>
+using Int = std::integral_constant<int, V>;
 
-// Parts of k: workgroups for the CUs, of at least 16 steps of 32 each.
+// Items at most: one per adapter with rows, and one more for every `rows` rows.
+static int64_t lora_items(int64_t m, int adapters, int rows) { return std::min<int64_t>(adapters, m) + m / rows; }
+
+// Parts of k: workgroups for the CUs, of at least 8 stages of 64 each.
 int lora_splits(int64_t m, int64_t k, int adapters) {
-  const int64_t want = std::max<int64_t>(256 / lora_items(m, adapters), 1), most = std::max<int64_t>((k + 511) / 512, 1);
+  const int64_t want = std::max<int64_t>(256 / lora_items(m, adapters, 16), 1), most = std::max<int64_t>((k + 511) / 512, 1);
   return (int)std::min<int64_t>(std::min(want, most), 16);
 }
 
-hipError_t launch_lora(const LoraArgs &a, bool y_f32, hipStream_t s) {
-  const int rows = lora_rows(a.m, a.adapters);
-  const unsigned items = (unsigned)lora_items(a.m, a.adapters);
-  auto down = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, dim3(items, a.splits), dim3(threads), 0, s, a); };
-  if (rows == 64)
-    a.rank <= 16    ? down(lora_down_kernel<1, 4, 1>, 256)
-    : a.rank <= 32  ? down(lora_down_kernel<2, 4, 1>, 256)
-    : a.rank <= 64  ? down(lora_down_kernel<4, 4, 1>, 256)
-    : a.rank <= 128 ? down(lora_down_kernel<8, 4, 1>, 256)
-                    : down(lora_down_kernel<16, 4, 1>, 256);
-  else
-    a.rank <= 16    ? down(lora_down_kernel<1, 1, 8>, 512)
-    : a.rank <= 32  ? down(lora_down_kernel<2, 1, 8>, 512)
-    : a.rank <= 64  ? down(lora_down_kernel<4, 1, 8>, 512)
-    : a.rank <= 128 ? down(lora_down_kernel<8, 1, 4>, 256)
-                    : down(lora_down_kernel<16, 1, 4>, 256);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int parts = y_f32 ? 3 : 2, lds = (parts * a.rank / 8 + 3) / 4 * 4 * rows * 16;
-  auto up = [&](auto kern) {
+hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  auto launch = [&](auto kern, const dim3 &grid, int threads, int lds) {
     e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((a.n + 255) / 256), items), dim3(256), lds, s, a);
+    hipLaunchKernelGGL(kern, grid, dim3(threads), lds, s, a);
     e = hipGetLastError();
   };
-  if (rows == 64)
-    y_f32 ? up(lora_up_kernel<4, true>) : up(lora_up_kernel<4, false>);
+  auto down = [&](auto blocks, auto waves, auto stages) {
+    constexpr int NB = decltype(blocks)::value, KW = decltype(waves)::value, ST = decltype(stages)::value;
+    launch(lora_down_kernel<NB, KW, ST>, dim3((unsigned)lora_items(a.m, a.adapters, 16), a.splits), 64 * KW,
+           KW * ST * (1 + NB) * 2048);
+  };
+  // (rings of 3 stages where two workgroups of them fit a CU)
+  if (a.rank <= 16)
+    down(Int<1>(), Int<4>(), Int<3>());
+  else if (a.rank <= 32)
+    down(Int<2>(), Int<4>(), Int<3>());
+  else if (a.rank <= 64)
+    down(Int<4>(), Int<4>(), Int<2>());
+  else if (a.rank <= 128)
+    down(Int<8>(), Int<4>(), Int<2>());
   else
-    y_f32 ? up(lora_up_kernel<1, true>) : up(lora_up_kernel<1, false>);
+    down(Int<16>(), Int<2>(), Int<2>());
+  if (e != hipSuccess) return e;
+
+  // Second product: rows of an item as many as the adapters have on average, as long
+  // as workgroups are left for the CUs.
+  const int64_t columns = (a.n + 255) / 256;
+  int rb = 4;
+  while (rb > 1 && (a.m < 8ll * rb * a.adapters || lora_items(a.m, a.adapters, 16 * rb) * columns < 1024)) rb /= 2;
+  const int64_t rows = lora_items(a.m, a.adapters, 16 * rb);
+  // Chunks of a workgroup: rounds of the CUs times the chunks and what comes ahead
+  // of them (of the items that may be, half of the adapters' last ones are there).
+  // Many rows: workgroups side by side a multiple of the XCDs, each of which then
+  // reads its own columns of B (4096 rows, n 14336, rank 64: 8 side by side 54.9 us,
+  // 10 67.5, 19 62.3, 56 64.4; 44 rows of 35 adapters: 56 11.4, 28 8.3, 19 9.1).
+  const double expected = (double)a.m / (16 * rb) + 0.5 * (double)std::min<int64_t>(a.adapters, a.m);
+  const int places = 256 * (rb == 4 ? (y_f32 ? 2 : 3) : rb == 2 ? (y_f32 ? 3 : 4) : 5);
+  double best = 0;
+  for (int64_t c = 1; c <= std::min<int64_t>(columns, 32); ++c) {
+    const int64_t side = (columns + c - 1) / c;
+    const double cost = std::ceil(expected * side / places) * (c + 1) * (rb > 1 && side % kXcds != 0 ? 1.25 : 1.);
+    if (c > 1 && cost >= best) continue;
+    best = cost;
+    a.chunks = (int32_t)c;
+  }
+  const int units = a.rank / 8, parts = y_f32 ? 3 : 2;
+  const int sd = units <= 4 ? 1 : units <= 8 ? 2 : 4;
+  const int lds_units = units <= 2 ? (parts * units + 3) / 4 * 4 : parts * ((units + 4 * sd - 1) / (4 * sd)) * 4 * sd;
+  const int lds = lds_units * (16 * rb + 1) * 16 + 4 * 16 * (64 * 4 + 16);
+  const dim3 grid((unsigned)((columns + a.chunks - 1) / a.chunks), (unsigned)rows);
+  auto up = [&](auto blocks, auto steps) {
+    constexpr int RB = decltype(blocks)::value, SD = decltype(steps)::value;
+    y_f32 ? launch(lora_up_kernel<RB, SD, true>, grid, 256, lds) : launch(lora_up_kernel<RB, SD, false>, grid, 256, lds);
+  };
+  auto with_rows = [&](auto blocks) {
+    if (sd == 1)
+      up(blocks, Int<1>());
+    else if (sd == 2)
+      up(blocks, Int<2>());
+    else
+      up(blocks, Int<4>());
+  };
+  if (rb == 4)
+    with_rows(Int<4>());
+  else if (rb == 2)
+    with_rows(Int<2>());
+  else
+    with_rows(Int<1>());
   return e;
 }
 
