@@ -362,7 +362,7 @@ int lora_splits(int64_t m, int64_t k, int adapters) {
 hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s) {
   hipError_t e = hipSuccess;
   auto launch = [&](auto kern, const dim3 &grid, int threads, int lds) {
-    e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (lds > 64 * 1024) e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return;
     hipLaunchKernelGGL(kern, grid, dim3(threads), lds, s, a);
     e = hipGetLastError();

@@ -56,10 +56,19 @@ __device__ __forceinline__ void store8(void *row, int64_t c, const float (&v)[8]
   }
 }
 
-// Sum of a and, MAX, maximum of b (else its sum) over the TEAM threads of a row.
+// e4m3 codes of 8 values times 1 / scale
+__device__ __forceinline__ uint2 e4m3_8(const float (&v)[8], float inv) {
+  uint32_t c[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    c[h] = e4m3_pair(v[4 * h] * inv, v[4 * h + 1] * inv) | (e4m3_pair(v[4 * h + 2] * inv, v[4 * h + 3] * inv) << 16);
+  return uint2{c[0], c[1]};
+}
+
+// Sum of a and, MAX, maximum of b (else its sum) over the threads of a row.
 // red: 2 x 2 x 16 floats, of which rows in turn use one half each: the barrier of
 // one row lies between another's reads and the next writes of its half.
-template <int TEAM, bool MAX>
+template <bool WAVE, bool MAX>
 __device__ __forceinline__ void team_reduce(float &a, float &b, float (*red)[2][16], int half) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -67,7 +76,7 @@ __device__ __forceinline__ void team_reduce(float &a, float &b, float (*red)[2][
     const float o = __shfl_xor(b, off);
     b = MAX ? fmaxf(b, o) : b + o;
   }
-  if constexpr (TEAM > 64) {
+  if constexpr (!WAVE) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
       red[half][0][wave] = a;
@@ -76,8 +85,7 @@ __device__ __forceinline__ void team_reduce(float &a, float &b, float (*red)[2][
     __syncthreads();
     a = red[half][0][0];
     b = red[half][1][0];
-#pragma unroll
-    for (int w = 1; w < TEAM / 64; ++w) {
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) {
       a += red[half][0][w];
       b = MAX ? fmaxf(b, red[half][1][w]) : b + red[half][1][w];
     }
@@ -86,19 +94,20 @@ __device__ __forceinline__ void team_reduce(float &a, float &b, float (*red)[2][
 
 }  // namespace
 
-// TEAM threads hold VEC x 8 values each of a row; LONG: what lies behind them is
-// read twice.  RES: 0 no residual and no sum, 1 bf16, 2 fp32.
-template <int TEAM, int TEAMS, int VEC, bool LONG, bool XF32, int RES>
-__global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
-  static_assert(TEAMS == 1 || TEAM == 64, "rows of one wave share workgroups");
+// The threads of a row (a wave, or TEAMS 1: the workgroup) hold VEC x 8 values each;
+// LONG: what lies behind them is read twice.  RES: 0 no residual and no sum, 1 bf16,
+// 2 fp32.
+template <int TEAMS, int VEC, bool LONG, bool XF32, int RES>
+__global__ __launch_bounds__(TEAMS > 1 ? 64 * TEAMS : 1024) void rmsnorm_kernel(NormArgs a) {
   __shared__ float red[2][2][16];
-  const int t = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int team_size = TEAMS > 1 ? 64 : blockDim.x;
+  const int t = TEAMS > 1 ? threadIdx.x & 63 : threadIdx.x;
   const int k8 = (int)(a.k / 8);
   u32x4 wv[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) wv[v] = ((const u32x4 *)a.w)[min(v * TEAM + t, k8 - 1)];
+  for (int v = 0; v < VEC; ++v) wv[v] = ((const u32x4 *)a.w)[min(v * team_size + t, k8 - 1)];
   int half = 0;
-  for (int64_t row = blockIdx.x * TEAMS + (TEAM == 64 ? threadIdx.x >> 6 : 0); row < a.rows;
+  for (int64_t row = blockIdx.x * TEAMS + (TEAMS > 1 ? threadIdx.x >> 6 : 0); row < a.rows;
        row += (int64_t)gridDim.x * TEAMS, half ^= 1) {
     const uint8_t *xr = (const uint8_t *)a.x + row * a.ldx * (XF32 ? 4 : 2);
     const uint8_t *rr = (const uint8_t *)a.res + row * a.ldr * (RES == 2 ? 4 : 2);
@@ -132,7 +141,7 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
     Raw8<RES == 2> res[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const int c = min(v * TEAM + t, k8 - 1);
+      const int c = min(v * team_size + t, k8 - 1);
       x[v].load(xr, c);
       if constexpr (RES != 0)
         if (a.res) res[v].load(rr, c);
@@ -140,7 +149,7 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
     float s[VEC][8];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const int c = v * TEAM + t;
+      const int c = v * team_size + t;
       total(c, c < k8, x[v], res[v], s[v]);
       count(c < k8, s[v], wv[v]);
     }
@@ -163,18 +172,19 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
       total(c, !again, xl, rl, s8);
     };
     if constexpr (LONG)
-      for (int c = VEC * TEAM + t; c < k8; c += TEAM) {
+      for (int c = VEC * team_size + t; c < k8; c += team_size) {
         float s8[8];
         later(c, false, s8);
         count(true, s8, ((const u32x4 *)a.w)[c]);
       }
-    team_reduce<TEAM, true>(ss, most, red, half);
+    team_reduce<(TEAMS > 1), true>(ss, most, red, half);
     const float r = 1.f / sqrtf(ss / (float)a.k + a.eps);
     most *= r;
     float scale = 1.f;
     if (most > 0.f && a.q_type == QG_A_INT8_TOKEN) scale = fmaxf(most / 127.f, kLeastScale);
     if (most > 0.f && a.q_type == QG_A_FP8_TOKEN) scale = fmaxf(most / 448.f, kLeastScale);
     if (t == 0 && (a.q_type == QG_A_INT8_TOKEN || a.q_type == QG_A_FP8_TOKEN)) ((float *)a.qs)[row] = scale;
+    const float inv_scale = 1.f / scale;
     uint8_t *qr = a.q + row * a.ldq;
     // outputs of chunk c (every lane of the wave comes here: blocks are reduced over lanes)
     auto emit = [&](int c, bool ok, const float (&s8)[8], const u32x4 &w) {
@@ -186,9 +196,12 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
       if (a.q_type == QG_A_BF16) return;
       uint2 codes;
       if (a.q_type == QG_A_INT8_TOKEN) {
-        codes = uint2{i8_codes4(y, scale), i8_codes4(y + 4, scale)};
+        uint32_t c8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c8[i] = (uint32_t)(int)rintf(y[i] * inv_scale) & 255u;
+        codes = uint2{c8[0] | c8[1] << 8 | c8[2] << 16 | c8[3] << 24, c8[4] | c8[5] << 8 | c8[6] << 16 | c8[7] << 24};
       } else if (a.q_type == QG_A_FP8_TOKEN) {
-        codes = fp8_store8(y, scale);
+        codes = e4m3_8(y, inv_scale);
       } else {
         float m = 0.f;
 #pragma unroll
@@ -198,26 +211,21 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
 #pragma unroll
           for (int off = 1; off < 16; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
           const float bs = m > 0.f ? fmaxf(m / 448.f, kLeastScale) : 1.f;
-          codes = fp8_store8(y, bs);
+          codes = e4m3_8(y, 1.f / bs);
           if (ok && (t & 15) == 0) ((float *)a.qs)[row * ((k8 + 15) / 16) + c / 16] = bs;
         } else {  // MXFP8, 32 values: 4 lanes
           const int e = mx_block_exp(quad_max(__float_as_uint(m)));
           const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-          uint32_t cw[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            cw[h] = e4m3_pair(y[4 * h] * inv, y[4 * h + 1] * inv) |
-                    (e4m3_pair(y[4 * h + 2] * inv, y[4 * h + 3] * inv) << 16);
-          codes = uint2{cw[0], cw[1]};
+          codes = e4m3_8(y, inv);
           if (ok && (t & 3) == 0) ((uint8_t *)a.qs)[row * (k8 / 4) + c / 4] = (uint8_t)(e + 127);
         }
       }
       if (ok) *(uint2 *)(qr + 8 * (int64_t)c) = codes;
     };
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) emit(v * TEAM + t, v * TEAM + t < k8, s[v], wv[v]);
+    for (int v = 0; v < VEC; ++v) emit(v * team_size + t, v * team_size + t < k8, s[v], wv[v]);
     if constexpr (LONG)
-      for (int c0 = VEC * TEAM; c0 < k8; c0 += TEAM) {
+      for (int c0 = VEC * team_size; c0 < k8; c0 += team_size) {
         const int c = c0 + t;
         float s8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         u32x4 w = {0u, 0u, 0u, 0u};
@@ -233,11 +241,12 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_kernel(NormArgs a) {
 // Backward pass: every workgroup sums dy s r of its rows, in registers, and leaves
 // one row of `partial` ([gridDim.x][k] fp32), which rmsnorm_dw_kernel adds up in
 // order.  LONG: what lies behind the registers is summed in `partial` itself.
-template <int TEAM, int TEAMS, int VEC, bool LONG, bool SF32>
-__global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackArgs a) {
+template <int TEAMS, int VEC, bool LONG, bool SF32>
+__global__ __launch_bounds__(TEAMS > 1 ? 64 * TEAMS : 1024) void rmsnorm_backward_kernel(NormBackArgs a) {
   __shared__ float red[2][2][16];
   __shared__ float join[TEAMS > 1 ? TEAMS * VEC * 64 * 8 : 1];
-  const int t = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x, team = TEAM == 64 ? threadIdx.x >> 6 : 0;
+  const int team_size = TEAMS > 1 ? 64 : blockDim.x;
+  const int t = TEAMS > 1 ? threadIdx.x & 63 : threadIdx.x, team = TEAMS > 1 ? threadIdx.x >> 6 : 0;
   const int k8 = (int)(a.k / 8);
   constexpr int EL = SF32 ? 4 : 2;
   float *mine = a.partial ? a.partial + (int64_t)blockIdx.x * a.k : nullptr;
@@ -245,7 +254,7 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackA
   float dw[VEC][8];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    wv[v] = ((const u32x4 *)a.w)[min(v * TEAM + t, k8 - 1)];
+    wv[v] = ((const u32x4 *)a.w)[min(v * team_size + t, k8 - 1)];
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
   }
@@ -261,7 +270,7 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackA
     Raw8<false> dy[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const int c = min(v * TEAM + t, k8 - 1);
+      const int c = min(v * team_size + t, k8 - 1);
       s[v].load(sr, c);
       dy[v].load(dyr, c);
       if (a.dsum) ds[v].load(dsr, c);
@@ -280,16 +289,16 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackA
       }
     };
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) count(v * TEAM + t < k8, s[v], dy[v], wv[v]);
+    for (int v = 0; v < VEC; ++v) count(v * team_size + t < k8, s[v], dy[v], wv[v]);
     if constexpr (LONG)
-      for (int c = VEC * TEAM + t; c < k8; c += TEAM) {
+      for (int c = VEC * team_size + t; c < k8; c += team_size) {
         Raw8<SF32> sl;
         Raw8<false> dl;
         sl.load(sr, c);
         dl.load(dyr, c);
         count(true, sl, dl, ((const u32x4 *)a.w)[c]);
       }
-    team_reduce<TEAM, false>(ss, gs, red, half);
+    team_reduce<(TEAMS > 1), false>(ss, gs, red, half);
     const float r = 1.f / sqrtf(ss / (float)a.k + a.eps);
     const float back = r * r * (gs / (float)a.k);
     auto emit = [&](int c, bool ok, const Raw8<SF32> &s8, const Raw8<false> &d8, const Raw8<SF32> &ds8, const u32x4 &w,
@@ -308,9 +317,9 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackA
       if (a.dx && ok) store8<SF32>(dxr, c, out);
     };
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) emit(v * TEAM + t, v * TEAM + t < k8, s[v], dy[v], ds[v], wv[v], dw[v]);
+    for (int v = 0; v < VEC; ++v) emit(v * team_size + t, v * team_size + t < k8, s[v], dy[v], ds[v], wv[v], dw[v]);
     if constexpr (LONG)
-      for (int c = VEC * TEAM + t; c < k8; c += TEAM) {
+      for (int c = VEC * team_size + t; c < k8; c += team_size) {
         Raw8<SF32> sl, ol;
         Raw8<false> dl;
         sl.load(sr, c);
@@ -341,22 +350,26 @@ __global__ __launch_bounds__(TEAM *TEAMS) void rmsnorm_backward_kernel(NormBackA
   }
 #pragma unroll
   for (int v = 0; v < VEC; ++v)
-    if (v * TEAM + t < k8) store8<true>(mine, v * TEAM + t, dw[v]);
+    if (v * team_size + t < k8) store8<true>(mine, v * team_size + t, dw[v]);
 }
 
-// dw from `parts` rows of fp32 sums: 16 lanes side by side, 4 columns each, 16
-// lanes along the parts, joined in order.
+// dw from `parts` rows of fp32 sums: 8 lanes side by side, 4 columns each (a cache
+// line), 32 lanes along the parts, joined in order.  512 parts of 4096: 4 us (10 with
+// 16 lanes side by side and 64 workgroups).
 __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float *partial, int parts, int64_t k, void *dw, bool f32) {
-  __shared__ f32x4 join[16][16];
-  const int side = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 64 + 4 * side;
+  __shared__ f32x4 join[32][8];
+  const int side = threadIdx.x & 7, part = threadIdx.x >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 32 + 4 * side;
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  if (c < k)
-    for (int p = part; p < parts; p += 16) sum += *(const f32x4 *)(partial + p * k + c);
+  if (c < k) {
+#pragma unroll 8
+    for (int p = part; p < parts; p += 32) sum += *(const f32x4 *)(partial + p * k + c);
+  }
   join[part][side] = sum;
   __syncthreads();
   if (part != 0 || c >= k) return;
-  for (int o = 1; o < 16; ++o) sum += join[o][side];
+#pragma unroll
+  for (int o = 1; o < 32; ++o) sum += join[o][side];
   if (f32)
     *(f32x4 *)((float *)dw + c) = sum;
   else
@@ -365,46 +378,41 @@ __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float *partial, i
 
 namespace {
 
-// Calls go(team, teams, vec, long) with the shape for rows of k values.
+// Calls go(waves, rows per workgroup, vec, long) with the shape for rows of k
+// values: a wave each up to 1024 values, else the fewest waves that hold the row.
 template <typename F>
 void norm_shape(int64_t k, F &&go) {
+  auto call = [&](int waves, auto rows, auto vec, auto is_long) { go(waves, rows, vec, is_long); };
+  using std::false_type;
   using std::integral_constant;
-  auto call = [&](auto team, auto teams, auto vec, auto is_long) { go(team, teams, vec, is_long); };
-#define QG_NORM_SHAPE(T, N, V, L) \
-  call(integral_constant<int, T>(), integral_constant<int, N>(), integral_constant<int, V>(), integral_constant<bool, L>())
   if (k <= 512)
-    QG_NORM_SHAPE(64, 4, 1, false);
+    call(4, integral_constant<int, 4>(), integral_constant<int, 1>(), false_type());
   else if (k <= 1024)
-    QG_NORM_SHAPE(64, 4, 2, false);
+    call(4, integral_constant<int, 4>(), integral_constant<int, 2>(), false_type());
   else if (k <= 2048)
-    QG_NORM_SHAPE(256, 1, 1, false);
-  else if (k <= 4096)
-    QG_NORM_SHAPE(256, 1, 2, false);
-  else if (k <= 8192)
-    QG_NORM_SHAPE(512, 1, 2, false);
+    call((int)((k + 511) / 512), integral_constant<int, 1>(), integral_constant<int, 1>(), false_type());
   else if (k <= 16384)
-    QG_NORM_SHAPE(1024, 1, 2, false);
+    call((int)((k + 1023) / 1024), integral_constant<int, 1>(), integral_constant<int, 2>(), false_type());
   else
-    QG_NORM_SHAPE(1024, 1, 2, true);
-#undef QG_NORM_SHAPE
+    call(16, integral_constant<int, 1>(), integral_constant<int, 2>(), std::true_type());
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormArgs &a, bool x_f32, int res, hipStream_t s) {
-  norm_shape(a.k, [&](auto team, auto teams, auto vec, auto is_long) {
-    constexpr int T = decltype(team)::value, N = decltype(teams)::value, V = decltype(vec)::value;
+  norm_shape(a.k, [&](int waves, auto teams, auto vec, auto is_long) {
+    constexpr int N = decltype(teams)::value, V = decltype(vec)::value;
     constexpr bool L = decltype(is_long)::value;
     const unsigned grid = (unsigned)std::min<int64_t>((a.rows + N - 1) / N, 256 * 16);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(T * N), 0, s, a); };
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * waves), 0, s, a); };
     if (x_f32)
-      res == 0   ? go(rmsnorm_kernel<T, N, V, L, true, 0>)
-      : res == 1 ? go(rmsnorm_kernel<T, N, V, L, true, 1>)
-                 : go(rmsnorm_kernel<T, N, V, L, true, 2>);
+      res == 0   ? go(rmsnorm_kernel<N, V, L, true, 0>)
+      : res == 1 ? go(rmsnorm_kernel<N, V, L, true, 1>)
+                 : go(rmsnorm_kernel<N, V, L, true, 2>);
     else
-      res == 0   ? go(rmsnorm_kernel<T, N, V, L, false, 0>)
-      : res == 1 ? go(rmsnorm_kernel<T, N, V, L, false, 1>)
-                 : go(rmsnorm_kernel<T, N, V, L, false, 2>);
+      res == 0   ? go(rmsnorm_kernel<N, V, L, false, 0>)
+      : res == 1 ? go(rmsnorm_kernel<N, V, L, false, 1>)
+                 : go(rmsnorm_kernel<N, V, L, false, 2>);
   });
   return hipGetLastError();
 }
@@ -418,17 +426,17 @@ int64_t rmsnorm_back_parts(int64_t rows, int64_t k) {
 hipError_t launch_rmsnorm_backward(const NormBackArgs &a, bool s_f32, void *dw, bool dw_f32, hipStream_t s) {
   const unsigned parts = (unsigned)rmsnorm_back_parts(a.rows, a.k);
   if (a.rows > 0) {
-    norm_shape(a.k, [&](auto team, auto teams, auto vec, auto is_long) {
-      constexpr int T = decltype(team)::value, N = decltype(teams)::value, V = decltype(vec)::value;
+    norm_shape(a.k, [&](int waves, auto teams, auto vec, auto is_long) {
+      constexpr int N = decltype(teams)::value, V = decltype(vec)::value;
       constexpr bool L = decltype(is_long)::value;
-      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(parts), dim3(T * N), 0, s, a); };
-      s_f32 ? go(rmsnorm_backward_kernel<T, N, V, L, true>) : go(rmsnorm_backward_kernel<T, N, V, L, false>);
+      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(parts), dim3(64 * waves), 0, s, a); };
+      s_f32 ? go(rmsnorm_backward_kernel<N, V, L, true>) : go(rmsnorm_backward_kernel<N, V, L, false>);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (dw)
-    hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((unsigned)((a.k + 63) / 64)), dim3(256), 0, s, a.partial,
+    hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((unsigned)((a.k + 31) / 32)), dim3(256), 0, s, a.partial,
                        a.rows > 0 ? (int)parts : 0, a.k, dw, dw_f32);
   return hipGetLastError();
 }
