@@ -707,8 +707,9 @@ qg_status qg_linear_xent(const void *x, int64_t ldx, const void *w, int64_t ldw,
  *   dx   device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.
  *   dw   device, [vocab][lddw] of dw_type, 16-B aligned, lddw >= k, or NULL; it is
  *        overwritten; m == 0 fills it with zeros.
- *   ws   qg_linear_xent_backward_workspace_size bytes (some 130 MB and 4 m k, or
- *        16384 m + 4 m k where that is more), 256-B aligned, zero-filled once.
+ *   ws   qg_linear_xent_backward_workspace_size bytes (whatever the vocabulary at
+ *        most 128 MB or 16384 m for d, 80 MB or 4 m k for parts of dx, and 48 MB),
+ *        256-B aligned, zero-filled once.
  * An ignored row's dx is 0, and it adds nothing to dw as long as its x is finite.
  * Asynchronous on `stream`. */
 qg_status qg_linear_xent_backward_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);

@@ -492,6 +492,7 @@ struct XentCall {
   float *weight, *alpha;     // backward: [m], [1]
   void *d;                   // backward: bf16 [xent_d_rows][ldd], one piece
   int64_t ldd;
+  float *parts;              // backward: parts of dx, fp32 [][m][k]
 };
 int64_t xent_d_rows(int64_t m);
 int64_t xent_piece(int64_t m, int64_t vocab);
@@ -499,8 +500,9 @@ int64_t xent_piece(int64_t m, int64_t vocab);
 hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_xent_weights(const XentCall &c, const float *dloss, hipStream_t s);
 hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info = nullptr);
-hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, const float *add, int64_t ldadd, void *out,
-                          int out_type, int64_t ldout, hipStream_t s, MmInfo *info = nullptr);
+hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s,
+                          MmInfo *info = nullptr);
+hipError_t launch_xent_dx_sum(const XentCall &c, int parts, void *dx, int64_t lddx, hipStream_t s);
 hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, void *dw, int dw_type, int64_t lddw,
                           hipStream_t s, MmInfo *info = nullptr);
 // low-rank adapters (qg_lora.hip); strides in elements

@@ -133,12 +133,13 @@ struct XentSpace {
   uint64_t total() const { return kSplitCounterBytes + partials + stats + at_target; }
 };
 // Backward: [split-K counters][partial tiles][row weights][alpha][d of a
-// piece][dx in fp32, where there are several pieces].
+// piece][parts of dx].
 struct XentBackSpace {
   int64_t piece = 0;
-  uint64_t partials = 0, weight = 0, d = 0, dx = 0;
+  int splits = 1, last_splits = 1;  // parts of dx of a whole piece and of the last one
+  uint64_t partials = 0, weight = 0, d = 0, parts = 0;
   static constexpr uint64_t alpha = 256;
-  uint64_t total() const { return kSplitCounterBytes + partials + weight + alpha + d + dx; }
+  uint64_t total() const { return kSplitCounterBytes + partials + weight + alpha + d + parts; }
 };
 
 static bool xent_in_range(int64_t m, int64_t k, int64_t vocab) {
@@ -161,19 +162,21 @@ static XentBackSpace xent_back_space(const XentCall &c) {
   sp.piece = xent_piece(c.m, c.vocab);
   // the last piece may be shorter, and its products split otherwise
   const int64_t last = c.vocab - (c.vocab - 1) / sp.piece * sp.piece;
-  for (int64_t columns : {std::min(sp.piece, c.vocab), last}) {
+  auto count = [&](int64_t columns) {
     MmInfo i;
     (void)launch_xent_d(c, 0, columns, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
-    (void)launch_xent_dx(c, 0, columns, nullptr, 0, nullptr, 0, 0, nullptr, &i);
-    sp.partials = std::max(sp.partials, i.bytes);
     (void)launch_xent_dw(c, 0, columns, nullptr, 0, 0, nullptr, &i);
     sp.partials = std::max(sp.partials, i.bytes);
-  }
+    (void)launch_xent_dx(c, 0, columns, 0, nullptr, &i);
+    return i.splits;
+  };
+  sp.last_splits = count(last);
+  sp.splits = sp.piece < c.vocab ? count(sp.piece) : sp.last_splits;
   sp.partials = align_up(sp.partials, 256);
+  sp.parts = align_up((uint64_t)std::max(sp.splits, sp.last_splits) * c.m * c.k * 4, 256);
   sp.weight = align_up((uint64_t)c.m * 4, 256);
   sp.d = align_up((uint64_t)xent_d_rows(c.m) * sp.piece * 2, 256);
-  if (sp.piece < c.vocab) sp.dx = align_up((uint64_t)c.m * c.k * 4, 256);
   return sp;
 }
 
@@ -266,17 +269,14 @@ extern "C" qg_status qg_linear_xent_backward(const void *x, int64_t ldx, const v
   c.alpha = (float *)(p += sp.weight);
   c.d = p += sp.alpha;
   c.ldd = sp.piece;
-  float *sum = (float *)(p + sp.d);
+  c.parts = (float *)(p + sp.d);
   hipError_t e = launch_xent_weights(c, dloss, stream);
   for (int64_t first = 0; e == hipSuccess && first < vocab; first += sp.piece) {
     const int64_t columns = std::min(sp.piece, vocab - first);
     e = launch_xent_d(c, first, columns, stream);
-    const float *add = first > 0 ? sum : nullptr;
-    if (e == hipSuccess && dx && first + columns < vocab)
-      e = launch_xent_dx(c, first, columns, add, k, sum, QG_O_F32, k, stream);
-    else if (e == hipSuccess && dx)
-      e = launch_xent_dx(c, first, columns, add, k, dx, QG_O_BF16, lddx, stream);
+    if (e == hipSuccess && dx) e = launch_xent_dx(c, first, columns, first > 0 ? sp.splits : 0, stream);
     if (e == hipSuccess && dw) e = launch_xent_dw(c, first, columns, dw, dw_type, lddw, stream);
   }
+  if (e == hipSuccess && dx) e = launch_xent_dx_sum(c, std::max(sp.splits, sp.last_splits), dx, lddx, stream);
   return hip_status(e);
 }

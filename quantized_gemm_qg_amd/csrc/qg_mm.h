@@ -112,13 +112,16 @@ struct MmArgs {
   float scale;
   float *stats, *at_target;
   const float *lse, *row_weight;
-  // kScaled: y = alpha[0] times the product, plus `add` (fp32 [m][ldadd]) where given
-  const float *alpha, *add;
-  int64_t ldadd;
+  // kScaled: y = alpha[0] times the product.  kParts: split over k without a join,
+  // part p's sums go to y + p part_stride (fp32), on top of what is there where p <
+  // parts_there
+  const float *alpha;
+  int64_t part_stride;
+  int32_t parts_there;
 };
 
 // What is done with a tile's sums besides storing them.
-enum { kPlain = 0, kXentStats = 1, kXentGrad = 2, kScaled = 3 };
+enum { kPlain = 0, kXentStats = 1, kXentGrad = 2, kScaled = 3, kParts = 4 };
 
 // Partial tiles of a call take at most this much.
 constexpr uint64_t kMmPartialBytes = 48u << 20;
@@ -146,7 +149,8 @@ struct MmCfg {
   static constexpr int OUT_NB = GATED ? NB / 2 : NB;                  // 16-column blocks of a wave's output
   static constexpr int PITCH = 16 * OUT_NB * 4 + 16;                  // bytes of a slab row (fp32)
   static constexpr int SLAB = 16 * PITCH;
-  static constexpr int LDS = STAGE * ST > WAVES * SLAB ? STAGE * ST : WAVES * SLAB;
+  static constexpr int OUT = WAVES * SLAB + (EPI == kXentGrad ? 16 * BM : 0);  // slabs, rows' values
+  static constexpr int LDS = STAGE * ST > OUT ? STAGE * ST : OUT;
   static constexpr bool ROW_HALVES = !I8 && AF == kRows && BF == kCols && BM == 32, K_HALVES = AF == kCols;
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && (!GATED || NB % 2 == 0), "blocks");
   static_assert(!I8 || AF == kRows, "int8 activations are rows");
@@ -226,6 +230,12 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   if (!tile_of(pid, m_tiles, n_tiles, a.group_m, &tm, &tn)) return;
   const int m0 = tm * C::BM, n0 = tn * OUT_BN;
   const int rows = min(C::BM, a.m - m0);
+  static_assert(C::EPI != kXentGrad || C::THREADS >= C::BM, "a thread per row");
+  f32x4 my_row = {0.f, 0.f, 0.f, 0.f};  // kXentGrad: what the epilogue needs of this thread's row
+  if constexpr (C::EPI == kXentGrad) {
+    const int row = min(m0 + (int)threadIdx.x, a.m - 1);
+    my_row = f32x4{a.row_weight[row], a.lse[row] * 1.4426950408889634f, __int_as_float(a.targets[row] - a.first_token), 0.f};
+  }
 
   // B column of block jb of the tile (the up half of a gated tile starts at
   // column n), not clamped; and the last valid one of its half
@@ -445,7 +455,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   multiply(f[0]);
   multiply(f[1]);
 
-  if constexpr (C::SPLIT) {
+  if constexpr (C::SPLIT && C::EPI != kParts) {
     if (a.splits > 1) {
       // Publish this part of k (agent-scope stores, complete before the counter
       // moves); the last workgroup of the tile adds the parts in their order,
@@ -582,36 +592,36 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   // whole 16-byte units: the products that read it take units whole)
   const int n_out = C::EPI == kXentGrad ? (a.n + 7) & ~7 : a.n;
   // kXentGrad: per row its weight, the logarithm (base 2) of its sum and its target
-  float weight[C::EPI == kXentGrad ? C::MB : 1], log_sum[C::EPI == kXentGrad ? C::MB : 1];
-  int target[C::EPI == kXentGrad ? C::MB : 1];
+  float *row_info = (float *)(smem + C::WAVES * C::SLAB);  // [BM][4]
   if constexpr (C::EPI == kXentGrad) {
-#pragma unroll
-    for (int i = 0; i < C::MB; ++i) {
-      const int row = min(row_w + 16 * i + r16, a.m - 1);
-      weight[i] = a.row_weight[row];
-      log_sum[i] = a.lse[row] * 1.4426950408889634f;
-      target[i] = a.targets[row] - a.first_token;
-    }
+    if (threadIdx.x < C::BM) *(f32x4 *)(row_info + 4 * threadIdx.x) = my_row;
+    mm_barrier();
   }
   const float alpha = C::EPI == kScaled ? a.alpha[0] : 1.f;
+  if constexpr (C::EPI == kParts) a.y = (float *)a.y + split * a.part_stride;
   // fp32 values of block (i, j), scales applied
   auto value = [&](int i, int j) {
     f32x4 v;
     if constexpr (C::EPI == kXentGrad) {
       const float base2 = a.scale * 1.4426950408889634f;
       const int col = col_w + 16 * j + 4 * q;
+      const f32x4 info = *(const f32x4 *)(row_info + 4 * ((wm * C::MB + i) * 16 + r16));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], base2, -log_sum[i]));
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], base2, -info[1]));
         // (a weight of 0: nothing, whatever the logits are)
-        v[e] = weight[i] == 0.f || col + e >= a.n ? 0.f : weight[i] * (col + e == target[i] ? p - 1.f : p);
+        v[e] = info[0] == 0.f || col + e >= a.n ? 0.f : info[0] * (col + e == __float_as_int(info[2]) ? p - 1.f : p);
       }
       return v;
     }
     if constexpr (C::EPI == kScaled) {
       v = acc[i][j] * alpha;
+      return v;
+    }
+    if constexpr (C::EPI == kParts) {
+      v = acc[i][j];
       const int row = row_w + 16 * i + r16, col = col_w + 16 * j + 4 * q;
-      if (a.add && row < m_out && col < a.n) v += *(const f32x4 *)(a.add + row * a.ldadd + col);
+      if (split < a.parts_there && row < m_out && col < a.n) v += *(const f32x4 *)((const float *)a.y + row * a.ldy + col);
       return v;
     }
     if constexpr (C::I8) {
@@ -734,6 +744,8 @@ struct MmPlan {
   int splits = 1, per = 0;
   double cost = 0;
 };
+// Parts without a join in the kernel (kParts) cost their way to memory and back, by
+// all CUs, and a launch.
 template <class C>
 static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
@@ -747,7 +759,9 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;
   const double memory = (double)(m + (C::GATED ? 2 * n : n)) * kd * C::EL / 2100;
   MmPlan best;
-  const int64_t most = C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(budget / (uint64_t)(partial * tiles)) : 1;
+  const bool parts = C::EPI == kParts;
+  const int64_t most = parts ? (int64_t)(budget / (uint64_t)(4 * m * n))
+                       : C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(budget / (uint64_t)(partial * tiles)) : 1;
   for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), 32); ++want) {
     const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
     if (splits != want) continue;  // the same as a smaller number of parts
@@ -755,7 +769,10 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
     if (splits > 1 && rounds > 1) break;  // (more parts than places: slower than fewer)
     const double stages = (double)per * std::max(wgs * matrix, rounds * latency);
     double cost = std::sqrt(stages * stages + memory * memory) + 4000. * wgs;
-    if (splits > 1) cost += 6000 + splits * partial / 24;
+    if (parts)
+      cost += splits > 1 ? 8000 + (double)splits * m * n * 8 / 2100 : 0;
+    else if (splits > 1)
+      cost += 6000 + splits * partial / 24;
     if (best.per == 0 || cost < best.cost) best = MmPlan{(int)splits, (int)per, cost};
   }
   return best;
@@ -764,6 +781,7 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
 template <class C>
 static uint64_t mm_partial_bytes(int64_t m, int64_t n, const MmPlan &p) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+  if (C::EPI == kParts) return p.splits > 1 ? (uint64_t)p.splits * m * n * 4 : 0;
   return p.splits > 1 ? (uint64_t)p.splits * ((m + C::BM - 1) / C::BM) * ((n + OUT_BN - 1) / OUT_BN) * C::BM * C::BN * 4
                       : 0;
 }
@@ -774,7 +792,7 @@ static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) 
   MmArgs a = args;
   a.splits = p.splits;
   a.per = p.per;
-  if (p.splits > 1 && (!a.counters || !a.partials)) return hipErrorInvalidValue;
+  if (p.splits > 1 && C::EPI != kParts && (!a.counters || !a.partials)) return hipErrorInvalidValue;
   const int64_t total = (int64_t)((a.m + C::BM - 1) / C::BM) * ((a.n + OUT_BN - 1) / OUT_BN);
   const int64_t grid = (total + kXcds - 1) / kXcds * kXcds * p.splits;
   auto kern = mm_kernel<C>;

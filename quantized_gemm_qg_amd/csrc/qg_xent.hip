@@ -22,43 +22,73 @@
 namespace qg {
 
 // lse and loss from the statistics of every tile of columns ([tiles][m] of largest
-// logit and sum): 16 rows side by side, 64 lanes along the tiles.
+// logit and sum): 16 rows side by side, 64 lanes along the tiles, joined as a tree.
 __global__ __launch_bounds__(1024) void xent_join_kernel(const float2 *stats, const float *at_target, int tiles, int m,
                                                          int vocab, const int32_t *targets, float scale, float *loss,
                                                          float *lse) {
-  __shared__ float2 join[64][16];
+  __shared__ float2 join[16][16];
   const int side = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int row = blockIdx.x * 16 + side;
+  const int row = blockIdx.x * 16 + side, at = min(row, m - 1);
   const float base2 = scale * 1.4426950408889634f;
   float most = -INFINITY, sum = 0.f;
-  auto add = [&](const float2 &v) {
-    const float big = fmaxf(most, v.x), from = big == -INFINITY ? 0.f : big;
-    sum = sum * __builtin_amdgcn_exp2f((most - from) * base2) + v.y * __builtin_amdgcn_exp2f((v.x - from) * base2);
-    most = big;
+  auto add = [&](float big, float s) {
+    const float both = fmaxf(most, big), from = both == -INFINITY ? 0.f : both;
+    sum = sum * __builtin_amdgcn_exp2f((most - from) * base2) + s * __builtin_amdgcn_exp2f((big - from) * base2);
+    most = both;
   };
-  if (row < m) {
-    constexpr int GO = 8;  // loads out together
-    for (int t0 = part; t0 < tiles; t0 += 64 * GO) {
-      float2 v[GO];
+  auto join_lanes = [&] {
 #pragma unroll
-      for (int g = 0; g < GO; ++g) v[g] = stats[(int64_t)min(t0 + 64 * g, tiles - 1) * m + row];
+    for (int off = 16; off < 64; off <<= 1) add(__shfl_xor(most, off), __shfl_xor(sum, off));
+  };
+  const int t = targets ? targets[at] : -1;
+  const bool counts = t >= 0 && t < vocab;
+  const float hit = loss && counts ? at_target[at] : 0.f;
+  constexpr int GO = 8;  // loads out together
+  for (int t0 = part; t0 < tiles; t0 += 64 * GO) {
+    float2 v[GO];
 #pragma unroll
-      for (int g = 0; g < GO; ++g)
-        if (t0 + 64 * g < tiles) add(v[g]);
-    }
+    for (int g = 0; g < GO; ++g) v[g] = stats[(int64_t)min(t0 + 64 * g, tiles - 1) * m + at];
+#pragma unroll
+    for (int g = 0; g < GO; ++g)
+      if (t0 + 64 * g < tiles) add(v[g].x, v[g].y);
   }
-  join[part][side] = float2{most, sum};
+  join_lanes();
+  if ((threadIdx.x & 63) < 16) join[threadIdx.x >> 6][side] = float2{most, sum};
   __syncthreads();
-  if (part != 0 || row >= m) return;
-  for (int o = 1; o < 64; ++o) add(join[o][side]);
-  const float log_sum = logf(sum);
+  if (threadIdx.x >= 64) return;
+  const int first = threadIdx.x >> 4;
+  most = join[first][side].x;
+  sum = join[first][side].y;
+#pragma unroll
+  for (int o = 4; o < 16; o += 4) add(join[first + o][side].x, join[first + o][side].y);
+  join_lanes();
+  if (threadIdx.x >= 16 || row >= m) return;
   // (nothing but NaN logits: `most` is -inf and the sum NaN)
+  const float log_sum = logf(sum);
   if (lse) lse[row] = __builtin_fmaf(scale, most, log_sum);
-  if (loss) {
-    const int t = targets[row];
-    // (an ignored row's loss is 0; scale (largest - target's) is exact where the two are near)
-    loss[row] = t >= 0 && t < vocab ? __builtin_fmaf(scale, most - at_target[row], log_sum) : 0.f;
+  // (an ignored row's loss is 0; scale (largest - target's) is exact where the two are near)
+  if (loss) loss[row] = counts ? __builtin_fmaf(scale, most - hit, log_sum) : 0.f;
+}
+
+// dx (bf16) = alpha times the sum of `parts` fp32 matrices [m][k], in order; k % 8 ==
+// 0, 8 values per thread.
+__global__ __launch_bounds__(256) void xent_dx_kernel(const float *p, int parts, int64_t stride, int64_t k8, int64_t units,
+                                                      const float *alpha, uint16_t *dx, int64_t lddx) {
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (u >= units) return;
+  const float by = alpha[0];
+  f32x4 sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const f32x4 *v = (const f32x4 *)(p + s * stride) + 2 * u;
+    sum[0] += v[0];
+    sum[1] += v[1];
   }
+  const int64_t row = u / k8, c8 = u - row * k8;
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = bf16_rne(by * sum[e / 2][e % 2 * 2]) | bf16_rne(by * sum[e / 2][e % 2 * 2 + 1]) << 16;
+  *(u32x4_any *)(dx + row * lddx + 8 * c8) = w;  // (rows of dx start at any element)
 }
 
 // Row weights dloss / c (0 for ignored rows) and alpha = scale c, c the largest
@@ -80,6 +110,9 @@ __global__ __launch_bounds__(1024) void xent_weights_kernel(const float *dloss, 
     weight[r] = targets[r] >= 0 && targets[r] < vocab ? dloss[r] / c : 0.f;
   if (threadIdx.x == 0) alpha[0] = scale * c;
 }
+
+// Parts of dx take at most this much (or one part).
+constexpr uint64_t kXentPartBytes = 80u << 20;
 
 static int64_t xent_halves(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 0; }
 int64_t xent_d_rows(int64_t m) { return m + xent_halves(m); }
@@ -160,30 +193,38 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
   return xent_logits<kXentGrad>(a, s, info);
 }
 
-// dx from one piece: out (bf16 or fp32) = alpha d W (+ add)
-hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, const float *add, int64_t ldadd, void *out,
-                          int out_type, int64_t ldout, hipStream_t s, MmInfo *info) {
+// d W of one piece into parts of dx.  The contraction is long and the tiles are
+// few: parts of it in fp32, which a kernel of all CUs adds up behind the last piece
+// (one workgroup per tile would read 4 MB of 16 parts by itself).
+// info->splits: how many parts the piece has; there: how many hold earlier pieces.
+hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s, MmInfo *info) {
   MmArgs a = xent_args(c, first, columns);
   a.a = (const uint8_t *)c.d;
   a.lda = c.ldd * 2;
   a.n = (int32_t)c.k;
   a.kd = (int32_t)columns;
-  a.alpha = c.alpha;
-  a.add = add;
-  a.ldadd = ldadd;
-  a.y = out;
-  a.otype = out_type;
-  a.ldy = ldout;
-  using Few = MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true, kScaled>;
+  a.y = c.parts;
+  a.otype = QG_O_F32;
+  a.ldy = c.k;
+  a.part_stride = c.m * c.k;
+  a.parts_there = there;
+  using Few = MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true, kParts>;
   if (c.m <= 16) {
     a.halves = (int32_t)xent_halves(c.m);
     a.m += a.halves;
-    return mm_dispatch<Few>(a, kMmPartialBytes, s, info);
+    return mm_dispatch<Few>(a, kXentPartBytes, s, info);
   }
-  return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, false, kScaled>,
-                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true, kScaled>,
-                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true, kScaled>,
-                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true, kScaled>, Few>(a, kMmPartialBytes, s, info);
+  return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, true, kParts>,
+                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true, kParts>,
+                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true, kParts>,
+                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true, kParts>, Few>(a, kXentPartBytes, s, info);
+}
+
+hipError_t launch_xent_dx_sum(const XentCall &c, int parts, void *dx, int64_t lddx, hipStream_t s) {
+  const int64_t units = c.m * c.k / 8;
+  hipLaunchKernelGGL(xent_dx_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s, (const float *)c.parts, parts,
+                     c.m * c.k, c.k / 8, units, c.alpha, (uint16_t *)dx, lddx);
+  return hipGetLastError();
 }
 
 // rows of dW of one piece
