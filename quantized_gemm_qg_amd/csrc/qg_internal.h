@@ -489,7 +489,8 @@ struct XentCall {
   uint32_t *counters;  // split-K counters and partial tiles
   void *partials;
   float *stats, *at_target;  // forward: [tiles of columns][m][2], [m]
-  float *weight, *alpha;     // backward: [m], [1]
+  const float *dloss;        // backward: [m]
+  float *alpha;              // backward: [1]
   void *d;                   // backward: bf16 [xent_d_rows][ldd], one piece
   int64_t ldd;
   float *parts;              // backward: parts of dx, fp32 [][m][k]
@@ -498,7 +499,6 @@ int64_t xent_d_rows(int64_t m);
 int64_t xent_piece(int64_t m, int64_t vocab);
 // info: NULL, or nothing is launched and the choice reported
 hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info = nullptr);
-hipError_t launch_xent_weights(const XentCall &c, const float *dloss, hipStream_t s);
 hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info = nullptr);
 hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s,
                           MmInfo *info = nullptr);

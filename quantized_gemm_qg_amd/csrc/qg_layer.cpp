@@ -132,14 +132,13 @@ struct XentSpace {
   uint64_t partials = 0, stats = 0, at_target = 0;  // bytes
   uint64_t total() const { return kSplitCounterBytes + partials + stats + at_target; }
 };
-// Backward: [split-K counters][partial tiles][row weights][alpha][d of a
-// piece][parts of dx].
+// Backward: [split-K counters][partial tiles][alpha][d of a piece][parts of dx].
 struct XentBackSpace {
   int64_t piece = 0;
   int splits = 1, last_splits = 1;  // parts of dx of a whole piece and of the last one
-  uint64_t partials = 0, weight = 0, d = 0, parts = 0;
+  uint64_t partials = 0, d = 0, parts = 0;
   static constexpr uint64_t alpha = 256;
-  uint64_t total() const { return kSplitCounterBytes + partials + weight + alpha + d + parts; }
+  uint64_t total() const { return kSplitCounterBytes + partials + alpha + d + parts; }
 };
 
 static bool xent_in_range(int64_t m, int64_t k, int64_t vocab) {
@@ -175,7 +174,6 @@ static XentBackSpace xent_back_space(const XentCall &c) {
   sp.splits = sp.piece < c.vocab ? count(sp.piece) : sp.last_splits;
   sp.partials = align_up(sp.partials, 256);
   sp.parts = align_up((uint64_t)std::max(sp.splits, sp.last_splits) * c.m * c.k * 4, 256);
-  sp.weight = align_up((uint64_t)c.m * 4, 256);
   sp.d = align_up((uint64_t)xent_d_rows(c.m) * sp.piece * 2, 256);
   return sp;
 }
@@ -262,15 +260,15 @@ extern "C" qg_status qg_linear_xent_backward(const void *x, int64_t ldx, const v
   const XentBackSpace sp = xent_back_space(c);
   QG_TRY(ws_check(sp.total(), ws, ws_bytes));
   c.lse = const_cast<float *>(lse);
+  c.dloss = dloss;
   uint8_t *p = (uint8_t *)ws;
   c.counters = (uint32_t *)p;
   c.partials = p += kSplitCounterBytes;
-  c.weight = (float *)(p += sp.partials);
-  c.alpha = (float *)(p += sp.weight);
+  c.alpha = (float *)(p += sp.partials);
   c.d = p += sp.alpha;
   c.ldd = sp.piece;
   c.parts = (float *)(p + sp.d);
-  hipError_t e = launch_xent_weights(c, dloss, stream);
+  hipError_t e = hipSuccess;
   for (int64_t first = 0; e == hipSuccess && first < vocab; first += sp.piece) {
     const int64_t columns = std::min(sp.piece, vocab - first);
     e = launch_xent_d(c, first, columns, stream);

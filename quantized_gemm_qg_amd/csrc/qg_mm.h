@@ -106,12 +106,15 @@ struct MmArgs {
   // cross entropy of a head (kXentStats, kXentGrad): y's columns are the logits of
   // tokens first_token ..; kXentStats leaves the largest logit and the sum of
   // exponentials of every row and tile in stats [tile][m] and the target's logit
-  // in at_target; kXentGrad writes row_weight (softmax - target)
+  // in at_target; kXentGrad writes weight (softmax - target), weight the rows' dloss
+  // over their largest, alpha_out = scale times that
   const int32_t *targets;
   int32_t first_token;
   float scale;
   float *stats, *at_target;
-  const float *lse, *row_weight;
+  const float *lse, *dloss;
+  float *alpha_out;
+  int32_t vocab;
   // kScaled: y = alpha[0] times the product.  kParts: split over k without a join,
   // part p's sums go to y + p part_stride (fp32), on top of what is there where p <
   // parts_there
@@ -232,9 +235,18 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   const int rows = min(C::BM, a.m - m0);
   static_assert(C::EPI != kXentGrad || C::THREADS >= C::BM, "a thread per row");
   f32x4 my_row = {0.f, 0.f, 0.f, 0.f};  // kXentGrad: what the epilogue needs of this thread's row
+  __shared__ float most_of[C::EPI == kXentGrad ? C::WAVES : 1];
+  float dloss_most = 0.f;
   if constexpr (C::EPI == kXentGrad) {
+    // (every workgroup looks for the largest |dloss| of the rows that count: a launch
+    // of its own for it took 5 us)
+    auto dloss_of = [&](int r) { return (uint32_t)a.targets[r] < (uint32_t)a.vocab ? a.dloss[r] : 0.f; };
+    for (int r = threadIdx.x; r < a.m; r += C::THREADS) dloss_most = fmaxf(dloss_most, fabsf(dloss_of(r)));
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) dloss_most = fmaxf(dloss_most, __shfl_xor(dloss_most, off));
+    if (lane == 0) most_of[wave] = dloss_most;
     const int row = min(m0 + (int)threadIdx.x, a.m - 1);
-    my_row = f32x4{a.row_weight[row], a.lse[row] * 1.4426950408889634f, __int_as_float(a.targets[row] - a.first_token), 0.f};
+    my_row = f32x4{dloss_of(row), a.lse[row] * 1.4426950408889634f, __int_as_float(a.targets[row] - a.first_token), 0.f};
   }
 
   // B column of block jb of the tile (the up half of a gated tile starts at
@@ -454,6 +466,14 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
   read(steps - 1, 1, f[1]);
   multiply(f[0]);
   multiply(f[1]);
+
+  if constexpr (C::EPI == kXentGrad) {
+    // (the loop's barriers lie between most_of's writes and this)
+    for (int w = 0; w < C::WAVES; ++w) dloss_most = fmaxf(dloss_most, most_of[w]);
+    const float c = dloss_most >= 0x1p-126f && dloss_most < INFINITY ? dloss_most : 1.f;
+    my_row[0] /= c;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.alpha_out[0] = a.scale * c;
+  }
 
   if constexpr (C::SPLIT && C::EPI != kParts) {
     if (a.splits > 1) {

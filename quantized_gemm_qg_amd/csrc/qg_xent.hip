@@ -91,26 +91,6 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const float *p, int parts,
   *(u32x4_any *)(dx + row * lddx + 8 * c8) = w;  // (rows of dx start at any element)
 }
 
-// Row weights dloss / c (0 for ignored rows) and alpha = scale c, c the largest
-// |dloss| of the rows that count (1 where that is 0 or not finite).
-__global__ __launch_bounds__(1024) void xent_weights_kernel(const float *dloss, const int32_t *targets, int m, int vocab,
-                                                            float scale, float *weight, float *alpha) {
-  __shared__ float wave_max[16];
-  float most = 0.f;
-  for (int r = threadIdx.x; r < m; r += 1024)
-    if (targets[r] >= 0 && targets[r] < vocab) most = fmaxf(most, fabsf(dloss[r]));
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) most = fmaxf(most, __shfl_xor(most, off));
-  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = most;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 16; ++w) most = fmaxf(most, wave_max[w]);
-  const float c = most >= 0x1p-126f && most < INFINITY ? most : 1.f;
-  for (int r = threadIdx.x; r < m; r += 1024)
-    weight[r] = targets[r] >= 0 && targets[r] < vocab ? dloss[r] / c : 0.f;
-  if (threadIdx.x == 0) alpha[0] = scale * c;
-}
-
 // Parts of dx take at most this much (or one part).
 constexpr uint64_t kXentPartBytes = 80u << 20;
 
@@ -174,17 +154,14 @@ hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_weights(const XentCall &c, const float *dloss, hipStream_t s) {
-  hipLaunchKernelGGL(xent_weights_kernel, dim3(1), dim3(1024), 0, s, dloss, c.targets, (int)c.m, (int)c.vocab, c.scale,
-                     c.weight, c.alpha);
-  return hipGetLastError();
-}
-
 // d of one piece
+// (and alpha, by the workgroup of the first tile)
 hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info) {
   MmArgs a = xent_args(c, first, columns);
   a.lse = c.lse;
-  a.row_weight = c.weight;
+  a.dloss = c.dloss;
+  a.alpha_out = c.alpha;
+  a.vocab = (int32_t)c.vocab;
   a.y = c.d;
   a.ldy = c.ldd;
   a.otype = QG_O_BF16;

@@ -156,6 +156,16 @@ def test_forward_and_backward(m, k, vocab):
     assert torch.equal(dw16, got_dw.to(torch.bfloat16))
 
 
+# every tile shape of the three products, whole and in parts of the contraction
+TILES = [(33, 16, 34), (34, 16, 32871), (1379, 16, 1204), (686, 16, 35037), (909, 1216, 30), (2747, 1800, 30), (2713, 808, 678),
+         (2803, 2832, 264), (579, 3280, 7231), (2315, 3408, 954), (2953, 1408, 3564)]
+
+
+@pytest.mark.parametrize("m,k,vocab", TILES)
+def test_every_tile_shape(m, k, vocab):
+    test_forward_and_backward(m, k, vocab)
+
+
 @pytest.mark.parametrize("m,k,vocab", [(1, 8, 1100000), (20, 16, 1100001), (9000, 64, 20003), (40, 24, 2200000)])
 def test_several_pieces(m, k, vocab):
     print(f"xent pieces m={m} k={k} vocab={vocab}", flush=True)
