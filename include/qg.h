@@ -615,9 +615,10 @@ qg_status qg_token_logprobs_backward(const void *logits, int32_t ltype, int64_t 
  *   y        device, bf16 [rows][ldy], or NULL.
  *   q, q_scales, q_type  the codes of y and their scales, or NULL, NULL and
  *            QG_A_BF16 (one of y and q is wanted): QG_A_INT8_TOKEN, QG_A_FP8_TOKEN,
- *            QG_A_FP8_BLOCK or QG_A_MXFP8, layouts, scales and roundings as
- *            qg_quantize_int8, qg_quantize_fp8 and qg_quantize_mxfp8 (fp32 scales
- *            are at least 2^-126) but of the fp32 y; [rows][ldq] bytes.
+ *            QG_A_FP8_BLOCK or QG_A_MXFP8, layouts and scales as qg_quantize_int8,
+ *            qg_quantize_fp8 and qg_quantize_mxfp8 (fp32 scales are at least
+ *            2^-126), of the fp32 y: the codes nearest to y times the fp32
+ *            reciprocal of the scale, ties to even; [rows][ldq] bytes.
  * k % 8 == 0 (MXFP8: % 32), k <= 2^24; 16-B aligned rows (q: 8-B; a product that
  * reads it wants 16).  Outputs other than sum overlap no input.  rows == 0 is a
  * no-op.  A row with NaN, Inf or a mean square beyond fp32 gives unspecified
@@ -666,7 +667,8 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
  *   y       device, [m][ldy] of y_type (QG_O_BF16 / QG_O_F32), ldy >= n, any element
  *           alignment (rows on 16 bytes are faster); some columns of a fused
  *           projection are y + their first column.  It overlaps no input.
- *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents.
+ *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents; NULL when
+ *           that size is 0.
  * m == 0 is a no-op.  A row's result does not depend on the other rows' values.
  * Asynchronous on `stream`. */
 #define QG_LORA_MAX_RANK 256

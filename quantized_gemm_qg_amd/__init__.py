@@ -154,14 +154,16 @@ LIB_PATH = _LIB_PATH
 
 def _ptr(x) -> int | None:
     """Device/host address of a torch tensor, a numpy array, an int, or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):
         return x.ctypes.data
+    if isinstance(x, int):
+        return x
     raise TypeError(f"cannot take the address of {type(x)}")
 
 

@@ -490,7 +490,7 @@ struct XentCall {
   void *partials;
   float *stats, *at_target;  // forward: [tiles of columns][m][2], [m]
   const float *dloss;        // backward: [m]
-  float *alpha;              // backward: [1]
+  float *alpha;              // backward: [2]
   void *d;                   // backward: bf16 [xent_d_rows][ldd], one piece
   int64_t ldd;
   float *parts;              // backward: parts of dx, fp32 [][m][k]
@@ -519,10 +519,11 @@ struct LoraArgs {
   void *y;
   int64_t ldy;
   bool y_vectors;  // y's rows are 16-byte aligned
-  float *t;        // [splits][m][rank]
+  float *t;        // [splits][m][rank]; NULL: one launch (lora_small)
   int32_t splits;
   int32_t chunks;  // (set by the launch) 256-column chunks of a workgroup
 };
+bool lora_small(int64_t m, int64_t k, int64_t n, int adapters, int rank);
 int lora_splits(int64_t m, int64_t k, int adapters);
 hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,

@@ -95,7 +95,7 @@ extern "C" qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int
                                             uint64_t *bytes) {
   if (!bytes) return QG_ERR_INVALID_ARGUMENT;
   QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
-  *bytes = m == 0 ? 0 : align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
+  *bytes = m == 0 || lora_small(m, k, n, num_adapters, rank) ? 0 : align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
   return QG_OK;
 }
 
@@ -119,7 +119,7 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   QG_TRY(ws_check(need, ws, ws_bytes));
   const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
   const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
-                      num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors, (float *)ws,
+                      num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors, need ? (float *)ws : nullptr,
                       lora_splits(m, k, num_adapters), 0};
   return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
 }

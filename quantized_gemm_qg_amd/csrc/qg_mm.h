@@ -112,7 +112,7 @@ struct MmArgs {
   int32_t first_token;
   float scale;
   float *stats, *at_target;
-  const float *lse, *dloss;
+  const float *lse, *dloss, *dloss_most;  // (dloss_most: found before, or NULL)
   float *alpha_out;
   int32_t vocab;
   // kScaled: y = alpha[0] times the product.  kParts: split over k without a join,
@@ -241,7 +241,10 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     // (every workgroup looks for the largest |dloss| of the rows that count: a launch
     // of its own for it took 5 us)
     auto dloss_of = [&](int r) { return (uint32_t)a.targets[r] < (uint32_t)a.vocab ? a.dloss[r] : 0.f; };
-    for (int r = threadIdx.x; r < a.m; r += C::THREADS) dloss_most = fmaxf(dloss_most, fabsf(dloss_of(r)));
+    if (a.dloss_most)
+      dloss_most = a.dloss_most[0];
+    else
+      for (int r = threadIdx.x; r < a.m; r += C::THREADS) dloss_most = fmaxf(dloss_most, fabsf(dloss_of(r)));
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) dloss_most = fmaxf(dloss_most, __shfl_xor(dloss_most, off));
     if (lane == 0) most_of[wave] = dloss_most;

@@ -91,6 +91,22 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const float *p, int parts,
   *(u32x4_any *)(dx + row * lddx + 8 * c8) = w;  // (rows of dx start at any element)
 }
 
+// The largest |dloss| of the rows that count, for calls of many rows (up to 8192 the
+// gradient's workgroups find it for themselves).
+__global__ __launch_bounds__(1024) void xent_most_kernel(const float *dloss, const int32_t *targets, int m, int vocab,
+                                                         float *out) {
+  __shared__ float wave_most[16];
+  float most = 0.f;
+  for (int r = threadIdx.x; r < m; r += 1024)
+    if ((uint32_t)targets[r] < (uint32_t)vocab) most = fmaxf(most, fabsf(dloss[r]));
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) most = fmaxf(most, __shfl_xor(most, off));
+  if ((threadIdx.x & 63) == 0) wave_most[threadIdx.x >> 6] = most;
+  __syncthreads();
+  for (int w = 0; w < 16; ++w) most = fmaxf(most, wave_most[w]);
+  if (threadIdx.x == 0) out[0] = most;
+}
+
 // Parts of dx take at most this much (or one part).
 constexpr uint64_t kXentPartBytes = 80u << 20;
 
@@ -155,12 +171,21 @@ hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info) {
 }
 
 // d of one piece
-// (and alpha, by the workgroup of the first tile)
+// (alpha: by the workgroup of the first tile; its neighbour holds the largest |dloss|
+// of calls that look for it once)
 hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info) {
   MmArgs a = xent_args(c, first, columns);
   a.lse = c.lse;
   a.dloss = c.dloss;
   a.alpha_out = c.alpha;
+  if (c.m > 8192) {
+    a.dloss_most = c.alpha + 1;
+    if (first == 0 && !info) {
+      hipLaunchKernelGGL(xent_most_kernel, dim3(1), dim3(1024), 0, s, c.dloss, c.targets, (int)c.m, (int)c.vocab, c.alpha + 1);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
   a.vocab = (int32_t)c.vocab;
   a.y = c.d;
   a.ldy = c.ldd;

@@ -142,8 +142,8 @@ def lora(x=DEV, ldx=64, a=DEV, lda=64, b=DEV, ldb=16, scales=DEV, adapters=3, ra
     (UNSUPPORTED, dict(n=(1 << 24) + 1, ldy=1 << 25)), (ALIGNMENT, dict(x=DEV + 8)), (ALIGNMENT, dict(a=DEV + 8)),
     (ALIGNMENT, dict(b=DEV + 8)), (ALIGNMENT, dict(ldx=68)), (ALIGNMENT, dict(lda=68)), (ALIGNMENT, dict(ldb=20)),
     (ALIGNMENT, dict(y=DEV + 1)), (ALIGNMENT, dict(y=DEV + 2, y_type=qg.O_F32)), (ALIGNMENT, dict(scales=DEV + 2)),
-    (ALIGNMENT, dict(rows=DEV + 2)), (ALIGNMENT, dict(offsets=DEV + 1)), (INVALID, dict(ws=None)), (SMALL, dict(wsb=16)),
-    (ALIGNMENT, dict(ws=DEV + 64)),
+    (ALIGNMENT, dict(rows=DEV + 2)), (ALIGNMENT, dict(offsets=DEV + 1)), (INVALID, dict(rank=128, ldb=128, ws=None)), (SMALL, dict(rank=128, ldb=128, wsb=16)),
+    (ALIGNMENT, dict(rank=128, ldb=128, ws=DEV + 64)),
 ])
 def test_lora_refusals(status, kw):
     refuses(status, lora, **kw)
@@ -156,3 +156,6 @@ def test_lora_sizes():
     assert qg._lib.qg_lora_workspace_size(1, 64, 8, 1, 8, None) == INVALID
     assert size(-1, 64, 8, 1, 8) == INVALID and size(1, 64, 8, 0, 8) == INVALID and size(1, 60, 8, 1, 8) == SHAPE
     assert size(1, 64, 8, 1, 264) == UNSUPPORTED
+    # none where one launch does both products, and what fp32 parts of the low-rank rows take where two do
+    assert qg.lora_workspace_size(1, 4096, 4096, 8, 16) == qg.lora_workspace_size(16, 4096, 4096, 8, 32) == 0
+    assert qg.lora_workspace_size(4096, 4096, 14336, 6, 64) == 4096 * 64 * 4
