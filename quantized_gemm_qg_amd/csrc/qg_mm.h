@@ -776,7 +776,9 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   const int64_t steps = (kd + C::KE - 1) / C::KE;
   constexpr int64_t mfma = (int64_t)C::BM * C::BN * C::KE / (C::I8 ? 4096 : 2048) * 17 / 10;
   constexpr int64_t lds = (C::WAVES * (C::MB + C::NB) * 16 * C::KB + C::STAGE) / 128 * 21 / 20;
-  constexpr int64_t matrix = mfma > lds ? mfma : lds;
+  // (kParts: what one operand with k across its rows takes, measured in long
+  // contractions: 256 x 256 5070 clocks a stage, 128 x 128 1760)
+  constexpr int64_t matrix = (mfma > lds ? mfma : lds) * (C::EPI != kParts ? 10 : C::BM > 128 ? 14 : 16) / 10;
   constexpr int64_t latency = C::BM <= 64 ? 700 : C::ST == 2 ? 1170 : 900;
   constexpr int64_t resident = 160 * 1024 / C::LDS;
   constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;

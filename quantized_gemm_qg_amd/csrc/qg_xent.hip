@@ -197,7 +197,9 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
 
 // d W of one piece into parts of dx.  The contraction is long and the tiles are
 // few: parts of it in fp32, which a kernel of all CUs adds up behind the last piece
-// (one workgroup per tile would read 4 MB of 16 parts by itself).
+// (one workgroup per tile would read 4 MB of 16 parts by itself).  400 tokens of
+// 50000 x 2048: 256 x 256 in 16 parts 108 us, 128 x 128 in 4 151 (two stages 152); 257
+// of 38531 x 1032: 128 x 128 in 8 parts 58, 256 x 256 70, 64 x 128 61.
 // info->splits: how many parts the piece has; there: how many hold earlier pieces.
 hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s, MmInfo *info) {
   MmArgs a = xent_args(c, first, columns);
@@ -217,7 +219,6 @@ hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int
     return mm_dispatch<Few>(a, kXentPartBytes, s, info);
   }
   return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, true, kParts>,
-                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 2, true, kParts>,
                      MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true, kParts>,
                      MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true, kParts>, Few>(a, kXentPartBytes, s, info);
 }
