@@ -122,6 +122,8 @@ int64_t xent_piece(int64_t m, int64_t vocab) {
   return std::min<int64_t>(((vocab + pieces - 1) / pieces + 255) / 256 * 256, (vocab + 63) / 64 * 64);
 }
 
+// (64 x 128 in three stages, two workgroups per CU: 61 tokens of 100003 x 2048 95 us,
+// in four stages 105)
 // (few tokens, whose d has two parts: one shape)
 template <int EPI>
 using XentFew = MmCfg<false, kRows, kRows, false, 32, 128, 1, 8, 4, true, EPI>;
@@ -131,7 +133,7 @@ static hipError_t xent_logits(const MmArgs &a, hipStream_t s, MmInfo *info) {
                      MmCfg<false, kRows, kRows, false, 192, 256, 4, 2, 2, false, EPI>,
                      MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 2, true, EPI>,
                      MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 4, true, EPI>,
-                     MmCfg<false, kRows, kRows, false, 64, 128, 2, 4, 4, true, EPI>,
+                     MmCfg<false, kRows, kRows, false, 64, 128, 2, 4, 3, true, EPI>,
                      XentFew<EPI>>(a, kMmPartialBytes, s, info);
 }
 
