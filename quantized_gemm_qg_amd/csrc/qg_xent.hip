@@ -91,8 +91,9 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const float *p, int parts,
   *(u32x4_any *)(dx + row * lddx + 8 * c8) = w;  // (rows of dx start at any element)
 }
 
-// The largest |dloss| of the rows that count, for calls of many rows (up to 8192 the
-// gradient's workgroups find it for themselves).
+// The largest |dloss| of the rows that count, for calls of many rows (up to 512, one
+// per thread, the gradient's workgroups find it for themselves; with 4096 that cost
+// 20 us a round of tiles).
 __global__ __launch_bounds__(1024) void xent_most_kernel(const float *dloss, const int32_t *targets, int m, int vocab,
                                                          float *out) {
   __shared__ float wave_most[16];
@@ -180,7 +181,7 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
   a.lse = c.lse;
   a.dloss = c.dloss;
   a.alpha_out = c.alpha;
-  if (c.m > 8192) {
+  if (c.m > 512) {
     a.dloss_most = c.alpha + 1;
     if (first == 0 && !info) {
       hipLaunchKernelGGL(xent_most_kernel, dim3(1), dim3(1024), 0, s, c.dloss, c.targets, (int)c.m, (int)c.vocab, c.alpha + 1);
