@@ -353,7 +353,9 @@ __global__ __launch_bounds__(64 * KW) void lora_down_kernel(LoraArgs a) {
 }
 
 // y += scale t B^T for one item and `chunks` times 256 columns, a stride apart so that
-// workgroups side by side work on neighbouring columns.
+// workgroups side by side work on neighbouring columns.  4096 rows of 14336 bf16
+// outputs, rank 64: 55 us, 4.3 TB/s of y (90 with y in the operand's layout, rows of
+// neighbouring lanes 28 KB apart); 333 fp32 rows of 8187: 9.2 us.
 template <int RB, int SD, bool F32>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];

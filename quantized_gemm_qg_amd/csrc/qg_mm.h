@@ -1,5 +1,5 @@
-// Tiled matrix product of the int8 layers and the bf16 gated feed-forward
-// block: Y[r][c] = sum_k A(r, k) B(c, k), int8 x int8 into int32 or bf16 x bf16
+// Tiled matrix product of the int8 layers, the bf16 gated feed-forward block and the
+// cross entropy of a head: Y[r][c] = sum_k A(r, k) B(c, k), int8 x int8 into int32 or bf16 x bf16
 // into fp32, with three operand forms:
 //
 //   kRows    the operand's rows run along k ([row][pitch], k contiguous):

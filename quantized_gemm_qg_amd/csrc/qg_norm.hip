@@ -9,6 +9,9 @@
 // in that order, so the largest |y| of a row is r max |s w| exactly, and one
 // reduction gives the sum of squares and the per-token scale.  Sums are fp32; y
 // is rounded once, to bf16 and from fp32 to the codes.
+// Bound by HBM from about 100 MB on: 16384 x 4096 with the residual, bf16 and MXFP8 out
+// 117 us (606 MB, 5.2 TB/s); 4096 x 4096 forward 26 and backward 25 us; below, by a
+// launch and two memory latencies (one row of 4096 3.5 us, 1001 x 2080 8.1 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -94,7 +97,9 @@ __device__ __forceinline__ void team_reduce(float &a, float &b, float (*red)[2][
 
 }  // namespace
 
-// The threads of a row (a wave, or TEAMS 1: the workgroup) hold VEC x 8 values each;
+// The threads of a row (a wave, or TEAMS 1: the workgroup) hold VEC x 8 values each
+// (rows of 4096 on 512 threads with 8 values each: one row 3.3 us instead of 3.5, 333
+// rows of 5128 6.8 instead of 6.2);
 // LONG: what lies behind them is read twice.  RES: 0 no residual and no sum, 1 bf16,
 // 2 fp32.
 template <int TEAMS, int VEC, bool LONG, bool XF32, int RES>

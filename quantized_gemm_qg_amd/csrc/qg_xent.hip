@@ -13,6 +13,9 @@
 // exactly 1 and the entries near -1; c comes back in the products' epilogues.  With
 // few tokens (dx 16, dW 32) single entries decide: there d is the sum of two bf16
 // parts, as in the gated block's backward pass.
+// 4096 tokens of 131072 x 4096: forward 3.15 ms (1.40 PFLOP/s), and per piece of 16384
+// tokens d 439 to 458 us (with its exponentials and 134 MB of stores), dx 390 to 417, dW
+// 400 to 434.  61 tokens of 100003 x 2048, forward: 95 us, 4.3 TB/s of weights.
 #include <hip/hip_runtime.h>
 
 #include "qg_device.h"
@@ -114,8 +117,9 @@ constexpr uint64_t kXentPartBytes = 80u << 20;
 static int64_t xent_halves(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 0; }
 int64_t xent_d_rows(int64_t m) { return m + xent_halves(m); }
 
-// Columns of a piece: d takes up to 128 MB, half of the last-level cache, and at
-// least 8192 columns (the products over a piece would be short).
+// Columns of a piece: d takes up to 128 MB, half of the last-level cache, in which both
+// products find it, and at least 8192 columns (the products over a piece would be
+// short).
 int64_t xent_piece(int64_t m, int64_t vocab) {
   int64_t most = (64ll << 20) / std::max<int64_t>(m, 1);
   most = std::min<int64_t>(std::max<int64_t>(most / 256 * 256, 8192), 1 << 20);
