@@ -51,6 +51,9 @@ extern "C" qg_status qg_rmsnorm(const void *x, int32_t x_type, int64_t ldx, cons
     if (!aligned(q, 8) || ldq % 8 != 0 || (q_type != QG_A_MXFP8 && !aligned(q_scales, 4))) return QG_ERR_ALIGNMENT;
   }
   if (rows == 0) return QG_OK;
+  // (a buffer that is read and written has to be the same matrix both times)
+  if (sum && ((sum == x && (x_type != res_type || lds != ldx)) || (sum == residual && lds != ldr)))
+    return QG_ERR_INVALID_ARGUMENT;
   const NormArgs a{x, ldx, residual, ldr, sum, lds, weight, eps, rows, k, (uint16_t *)y, ldy, q_type, (uint8_t *)q, ldq, q_scales};
   return hip_status(launch_rmsnorm(a, x_type == QG_O_F32, !added ? 0 : res_type == QG_O_BF16 ? 1 : 2, stream));
 }
@@ -73,6 +76,7 @@ extern "C" qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t 
   if (dsum) QG_TRY(matrix_check(dsum, ldds, k, el_of(s_type)));
   if (dx) QG_TRY(matrix_check(dx, lddx, k, el_of(s_type)));
   if (!aligned(dw, 16)) return QG_ERR_ALIGNMENT;
+  if (dx && dx == dsum && lddx != ldds) return QG_ERR_INVALID_ARGUMENT;
   if (!dw && (!dx || rows == 0)) return QG_OK;
   if (dw) {
     uint64_t need = 0;

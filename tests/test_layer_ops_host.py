@@ -28,6 +28,8 @@ def norm(x=DEV, x_type=qg.O_BF16, ldx=64, weight=DEV, eps=1e-5, rows=4, k=64, y=
     (UNSUPPORTED, dict(k=(1 << 24) + 8, ldx=1 << 25, ldy=1 << 25)), (ALIGNMENT, dict(x=DEV + 8)), (ALIGNMENT, dict(weight=DEV + 8)),
     (ALIGNMENT, dict(y=DEV + 2)), (ALIGNMENT, dict(ldx=68)), (ALIGNMENT, dict(ldy=66)), (ALIGNMENT, dict(x_type=qg.O_F32, ldx=66)),
     (SHAPE, dict(residual=DEV, ldr=56)), (ALIGNMENT, dict(residual=DEV + 4, ldr=64)), (INVALID, dict(residual=DEV, ldr=64, res_type=3)),
+    (INVALID, dict(sum=DEV, lds=72)), (INVALID, dict(sum=DEV, lds=64, res_type=qg.O_F32)),   # x's memory, another matrix
+    (INVALID, dict(residual=2 * DEV, ldr=64, sum=2 * DEV, lds=72)),
     (SHAPE, dict(sum=DEV, lds=8)), (ALIGNMENT, dict(sum=DEV, lds=68)), (ALIGNMENT, dict(sum=DEV + 8, lds=64)),
     (INVALID, dict(q=DEV, ldq=64, q_scales=DEV)),                                # codes without their type
     (INVALID, dict(q_type=qg.A_INT8_TOKEN)),                                     # a type without codes
@@ -55,7 +57,7 @@ def norm_back(s=DEV, s_type=qg.O_BF16, lds=64, weight=DEV, eps=1e-5, rows=4, k=6
 @pytest.mark.parametrize("status,kw", [
     (INVALID, dict(s=None)), (INVALID, dict(dy=None)), (INVALID, dict(weight=None)), (INVALID, dict(s_type=2)), (INVALID, dict(dw_type=2)),
     (INVALID, dict(rows=-1)), (INVALID, dict(eps=0.0)), (SHAPE, dict(k=12)), (SHAPE, dict(lds=56)), (SHAPE, dict(lddy=56)),
-    (SHAPE, dict(lddx=56)), (SHAPE, dict(dsum=DEV, ldds=8)), (ALIGNMENT, dict(dsum=DEV + 8, ldds=64)), (ALIGNMENT, dict(dx=DEV + 8)),
+    (SHAPE, dict(lddx=56)), (SHAPE, dict(dsum=DEV, ldds=8)), (INVALID, dict(dsum=DEV, ldds=72)), (ALIGNMENT, dict(dsum=DEV + 8, ldds=64)), (ALIGNMENT, dict(dx=DEV + 8)),
     (ALIGNMENT, dict(dw=DEV + 4)), (ALIGNMENT, dict(lddy=68)), (INVALID, dict(ws=None)), (SMALL, dict(wsb=100)),
     (ALIGNMENT, dict(ws=DEV + 64)), (UNSUPPORTED, dict(k=1 << 25, lds=1 << 25, lddy=1 << 25, lddx=1 << 25)),
 ])
