@@ -103,6 +103,11 @@ struct MmArgs {
   int32_t splits, per;
   uint32_t *counters;
   uint64_t *partials;
+};
+
+// What the other epilogues need besides (apart: the longer arguments alone cost the
+// int8 product of 333 rows 3 %).
+struct MmMoreArgs : MmArgs {
   // cross entropy of a head (kXentStats, kXentGrad): y's columns are the logits of
   // tokens first_token ..; kXentStats leaves the largest logit and the sum of
   // exponentials of every row and tile in stats [tile][m] and the target's logit
@@ -137,6 +142,7 @@ template <bool I8_, int AF_, int BF_, bool GATED_, int BM_, int BN_, int WM_, in
           int EPI_ = kPlain>
 struct MmCfg {
   static constexpr int EPI = EPI_;
+  using Args = typename std::conditional<EPI == 0, MmArgs, MmMoreArgs>::type;
   static constexpr bool I8 = I8_, GATED = GATED_;
   static constexpr bool SPLIT = SPLIT_;
   static constexpr int AF = AF_, BF = BF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = 128, ST = ST_;
@@ -214,7 +220,7 @@ __device__ __forceinline__ int row_swz(int row) { return row & 7; }
 __device__ __forceinline__ int col_swz(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
+__global__ __launch_bounds__(C::THREADS) void mm_kernel(typename C::Args a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   typedef typename std::conditional<C::I8, i32x4, f32x4>::type Acc;
   const int lane = threadIdx.x & 63;
@@ -620,7 +626,8 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(MmArgs a) {
     if (threadIdx.x < C::BM) *(f32x4 *)(row_info + 4 * threadIdx.x) = my_row;
     mm_barrier();
   }
-  const float alpha = C::EPI == kScaled ? a.alpha[0] : 1.f;
+  float alpha = 1.f;
+  if constexpr (C::EPI == kScaled) alpha = a.alpha[0];
   if constexpr (C::EPI == kParts) a.y = (float *)a.y + split * a.part_stride;
   // fp32 values of block (i, j), scales applied
   auto value = [&](int i, int j) {
@@ -812,9 +819,9 @@ static uint64_t mm_partial_bytes(int64_t m, int64_t n, const MmPlan &p) {
 }
 
 template <class C>
-static hipError_t launch_mm(const MmArgs &args, const MmPlan &p, hipStream_t s) {
+static hipError_t launch_mm(const typename C::Args &args, const MmPlan &p, hipStream_t s) {
   constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
-  MmArgs a = args;
+  typename C::Args a = args;
   a.splits = p.splits;
   a.per = p.per;
   if (p.splits > 1 && C::EPI != kParts && (!a.counters || !a.partials)) return hipErrorInvalidValue;
@@ -842,12 +849,12 @@ static bool mm_reaches(const MmArgs &a) {
 // The cheapest of the compiled shapes that reach their operands' rows: launches
 // it, or (info; the pitches count here too) only says which it is and what
 // partial tiles it needs.
-template <class... Cs>
-static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, MmInfo *info) {
-  const MmPlan plans[] = {mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
-  const bool reach[] = {mm_reaches<Cs>(a)...};
+template <class C0, class... Cs>
+static hipError_t mm_dispatch(const typename C0::Args &a, uint64_t budget, hipStream_t s, MmInfo *info) {
+  const MmPlan plans[] = {mm_plan<C0>(a.m, a.n, a.kd, budget), mm_plan<Cs>(a.m, a.n, a.kd, budget)...};
+  const bool reach[] = {mm_reaches<C0>(a), mm_reaches<Cs>(a)...};
   int best = -1;
-  for (int i = 0; i < (int)sizeof...(Cs); ++i)
+  for (int i = 0; i <= (int)sizeof...(Cs); ++i)
     if (reach[i] && (best < 0 || plans[i].cost < plans[best].cost)) best = i;
   int i = 0;
   hipError_t e = hipErrorInvalidValue;
@@ -861,6 +868,7 @@ static hipError_t mm_dispatch(const MmArgs &a, uint64_t budget, hipStream_t s, M
       e = launch_mm<C>(a, plans[best], s);
     }
   };
+  one((C0 *)nullptr);
   (one((Cs *)nullptr), ...);
   return e;
 }

@@ -133,7 +133,7 @@ int64_t xent_piece(int64_t m, int64_t vocab) {
 template <int EPI>
 using XentFew = MmCfg<false, kRows, kRows, false, 32, 128, 1, 8, 4, true, EPI>;
 template <int EPI>
-static hipError_t xent_logits(const MmArgs &a, hipStream_t s, MmInfo *info) {
+static hipError_t xent_logits(const MmMoreArgs &a, hipStream_t s, MmInfo *info) {
   return mm_dispatch<MmCfg<false, kRows, kRows, false, 256, 256, 4, 2, 2, false, EPI>,
                      MmCfg<false, kRows, kRows, false, 192, 256, 4, 2, 2, false, EPI>,
                      MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 2, true, EPI>,
@@ -142,8 +142,8 @@ static hipError_t xent_logits(const MmArgs &a, hipStream_t s, MmInfo *info) {
                      XentFew<EPI>>(a, kMmPartialBytes, s, info);
 }
 
-static MmArgs xent_args(const XentCall &c, int64_t first, int64_t columns) {
-  MmArgs a = {};
+static MmMoreArgs xent_args(const XentCall &c, int64_t first, int64_t columns) {
+  MmMoreArgs a = {};
   a.a = (const uint8_t *)c.x;
   a.lda = c.ldx * 2;
   a.b = (const uint8_t *)c.w + first * c.ldw * 2;
@@ -162,7 +162,7 @@ static MmArgs xent_args(const XentCall &c, int64_t first, int64_t columns) {
 
 // (info: nothing is launched, see mm_dispatch)
 hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info) {
-  MmArgs a = xent_args(c, 0, c.vocab);
+  MmMoreArgs a = xent_args(c, 0, c.vocab);
   a.stats = c.stats;
   a.at_target = c.at_target;
   MmInfo choice;
@@ -181,7 +181,7 @@ hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info) {
 // (alpha: by the workgroup of the first tile; its neighbour holds the largest |dloss|
 // of calls that look for it once)
 hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipStream_t s, MmInfo *info) {
-  MmArgs a = xent_args(c, first, columns);
+  MmMoreArgs a = xent_args(c, first, columns);
   a.lse = c.lse;
   a.dloss = c.dloss;
   a.alpha_out = c.alpha;
@@ -209,7 +209,7 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
 // of 38531 x 1032: 128 x 128 in 8 parts 58, 256 x 256 70, 64 x 128 61.
 // info->splits: how many parts the piece has; there: how many hold earlier pieces.
 hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s, MmInfo *info) {
-  MmArgs a = xent_args(c, first, columns);
+  MmMoreArgs a = xent_args(c, first, columns);
   a.a = (const uint8_t *)c.d;
   a.lda = c.ldd * 2;
   a.n = (int32_t)c.k;
@@ -240,7 +240,7 @@ hipError_t launch_xent_dx_sum(const XentCall &c, int parts, void *dx, int64_t ld
 // rows of dW of one piece
 hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, void *dw, int dw_type, int64_t lddw,
                           hipStream_t s, MmInfo *info) {
-  MmArgs a = xent_args(c, first, columns);
+  MmMoreArgs a = xent_args(c, first, columns);
   a.a = (const uint8_t *)c.d;
   a.lda = c.ldd * 2;
   a.b = (const uint8_t *)c.x;
