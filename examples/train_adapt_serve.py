@@ -96,17 +96,17 @@ class Server:
         self.h, self.out, self.s2, self.y2 = new(m, INTER), new(m, K), new(m, K), new(m, K)
         self.logits = new(m, VOCAB, t=torch.float32)
         self.sorted, self.offsets = new(m, t=torch.int32), new(ADAPTERS + 1, t=torch.int32)
+        self.sort_ws = workspace(256)
         self.ws = workspace(max(qg.gated_gemm_workspace_size(self.gate_up[0], m),
                                 qg.gemm_workspace_size_ex(self.down[0], m, qg.GEMM_QUANTIZE_X),
-                                qg.gemm_workspace_size_ex(self.head[0], m, 0), 256,
+                                qg.gemm_workspace_size_ex(self.head[0], m, 0),
                                 qg.lora_workspace_size(m, K, VOCAB, ADAPTERS, RANK)))
-        self.adapter_ws = workspace(self.ws.numel())   # (not zero-filled again: the products' stays apart)
 
     def __call__(self, token, adapter):
         """Logits of the rows' next tokens; adapter int32 [m], -1 for none."""
         p, m, w = self.p, self.m, (self.ws, self.ws.numel())
         s = p["embed"][token].contiguous()
-        qg.moe_sort(adapter, m, 1, ADAPTERS, self.sorted, self.offsets, self.adapter_ws, self.adapter_ws.numel())
+        qg.moe_sort(adapter, m, 1, ADAPTERS, self.sorted, self.offsets, self.sort_ws, 256)
         qg.rmsnorm(s, qg.O_BF16, K, p["norm1"], EPS, m, K, q_type=qg.A_INT8_TOKEN, q=self.q, ldq=K, q_scales=self.qs)
         qg.gated_gemm(self.gate_up[0], self.q, self.qs, m, K, self.h, qg.O_BF16, INTER, ACT, *w)
         qg.gemm_ex(self.down[0], self.h, None, m, INTER, self.out, qg.O_BF16, K, *w, qg.GEMM_QUANTIZE_X)
@@ -114,7 +114,7 @@ class Server:
                    ldy=K, q_type=qg.A_INT8_TOKEN, q=self.q, ldq=K, q_scales=self.qs)
         qg.gemm_ex(self.head[0], self.q, self.qs, m, K, self.logits, qg.O_F32, VOCAB, *w, 0)
         qg.lora(self.y2, K, self.a, K, self.b, RANK, None, ADAPTERS, RANK, self.sorted, self.offsets, m, K, VOCAB, self.logits,
-                qg.O_F32, VOCAB, self.adapter_ws, self.adapter_ws.numel())
+                qg.O_F32, VOCAB, *w)
         return self.logits
 
 

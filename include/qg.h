@@ -637,8 +637,9 @@ qg_status qg_rmsnorm(const void *x, int32_t x_type, int64_t ldx, const void *res
  *   dx   device, [rows][lddx] of s_type, or NULL; it may be dsum's own buffer.
  *   dw   device, [k] of dw_type, 16-B aligned, or NULL; overwritten (rows == 0:
  *        zeros).
- *   ws   qg_rmsnorm_backward_workspace_size bytes, 256-B aligned, any contents;
- *        NULL without dw.
+ *   ws   qg_rmsnorm_backward_workspace_size bytes, 256-B aligned, any contents (the
+ *        first 64 KiB are left alone: it may be a product's workspace); NULL without
+ *        dw.
  * Sums over the rows are in a fixed order.  Alignments and limits as above. */
 qg_status qg_rmsnorm_backward_workspace_size(int64_t rows, int64_t k, uint64_t *bytes);
 qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const void *weight, float eps, int64_t rows,
@@ -667,8 +668,9 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
  *   y       device, [m][ldy] of y_type (QG_O_BF16 / QG_O_F32), ldy >= n, any element
  *           alignment (rows on 16 bytes are faster); some columns of a fused
  *           projection are y + their first column.  It overlaps no input.
- *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents; NULL when
- *           that size is 0.
+ *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents (the first 64
+ *           KiB are left alone: it may be a product's workspace); NULL when that
+ *           size is 0.
  * m == 0 is a no-op.  A row's result does not depend on the other rows' values.
  * Asynchronous on `stream`. */
 #define QG_LORA_MAX_RANK 256

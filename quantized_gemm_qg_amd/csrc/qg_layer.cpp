@@ -19,6 +19,10 @@ static qg_status matrix_check(const void *p, int64_t ld, int64_t columns, int el
     if (st_ != QG_OK) return st_;           \
   } while (0)
 
+// (The workspaces of the norm's backward pass and of the adapters need no zeros; they
+// begin behind the place of the products' arrival counters, so that one buffer may
+// serve all of them.)
+
 // Checks that the two directions of the norm share.
 static qg_status norm_check(const void *weight, float eps, int64_t rows, int64_t k) {
   if (rows < 0 || k < 0 || !std::isfinite(eps) || !(eps > 0.f)) return QG_ERR_INVALID_ARGUMENT;
@@ -60,7 +64,7 @@ extern "C" qg_status qg_rmsnorm(const void *x, int32_t x_type, int64_t ldx, cons
 
 extern "C" qg_status qg_rmsnorm_backward_workspace_size(int64_t rows, int64_t k, uint64_t *bytes) {
   if (!bytes || rows < 0 || k < 0) return QG_ERR_INVALID_ARGUMENT;
-  *bytes = rows == 0 || k == 0 ? 0 : align_up((uint64_t)rmsnorm_back_parts(rows, k) * k * 4, 256);
+  *bytes = rows == 0 || k == 0 ? 0 : kSplitCounterBytes + align_up((uint64_t)rmsnorm_back_parts(rows, k) * k * 4, 256);
   return QG_OK;
 }
 
@@ -83,7 +87,8 @@ extern "C" qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t 
     (void)qg_rmsnorm_backward_workspace_size(rows, k, &need);
     QG_TRY(ws_check(need, ws, ws_bytes));
   }
-  const NormBackArgs a{s, lds, weight, eps, rows, k, (const uint16_t *)dy, lddy, dsum, ldds, dx, lddx, dw ? (float *)ws : nullptr};
+  const NormBackArgs a{s, lds, weight, eps, rows, k, (const uint16_t *)dy, lddy, dsum, ldds, dx, lddx,
+                       dw ? (float *)((uint8_t *)ws + kSplitCounterBytes) : nullptr};
   return hip_status(launch_rmsnorm_backward(a, s_type == QG_O_F32, dw, dw_type == QG_O_F32, stream));
 }
 
@@ -99,7 +104,8 @@ extern "C" qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int
                                             uint64_t *bytes) {
   if (!bytes) return QG_ERR_INVALID_ARGUMENT;
   QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
-  *bytes = m == 0 || lora_small(m, k, n, num_adapters, rank) ? 0 : align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
+  const bool none = m == 0 || lora_small(m, k, n, num_adapters, rank);
+  *bytes = none ? 0 : kSplitCounterBytes + align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
   return QG_OK;
 }
 
@@ -123,8 +129,8 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   QG_TRY(ws_check(need, ws, ws_bytes));
   const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
   const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
-                      num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors, need ? (float *)ws : nullptr,
-                      lora_splits(m, k, num_adapters), 0};
+                      num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors,
+                      need ? (float *)((uint8_t *)ws + kSplitCounterBytes) : nullptr, lora_splits(m, k, num_adapters), 0};
   return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
 }
 

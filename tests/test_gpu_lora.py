@@ -75,6 +75,7 @@ class Case:
         torch.cuda.synchronize()
         assert (self.flat[:self.shift] == 7).all() and (self.flat[self.shift + self.m * self.ldy:] == 7).all()
         assert (self.yd[:, self.n:] == 7).all()
+        assert (self.ws[:1 << 16] == 255).all()   # where a product's workspace has its counters
         return self.yd[:, :self.n].cpu()
 
     def check(self, got):

@@ -182,6 +182,7 @@ def backward(s, s_type, w, eps, dy, dsum, want_dx=True, dw_type=F32, in_place=Fa
         qg.rmsnorm_backward(sd, s_type, k + 8, wd, eps, rows, k, dyd, k + 16, dx, k + 8, dw, dw_type, ws if want_dw else None, n,
                             dsum=dsd, ldds=k + 8)
     torch.cuda.synchronize()
+    assert (ws[:1 << 16] == 255).all()   # where a product's workspace has its counters
     if want_dx and not in_place:
         assert (dx[rows:] == 7).all() and (dx[:, k:] == 7).all()
     if want_dw:
