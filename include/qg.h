@@ -668,9 +668,9 @@ qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const 
  *   y       device, [m][ldy] of y_type (QG_O_BF16 / QG_O_F32), ldy >= n, any element
  *           alignment (rows on 16 bytes are faster); some columns of a fused
  *           projection are y + their first column.  It overlaps no input.
- *   ws      qg_lora_workspace_size bytes, 256-B aligned, any contents (the first 64
- *           KiB are left alone: it may be a product's workspace); NULL when that
- *           size is 0.
+ *   ws      qg_lora_workspace_size bytes (enough for every smaller m too), 256-B
+ *           aligned, any contents (the first 64 KiB are left alone: it may be a
+ *           product's workspace); NULL when that size is 0.
  * m == 0 is a no-op.  A row's result does not depend on the other rows' values.
  * Asynchronous on `stream`. */
 #define QG_LORA_MAX_RANK 256

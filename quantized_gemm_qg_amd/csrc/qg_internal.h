@@ -525,6 +525,7 @@ struct LoraArgs {
 };
 bool lora_small(int64_t m, int64_t k, int64_t n, int adapters, int rank);
 int lora_splits(int64_t m, int64_t k, int adapters);
+int64_t lora_most_rows(int64_t m, int64_t k);
 hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,

@@ -100,12 +100,18 @@ static qg_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t adapters, i
   return QG_OK;
 }
 
+// Bytes for `t_rows` fp32 rows of the first product's parts (0: one launch, no workspace).
+static uint64_t lora_bytes(int64_t t_rows, int64_t m, int64_t k, int64_t n, int32_t adapters, int32_t rank) {
+  if (m == 0 || lora_small(m, k, n, adapters, rank)) return 0;
+  return kSplitCounterBytes + align_up((uint64_t)t_rows * rank * 4, 256);
+}
+
+// (for any call of up to m rows: fewer rows have more parts of k)
 extern "C" qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank,
                                             uint64_t *bytes) {
   if (!bytes) return QG_ERR_INVALID_ARGUMENT;
   QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
-  const bool none = m == 0 || lora_small(m, k, n, num_adapters, rank);
-  *bytes = none ? 0 : kSplitCounterBytes + align_up((uint64_t)lora_splits(m, k, num_adapters) * m * rank * 4, 256);
+  *bytes = lora_bytes(lora_most_rows(m, k), m, k, n, num_adapters, rank);
   return QG_OK;
 }
 
@@ -124,13 +130,13 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   if (!aligned(y, el_of(y_type)) || !aligned(scales, 4) || !aligned(sorted_rows, 4) || !aligned(offsets, 4))
     return QG_ERR_ALIGNMENT;
   if (m == 0) return QG_OK;
-  uint64_t need = 0;
-  (void)qg_lora_workspace_size(m, k, n, num_adapters, rank, &need);
+  const int splits = lora_splits(m, k, num_adapters);
+  const uint64_t need = lora_bytes(splits * m, m, k, n, num_adapters, rank);
   QG_TRY(ws_check(need, ws, ws_bytes));
   const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
   const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
                       num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors,
-                      need ? (float *)((uint8_t *)ws + kSplitCounterBytes) : nullptr, lora_splits(m, k, num_adapters), 0};
+                      need ? (float *)((uint8_t *)ws + kSplitCounterBytes) : nullptr, splits, 0};
   return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
 }
 

@@ -457,10 +457,16 @@ using Int = std::integral_constant<int, V>;
 // Items at most: one per adapter with rows, and one more for every `rows` rows.
 static int64_t lora_items(int64_t m, int adapters, int rows) { return std::min<int64_t>(adapters, m) + m / rows; }
 
-// Parts of k: workgroups for the CUs, of at least 8 stages of 64 each.
+// Parts of k: workgroups for the CUs, of about 8 stages of 64 or more (the last one has
+// what is left).
+static int64_t lora_most_splits(int64_t k) { return std::min<int64_t>((k + 511) / 512, 16); }
 int lora_splits(int64_t m, int64_t k, int adapters) {
-  const int64_t want = std::max<int64_t>(256 / lora_items(m, adapters, 16), 1), most = std::max<int64_t>((k + 511) / 512, 1);
-  return (int)std::min<int64_t>(std::min(want, most), 16);
+  return (int)std::min(std::max<int64_t>(256 / lora_items(m, adapters, 16), 1), lora_most_splits(k));
+}
+// Parts times rows of any call of up to m rows: s > 1 parts of r rows have s items <=
+// 256 and r < 16 items, so s r < 4096.
+int64_t lora_most_rows(int64_t m, int64_t k) {
+  return std::max(m, std::min<int64_t>(lora_most_splits(k) * m, 4096));
 }
 
 // Calls of one launch: a round of workgroups, each of which reads all of A for

@@ -207,3 +207,15 @@ def test_another_stream_and_a_captured_graph():
         kept, c.ids = c.ids, other
         c.check(c.yd[:, :c.n].cpu())
         c.ids = kept
+
+
+def test_a_workspace_for_more_rows():
+    """One buffer, allocated for the largest batch, for batches that split k into more parts."""
+    largest, k, n, rank = 2048, 4096, 264, 16
+    size = qg.lora_workspace_size(largest, k, n, 1, rank)
+    for m in (700, 1023, 2047):
+        c = Case(m, k, n, rank, 1, seed=m)
+        c.ws_bytes = size
+        c.ws = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+        c.check(c.run())
+        assert (c.ws[size:] == 255).all()

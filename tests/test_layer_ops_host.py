@@ -161,3 +161,16 @@ def test_lora_sizes():
     # none where one launch does both products, and what fp32 parts of the low-rank rows take where two do
     assert qg.lora_workspace_size(1, 4096, 4096, 8, 16) == qg.lora_workspace_size(16, 4096, 4096, 8, 32) == 0
     assert qg.lora_workspace_size(4096, 4096, 14336, 6, 64) == (64 << 10) + 4096 * 64 * 4
+
+
+def test_a_workspace_of_the_adapters_serves_fewer_rows():
+    """A program allocates once, for its largest batch."""
+    for k, n, adapters, rank in ((4096, 14336, 1, 16), (4096, 14336, 6, 64), (520, 300, 3, 128), (8192, 90, 40, 256), (264, 700, 1000, 8)):
+        for most in (20, 300, 1023, 2048, 2300):
+            size = qg.lora_workspace_size(most, k, n, adapters, rank)
+            for m in range(1, most):
+                need = qg.lora_workspace_size(m, k, n, adapters, rank)
+                assert need <= size, (m, most, k, n, adapters, rank)
+                if need:   # (the size is looked at before the alignment, which ends the call here)
+                    refuses(ALIGNMENT, lora, m=m, k=k, ldx=k, lda=k, n=n, ldy=n, adapters=adapters, rank=rank, ldb=rank, ws=DEV + 64,
+                            wsb=size)
