@@ -86,7 +86,7 @@ def int8_layer(weight):
 
 
 class Server:
-    """The model in int8 with adapters on its head's output, for up to m rows."""
+    """The model in int8 with adapters on its head's output, for m rows."""
 
     def __init__(self, p, a, b, m):
         self.p, self.a, self.b, self.m = {n: t.to(BF16) for n, t in p.items()}, a, b, m

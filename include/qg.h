@@ -637,9 +637,9 @@ qg_status qg_rmsnorm(const void *x, int32_t x_type, int64_t ldx, const void *res
  *   dx   device, [rows][lddx] of s_type, or NULL; it may be dsum's own buffer.
  *   dw   device, [k] of dw_type, 16-B aligned, or NULL; overwritten (rows == 0:
  *        zeros).
- *   ws   qg_rmsnorm_backward_workspace_size bytes, 256-B aligned, any contents (the
- *        first 64 KiB are left alone: it may be a product's workspace); NULL without
- *        dw.
+ *   ws   qg_rmsnorm_backward_workspace_size bytes (enough for fewer rows too), 256-B
+ *        aligned, any contents (the first 64 KiB are left alone: it may be a product's
+ *        workspace); NULL without dw.
  * Sums over the rows are in a fixed order.  Alignments and limits as above. */
 qg_status qg_rmsnorm_backward_workspace_size(int64_t rows, int64_t k, uint64_t *bytes);
 qg_status qg_rmsnorm_backward(const void *s, int32_t s_type, int64_t lds, const void *weight, float eps, int64_t rows,
@@ -692,8 +692,8 @@ qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t lda, const 
  *   scale   > 0: 1, or one over the temperature.
  *   loss, lse  device fp32 [m], one of them may be NULL; lse is for the backward
  *           pass.
- *   ws      qg_linear_xent_workspace_size bytes, 256-B aligned, zero-filled once
- *           (its first 64 KiB suffice).
+ *   ws      qg_linear_xent_workspace_size bytes (enough for every smaller m too),
+ *           256-B aligned, zero-filled once (its first 64 KiB suffice).
  * NaN in a row of x, or an infinite logit, gives NaN in that row alone.  m == 0 is
  * a no-op.  Sums are in a fixed order.  Asynchronous on `stream`. */
 qg_status qg_linear_xent_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);
@@ -711,9 +711,9 @@ qg_status qg_linear_xent(const void *x, int64_t ldx, const void *w, int64_t ldw,
  *   dx   device, bf16 [m][lddx], 16-B aligned, lddx >= k, or NULL.
  *   dw   device, [vocab][lddw] of dw_type, 16-B aligned, lddw >= k, or NULL; it is
  *        overwritten; m == 0 fills it with zeros.
- *   ws   qg_linear_xent_backward_workspace_size bytes (whatever the vocabulary at
- *        most 128 MB or 16384 m for d, 80 MB or 4 m k for parts of dx, and 48 MB),
- *        256-B aligned, zero-filled once.
+ *   ws   qg_linear_xent_backward_workspace_size bytes (enough for every smaller m
+ *        too; whatever the vocabulary at most 128 MB or 16384 m for d, 80 MB or 4 m k
+ *        for parts of dx, and 48 MB), 256-B aligned, zero-filled once.
  * An ignored row's dx is 0, and it adds nothing to dw as long as its x is finite.
  * Asynchronous on `stream`. */
 qg_status qg_linear_xent_backward_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);

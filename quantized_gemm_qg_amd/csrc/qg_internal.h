@@ -496,6 +496,12 @@ struct XentCall {
   float *parts;              // backward: parts of dx, fp32 [][m][k]
 };
 int64_t xent_d_rows(int64_t m);
+// bytes (stat_tiles: tiles of columns) that no call of up to m tokens exceeds
+struct XentMost {
+  uint64_t partials = 0, back_partials = 0, d = 0, parts = 0;
+  int64_t stat_tiles = 0;
+};
+XentMost xent_most(int64_t m, int64_t k, int64_t vocab);
 int64_t xent_piece(int64_t m, int64_t vocab);
 // info: NULL, or nothing is launched and the choice reported
 hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info = nullptr);

@@ -162,14 +162,18 @@ static bool xent_in_range(int64_t m, int64_t k, int64_t vocab) {
          tiles_fit(vocab, k);
 }
 
+static XentSpace xent_space(int64_t m, uint64_t partials, int64_t stat_tiles) {
+  XentSpace sp;
+  sp.partials = align_up(partials, 256);
+  sp.stats = align_up((uint64_t)stat_tiles * m * 8, 256);
+  sp.at_target = align_up((uint64_t)m * 4, 256);
+  return sp;
+}
+
 static XentSpace xent_space(const XentCall &c) {
   MmInfo i;
   (void)launch_xent(c, nullptr, &i);
-  XentSpace sp;
-  sp.partials = align_up(i.bytes, 256);
-  sp.stats = align_up((uint64_t)((c.vocab + i.bn - 1) / i.bn) * c.m * 8, 256);
-  sp.at_target = align_up((uint64_t)c.m * 4, 256);
-  return sp;
+  return xent_space(c.m, i.bytes, (c.vocab + i.bn - 1) / i.bn);
 }
 
 static XentBackSpace xent_back_space(const XentCall &c) {
@@ -221,12 +225,22 @@ static XentCall xent_call(const void *x, int64_t ldx, const void *w, int64_t ldw
   return c;
 }
 
-// Bytes of either workspace; 0 for sizes that the calls refuse or that need none.
+// Bytes of either workspace, for any call of up to m tokens; 0 for sizes that the calls
+// refuse or that need none.
 static qg_status xent_bytes(int64_t m, int64_t k, int64_t vocab, bool backward, uint64_t *bytes) {
   if (!bytes || m < 0 || k < 0 || vocab < 0) return QG_ERR_INVALID_ARGUMENT;
-  const XentCall c = xent_call(nullptr, k, nullptr, k, m, k, vocab, nullptr, 1.f);
-  const bool some = m > 0 && k > 0 && vocab > 0 && xent_in_range(m, k, vocab);
-  *bytes = !some ? 0 : backward ? xent_back_space(c).total() : xent_space(c).total();
+  *bytes = 0;
+  if (m == 0 || k == 0 || vocab == 0 || !xent_in_range(m, k, vocab)) return QG_OK;
+  const XentMost most = xent_most(m, k, vocab);
+  if (!backward) {
+    *bytes = xent_space(m, most.partials, most.stat_tiles).total();
+    return QG_OK;
+  }
+  XentBackSpace sp;
+  sp.partials = align_up(most.back_partials, 256);
+  sp.d = align_up(most.d, 256);
+  sp.parts = align_up(most.parts, 256);
+  *bytes = sp.total();
   return QG_OK;
 }
 

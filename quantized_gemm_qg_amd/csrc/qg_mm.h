@@ -774,6 +774,10 @@ struct MmPlan {
   int splits = 1, per = 0;
   double cost = 0;
 };
+// Workgroups of a shape that a CU holds.
+template <class C>
+constexpr int64_t kMmResident = 160 * 1024 / C::LDS;
+constexpr int64_t kMmMostSplits = 32;
 // Parts without a join in the kernel (kParts) cost their way to memory and back, by
 // all CUs, and a launch.
 template <class C>
@@ -787,14 +791,14 @@ static MmPlan mm_plan(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
   // contractions: 256 x 256 5070 clocks a stage, 128 x 128 1760)
   constexpr int64_t matrix = (mfma > lds ? mfma : lds) * (C::EPI != kParts ? 10 : C::BM > 128 ? 14 : 16) / 10;
   constexpr int64_t latency = C::BM <= 64 ? 700 : C::ST == 2 ? 1170 : 900;
-  constexpr int64_t resident = 160 * 1024 / C::LDS;
+  constexpr int64_t resident = kMmResident<C>;
   constexpr int64_t partial = (int64_t)C::BM * C::BN * 4;
   const double memory = (double)(m + (C::GATED ? 2 * n : n)) * kd * C::EL / 2100;
   MmPlan best;
   const bool parts = C::EPI == kParts;
   const int64_t most = parts ? (int64_t)(budget / (uint64_t)(4 * m * n))
                        : C::SPLIT && tiles <= kMaxSplitCounters ? (int64_t)(budget / (uint64_t)(partial * tiles)) : 1;
-  for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), 32); ++want) {
+  for (int64_t want = 1; want <= std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(most, 1), steps), kMmMostSplits); ++want) {
     const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
     if (splits != want) continue;  // the same as a smaller number of parts
     const int64_t wgs = ((tiles + kXcds - 1) / kXcds * splits + 31) / 32, rounds = (wgs + resident - 1) / resident;
@@ -816,6 +820,24 @@ static uint64_t mm_partial_bytes(int64_t m, int64_t n, const MmPlan &p) {
   if (C::EPI == kParts) return p.splits > 1 ? (uint64_t)p.splits * m * n * 4 : 0;
   return p.splits > 1 ? (uint64_t)p.splits * ((m + C::BM - 1) / C::BM) * ((n + OUT_BN - 1) / OUT_BN) * C::BM * C::BN * 4
                       : 0;
+}
+
+// The most that mm_partial_bytes comes to for up to m x n outputs and contractions of
+// up to kd, whichever of the shapes is taken: parts times tiles are at most the
+// places on all CUs.
+template <class C0, class... Cs>
+static uint64_t mm_most_partial_bytes(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
+  auto one = [&](auto *cfg) -> uint64_t {
+    using C = std::remove_pointer_t<decltype(cfg)>;
+    constexpr int OUT_BN = C::GATED ? C::BN / 2 : C::BN;
+    const int64_t steps = (kd + C::KE - 1) / C::KE, tiles = ((m + C::BM - 1) / C::BM) * ((n + OUT_BN - 1) / OUT_BN);
+    if (!C::SPLIT || steps < 2) return 0;
+    const int64_t places = 256 * kMmResident<C>, most = std::min(steps, kMmMostSplits);
+    return std::min<uint64_t>((uint64_t)std::min(tiles * most, places) * C::BM * C::BN * 4, budget);
+  };
+  uint64_t most = one((C0 *)nullptr);
+  ((most = std::max(most, one((Cs *)nullptr))), ...);
+  return most;
 }
 
 template <class C>
@@ -872,5 +894,18 @@ static hipError_t mm_dispatch(const typename C0::Args &a, uint64_t budget, hipSt
   (one((Cs *)nullptr), ...);
   return e;
 }
+
+// The compiled shapes of one product.
+template <class... Cs>
+struct MmShapes {
+  template <class Args>
+  static hipError_t dispatch(const Args &a, uint64_t budget, hipStream_t s, MmInfo *info) {
+    return mm_dispatch<Cs...>(a, budget, s, info);
+  }
+  static uint64_t most_bytes(int64_t m, int64_t n, int64_t kd, uint64_t budget) {
+    return mm_most_partial_bytes<Cs...>(m, n, kd, budget);
+  }
+  static constexpr int narrowest = std::min({Cs::BN...});  // columns of a tile
+};
 
 }  // namespace qg

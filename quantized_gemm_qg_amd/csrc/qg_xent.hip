@@ -133,14 +133,11 @@ int64_t xent_piece(int64_t m, int64_t vocab) {
 template <int EPI>
 using XentFew = MmCfg<false, kRows, kRows, false, 32, 128, 1, 8, 4, true, EPI>;
 template <int EPI>
-static hipError_t xent_logits(const MmMoreArgs &a, hipStream_t s, MmInfo *info) {
-  return mm_dispatch<MmCfg<false, kRows, kRows, false, 256, 256, 4, 2, 2, false, EPI>,
-                     MmCfg<false, kRows, kRows, false, 192, 256, 4, 2, 2, false, EPI>,
-                     MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 2, true, EPI>,
-                     MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 4, true, EPI>,
-                     MmCfg<false, kRows, kRows, false, 64, 128, 2, 4, 3, true, EPI>,
-                     XentFew<EPI>>(a, kMmPartialBytes, s, info);
-}
+using XentLogits = MmShapes<MmCfg<false, kRows, kRows, false, 256, 256, 4, 2, 2, false, EPI>,
+                            MmCfg<false, kRows, kRows, false, 192, 256, 4, 2, 2, false, EPI>,
+                            MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 2, true, EPI>,
+                            MmCfg<false, kRows, kRows, false, 128, 128, 4, 2, 4, true, EPI>,
+                            MmCfg<false, kRows, kRows, false, 64, 128, 2, 4, 3, true, EPI>, XentFew<EPI>>;
 
 static MmMoreArgs xent_args(const XentCall &c, int64_t first, int64_t columns) {
   MmMoreArgs a = {};
@@ -166,10 +163,10 @@ hipError_t launch_xent(const XentCall &c, hipStream_t s, MmInfo *info) {
   a.stats = c.stats;
   a.at_target = c.at_target;
   MmInfo choice;
-  hipError_t e = xent_logits<kXentStats>(a, nullptr, &choice);
+  hipError_t e = XentLogits<kXentStats>::dispatch(a, kMmPartialBytes, nullptr, &choice);
   if (info) *info = choice;
   if (info || e != hipSuccess) return e;
-  e = xent_logits<kXentStats>(a, s, nullptr);
+  e = XentLogits<kXentStats>::dispatch(a, kMmPartialBytes, s, nullptr);
   if (e != hipSuccess) return e;
   const int tiles = (int)((c.vocab + choice.bn - 1) / choice.bn);
   hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)((c.m + 15) / 16)), dim3(1024), 0, s, (const float2 *)c.stats,
@@ -199,7 +196,7 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
   a.otype = QG_O_BF16;
   a.halves = (int32_t)xent_halves(c.m);
   if (a.halves > 0) return mm_dispatch<XentFew<kXentGrad>>(a, kMmPartialBytes, s, info);
-  return xent_logits<kXentGrad>(a, s, info);
+  return XentLogits<kXentGrad>::dispatch(a, kMmPartialBytes, s, info);
 }
 
 // d W of one piece into parts of dx.  The contraction is long and the tiles are
@@ -208,6 +205,10 @@ hipError_t launch_xent_d(const XentCall &c, int64_t first, int64_t columns, hipS
 // 50000 x 2048: 256 x 256 in 16 parts 108 us, 128 x 128 in 4 151 (two stages 152); 257
 // of 38531 x 1032: 128 x 128 in 8 parts 58, 256 x 256 70, 64 x 128 61.
 // info->splits: how many parts the piece has; there: how many hold earlier pieces.
+using XentDxFew = MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true, kParts>;
+using XentDx = MmShapes<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, true, kParts>,
+                        MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true, kParts>,
+                        MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true, kParts>, XentDxFew>;
 hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int there, hipStream_t s, MmInfo *info) {
   MmMoreArgs a = xent_args(c, first, columns);
   a.a = (const uint8_t *)c.d;
@@ -219,15 +220,12 @@ hipError_t launch_xent_dx(const XentCall &c, int64_t first, int64_t columns, int
   a.ldy = c.k;
   a.part_stride = c.m * c.k;
   a.parts_there = there;
-  using Few = MmCfg<false, kRows, kCols, false, 32, 128, 1, 8, 4, true, kParts>;
   if (c.m <= 16) {
     a.halves = (int32_t)xent_halves(c.m);
     a.m += a.halves;
-    return mm_dispatch<Few>(a, kXentPartBytes, s, info);
+    return mm_dispatch<XentDxFew>(a, kXentPartBytes, s, info);
   }
-  return mm_dispatch<MmCfg<false, kRows, kCols, false, 256, 256, 4, 2, 2, true, kParts>,
-                     MmCfg<false, kRows, kCols, false, 128, 128, 4, 2, 4, true, kParts>,
-                     MmCfg<false, kRows, kCols, false, 64, 128, 2, 4, 4, true, kParts>, Few>(a, kXentPartBytes, s, info);
+  return XentDx::dispatch(a, kXentPartBytes, s, info);
 }
 
 hipError_t launch_xent_dx_sum(const XentCall &c, int parts, void *dx, int64_t lddx, hipStream_t s) {
@@ -238,6 +236,9 @@ hipError_t launch_xent_dx_sum(const XentCall &c, int parts, void *dx, int64_t ld
 }
 
 // rows of dW of one piece
+using XentDw = MmShapes<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 2, false, kScaled>,
+                        MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 2, true, kScaled>,
+                        MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 4, true, kScaled>>;
 hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, void *dw, int dw_type, int64_t lddw,
                           hipStream_t s, MmInfo *info) {
   MmMoreArgs a = xent_args(c, first, columns);
@@ -253,9 +254,24 @@ hipError_t launch_xent_dw(const XentCall &c, int64_t first, int64_t columns, voi
   a.ldy = lddw;
   a.halves = (int32_t)xent_halves(c.m);
   a.kd = (int32_t)c.m + a.halves;
-  return mm_dispatch<MmCfg<false, kCols, kCols, false, 256, 256, 4, 2, 2, false, kScaled>,
-                     MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 2, true, kScaled>,
-                     MmCfg<false, kCols, kCols, false, 128, 128, 4, 2, 4, true, kScaled>>(a, kMmPartialBytes, s, info);
+  return XentDw::dispatch(a, kMmPartialBytes, s, info);
+}
+
+// Bounds for any call of up to m tokens, which may have other shapes, parts and pieces
+// than one of m: a buffer for the largest batch serves the smaller ones.
+XentMost xent_most(int64_t m, int64_t k, int64_t vocab) {
+  const int64_t whole = (vocab + 63) / 64 * 64;  // a piece at most
+  const int64_t rows = m <= 16 ? m + 16 : m <= 32 ? m + 32 : std::max<int64_t>(m, 64);  // xent_d_rows at most
+  XentMost b;
+  b.partials = XentLogits<kXentStats>::most_bytes(m, vocab, k, kMmPartialBytes);
+  b.stat_tiles = (vocab + XentLogits<kXentStats>::narrowest - 1) / XentLogits<kXentStats>::narrowest;
+  b.back_partials = std::max(XentLogits<kXentGrad>::most_bytes(m, whole, k, kMmPartialBytes),
+                             XentDw::most_bytes(whole, k, rows, kMmPartialBytes));
+  // (pieces of up to 64 Mi / m columns, at least 8192, at most 2^20)
+  b.d = 2 * (uint64_t)std::min(std::max<int64_t>(64ll << 20, 8192 * m), rows * whole);
+  const uint64_t part = 4 * (uint64_t)m * k;
+  b.parts = std::max(part, std::min(part * kMmMostSplits, XentDx::most_bytes(rows, k, whole, kXentPartBytes)));
+  return b;
 }
 
 }  // namespace qg

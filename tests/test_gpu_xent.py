@@ -317,3 +317,24 @@ def test_two_graphs_share_a_workspace(m, k, vocab):
     step(cases[0], outs[0])
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(outs[0], want[0]))
+
+
+def test_a_workspace_for_more_tokens():
+    """One buffer, allocated for the largest batch, for smaller ones, which split otherwise."""
+    largest, k, vocab = 300, 520, 3001
+    n_f, n_b = qg.linear_xent_workspace_size(largest, k, vocab), qg.linear_xent_backward_workspace_size(largest, k, vocab)
+    ws = torch.zeros(max(n_f, n_b) + 256, dtype=torch.uint8, device="cuda")
+    ws[max(n_f, n_b):] = 7
+    for m in (1, 20, 60, 129, 256, 299):
+        c = Case(m, k, vocab, seed=m)
+        c.solve()
+        c.ws, c.fwd_bytes, c.bwd_bytes = ws, n_f, n_b
+        loss, lse = c.forward()
+        within(lse, c.lse, c.e_lse)
+        within(loss, c.loss, c.e_loss)
+        few = 2.0 ** -16
+        dx, dw, b_dx, b_dw = c.gradients(few if m <= 16 else U16, few if m <= 32 else U16)
+        got_dx, got_dw = c.backward(lse)
+        within(got_dx, dx, b_dx * (1 + U16) + U16 * dx.abs() + 1e-37)
+        within(got_dw, dw, b_dw + 2 * U32 * dw.abs() + 1e-37)
+        assert (ws[max(n_f, n_b):] == 7).all()

@@ -174,3 +174,22 @@ def test_a_workspace_of_the_adapters_serves_fewer_rows():
                 if need:   # (the size is looked at before the alignment, which ends the call here)
                     refuses(ALIGNMENT, lora, m=m, k=k, ldx=k, lda=k, n=n, ldy=n, adapters=adapters, rank=rank, ldb=rank, ws=DEV + 64,
                             wsb=size)
+
+
+@pytest.mark.parametrize("size,call", [(qg.linear_xent_workspace_size, xent), (qg.linear_xent_backward_workspace_size, xent_back)])
+@pytest.mark.parametrize("k,vocab,upto", [(4096, 3000, 1100), (1024, 128000, 700), (64, 50, 300), (520, 1100001, 70), (1032, 38531, 600)])
+def test_a_workspace_of_the_cross_entropy_serves_fewer_tokens(size, call, k, vocab, upto):
+    sizes = [size(m, k, vocab) for m in range(upto + 1)]
+    assert sizes == sorted(sizes)
+    sizes += [size(m, k, vocab) for m in (5000, 8191, 8192, 8193, 20000, 70000, 1 << 20)]
+    assert sizes == sorted(sizes)
+    more = dict(lddx=k, lddw=k) if call is xent_back else {}
+    for largest in (20, 33, 64, upto):
+        for m in range(1, largest + 1):   # (the size is looked at before the alignment, which ends the call here)
+            refuses(ALIGNMENT, call, m=m, k=k, ldx=k, ldw=k, vocab=vocab, ws=DEV + 64, wsb=sizes[largest], **more)
+
+
+def test_a_workspace_of_the_norm_serves_fewer_rows():
+    for k in (64, 1024, 1032, 4096, 1 << 20):
+        sizes = [qg.rmsnorm_backward_workspace_size(rows, k) for rows in [*range(700), 2047, 2048, 2049, 1 << 20]]
+        assert sizes == sorted(sizes)
