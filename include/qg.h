@@ -747,6 +747,12 @@ qg_status qg_describe_dispatch_ex(const qg_weight *w, int64_t m, uint32_t flags,
 qg_status qg_describe_moe_dispatch(const qg_weight *w, int64_t num_tokens, int32_t topk, char *buf,
                                    uint64_t buf_bytes);
 
+/* The kernels that qg_lora takes for these sizes, as text: one launch, or the two
+ * with their blocks of the rank, parts of k, 16-row blocks, steps of the rank and
+ * column chunks. */
+qg_status qg_describe_lora(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank, int32_t y_type, char *buf,
+                           uint64_t buf_bytes);
+
 /* Static description of a status code (never NULL). */
 const char *qg_status_string(qg_status status);
 

@@ -39,7 +39,7 @@ EXPORTS = (
     "qg_ffn_gated_workspace_size", "qg_ffn_gated", "qg_ffn_gated_backward_workspace_size", "qg_ffn_gated_backward",
     "qg_token_logprobs_workspace_size", "qg_token_logprobs", "qg_token_logprobs_backward",
     "qg_rmsnorm", "qg_rmsnorm_backward_workspace_size", "qg_rmsnorm_backward",
-    "qg_lora_workspace_size", "qg_lora",
+    "qg_lora_workspace_size", "qg_lora", "qg_describe_lora",
     "qg_linear_xent_workspace_size", "qg_linear_xent", "qg_linear_xent_backward_workspace_size", "qg_linear_xent_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -132,6 +132,7 @@ def _load():
         "qg_rmsnorm_backward": (I32, [P, I32, I64, P, ctypes.c_float, I64, I64, P, I64, P, I64, P, I64, P, I32, P, U64, P]),
         "qg_lora_workspace_size": (I32, [I64, I64, I64, I32, I32, ctypes.POINTER(U64)]),
         "qg_lora": (I32, [P, I64, P, I64, P, I64, P, I32, I32, P, P, I64, I64, I64, P, I32, I64, P, U64, P]),
+        "qg_describe_lora": (I32, [I64, I64, I64, I32, I32, I32, ctypes.c_char_p, U64]),
         "qg_linear_xent_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
         "qg_linear_xent": (I32, [P, I64, P, I64, I64, I64, I64, P, ctypes.c_float, P, P, P, U64, P]),
         "qg_linear_xent_backward_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
@@ -428,6 +429,12 @@ def lora(x, ldx: int, a, lda: int, b, ldb: int, scales, num_adapters: int, rank:
     """y[r] += scales[i] (x[r] a[i]^T) b[i]^T for the rows of every adapter i, grouped by moe_sort of their adapter ids."""
     _check(_lib.qg_lora(_ptr(x), ldx, _ptr(a), lda, _ptr(b), ldb, _ptr(scales), num_adapters, rank, _ptr(sorted_rows),
                         _ptr(offsets), m, k, n, _ptr(y), y_type, ldy, _ptr(ws), ws_bytes, _stream(stream)), "qg_lora")
+
+
+def describe_lora(m: int, k: int, n: int, num_adapters: int, rank: int, y_type: int) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(_lib.qg_describe_lora(m, k, n, num_adapters, rank, y_type, buf, 256), "qg_describe_lora")
+    return buf.value.decode()
 
 
 def linear_xent_workspace_size(m: int, k: int, vocab: int) -> int:

@@ -525,14 +525,19 @@ struct LoraArgs {
   void *y;
   int64_t ldy;
   bool y_vectors;  // y's rows are 16-byte aligned
-  float *t;        // [splits][m][rank]; NULL: one launch (lora_small)
-  int32_t splits;
-  int32_t chunks;  // (set by the launch) 256-column chunks of a workgroup
+  float *t;        // [splits][m][rank]; NULL: one launch
+  int32_t splits, chunks;  // (set by the launch)
 };
-bool lora_small(int64_t m, int64_t k, int64_t n, int adapters, int rank);
-int lora_splits(int64_t m, int64_t k, int adapters);
+// The kernels of a call: blocks of 16 of the rank; two launches: parts of k, and of
+// the second product 16-row blocks, 32-steps of the rank in registers and 256-column
+// chunks of a workgroup.
+struct LoraPlan {
+  bool small;  // one launch
+  int32_t nb, splits, rb, sd, chunks;
+};
+LoraPlan lora_plan(int64_t m, int64_t k, int64_t n, int adapters, int rank, bool y_f32);
 int64_t lora_most_rows(int64_t m, int64_t k);
-hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s);
+hipError_t launch_lora(LoraArgs a, const LoraPlan &p, bool y_f32, hipStream_t s);
 hipError_t launch_moe_sort(const int32_t *ids, int64_t pairs, int32_t experts,
                            int32_t *sorted, int32_t *offsets, int32_t *ws_counts,
                            hipStream_t s);

@@ -3,6 +3,7 @@
 // head.  Argument checks, workspaces and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 
 #include "qg_internal.h"
 
@@ -100,9 +101,8 @@ static qg_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t adapters, i
   return QG_OK;
 }
 
-// Bytes for `t_rows` fp32 rows of the first product's parts (0: one launch, no workspace).
-static uint64_t lora_bytes(int64_t t_rows, int64_t m, int64_t k, int64_t n, int32_t adapters, int32_t rank) {
-  if (m == 0 || lora_small(m, k, n, adapters, rank)) return 0;
+// Bytes for `t_rows` fp32 rows of the first product's parts.
+static uint64_t lora_bytes(int64_t t_rows, int32_t rank) {
   return kSplitCounterBytes + align_up((uint64_t)t_rows * rank * 4, 256);
 }
 
@@ -111,7 +111,8 @@ extern "C" qg_status qg_lora_workspace_size(int64_t m, int64_t k, int64_t n, int
                                             uint64_t *bytes) {
   if (!bytes) return QG_ERR_INVALID_ARGUMENT;
   QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
-  *bytes = lora_bytes(lora_most_rows(m, k), m, k, n, num_adapters, rank);
+  const bool none = m == 0 || lora_plan(m, k, n, num_adapters, rank, false).small;
+  *bytes = none ? 0 : lora_bytes(lora_most_rows(m, k), rank);
   return QG_OK;
 }
 
@@ -130,14 +131,29 @@ extern "C" qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t 
   if (!aligned(y, el_of(y_type)) || !aligned(scales, 4) || !aligned(sorted_rows, 4) || !aligned(offsets, 4))
     return QG_ERR_ALIGNMENT;
   if (m == 0) return QG_OK;
-  const int splits = lora_splits(m, k, num_adapters);
-  const uint64_t need = lora_bytes(splits * m, m, k, n, num_adapters, rank);
-  QG_TRY(ws_check(need, ws, ws_bytes));
+  const LoraPlan plan = lora_plan(m, k, n, num_adapters, rank, y_type == QG_O_F32);
+  if (!plan.small) QG_TRY(ws_check(lora_bytes(plan.splits * m, rank), ws, ws_bytes));
   const bool vectors = aligned(y, 16) && ldy * el_of(y_type) % 16 == 0;
   const LoraArgs args{(const uint16_t *)x, ldx, (const uint16_t *)a, lda, (const uint16_t *)b, ldb, scales, sorted_rows, offsets,
                       num_adapters, rank, (int32_t)m, (int32_t)k, (int32_t)n, y, ldy, vectors,
-                      need ? (float *)((uint8_t *)ws + kSplitCounterBytes) : nullptr, splits, 0};
-  return hip_status(launch_lora(args, y_type == QG_O_F32, stream));
+                      plan.small ? nullptr : (float *)((uint8_t *)ws + kSplitCounterBytes), plan.splits, plan.chunks};
+  return hip_status(launch_lora(args, plan, y_type == QG_O_F32, stream));
+}
+
+extern "C" qg_status qg_describe_lora(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank, int32_t y_type,
+                                      char *buf, uint64_t buf_bytes) {
+  if (!buf || buf_bytes == 0 || !out_type(y_type)) return QG_ERR_INVALID_ARGUMENT;
+  QG_TRY(lora_sizes(m, k, n, num_adapters, rank));
+  if (m == 0) {
+    snprintf(buf, buf_bytes, "nothing");
+    return QG_OK;
+  }
+  const LoraPlan p = lora_plan(m, k, n, num_adapters, rank, y_type == QG_O_F32);
+  if (p.small)
+    snprintf(buf, buf_bytes, "lora_small NB=%d", p.nb);
+  else
+    snprintf(buf, buf_bytes, "lora_down NB=%d splits=%d; lora_up RB=%d SD=%d chunks=%d", p.nb, p.splits, p.rb, p.sd, p.chunks);
+  return QG_OK;
 }
 
 namespace qg {

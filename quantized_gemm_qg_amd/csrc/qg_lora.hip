@@ -460,7 +460,7 @@ static int64_t lora_items(int64_t m, int adapters, int rows) { return std::min<i
 // Parts of k: workgroups for the CUs, of about 8 stages of 64 or more (the last one has
 // what is left).
 static int64_t lora_most_splits(int64_t k) { return std::min<int64_t>((k + 511) / 512, 16); }
-int lora_splits(int64_t m, int64_t k, int adapters) {
+static int lora_splits(int64_t m, int64_t k, int adapters) {
   return (int)std::min(std::max<int64_t>(256 / lora_items(m, adapters, 16), 1), lora_most_splits(k));
 }
 // Parts times rows of any call of up to m rows: s > 1 parts of r rows have s items <=
@@ -475,11 +475,42 @@ int64_t lora_most_rows(int64_t m, int64_t k) {
 // rows of 8 adapters, n 14336, rank 16 7.5 / 8.3 (8.0 / 10.1), 4 rows, rank 32 8.2 /
 // 8.4 (8.1 / 10.1), rank 64 10.5 / 9.4; k 14336, rank 16 11.6 / 9.1; 64 rows, k 1024
 // 5.1 / 7.3.
-bool lora_small(int64_t m, int64_t k, int64_t n, int adapters, int rank) {
+static bool lora_small(int64_t m, int64_t k, int64_t n, int adapters, int rank) {
   return rank <= 64 && rank * k <= 32 * 4096 && lora_items(m, adapters, 16) * ((n + 511) / 512) <= 256;
 }
 
-hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s) {
+LoraPlan lora_plan(int64_t m, int64_t k, int64_t n, int adapters, int rank, bool y_f32) {
+  const int units = rank / 8;
+  LoraPlan p = {};
+  p.small = lora_small(m, k, n, adapters, rank);
+  p.nb = units <= 2 ? 1 : units <= 4 ? 2 : units <= 8 ? 4 : units <= 16 ? 8 : 16;
+  if (p.small) return p;
+  p.splits = lora_splits(m, k, adapters);
+  p.sd = units <= 4 ? 1 : units <= 8 ? 2 : 4;
+  // Second product: rows of an item as many as the adapters have on average, as long
+  // as workgroups are left for the CUs.
+  const int64_t columns = (n + 255) / 256;
+  p.rb = 4;
+  while (p.rb > 1 && (m < 8ll * p.rb * adapters || lora_items(m, adapters, 16 * p.rb) * columns < 1024)) p.rb /= 2;
+  // Chunks of a workgroup: rounds of the CUs times the chunks and what comes ahead
+  // of them (of the items that may be, half of the adapters' last ones are there).
+  // Many rows: workgroups side by side a multiple of the XCDs, each of which then
+  // reads its own columns of B (4096 rows, n 14336, rank 64: 8 side by side 54.9 us,
+  // 10 67.5, 19 62.3, 56 64.4; 44 rows of 35 adapters: 56 11.4, 28 8.3, 19 9.1).
+  const double expected = (double)m / (16 * p.rb) + 0.5 * (double)std::min<int64_t>(adapters, m);
+  const int places = 256 * (p.rb == 4 ? (y_f32 ? 2 : 3) : p.rb == 2 ? (y_f32 ? 3 : 4) : 5);
+  double best = 0;
+  for (int64_t c = 1; c <= std::min<int64_t>(columns, 32); ++c) {
+    const int64_t side = (columns + c - 1) / c;
+    const double cost = std::ceil(expected * side / places) * (c + 1) * (p.rb > 1 && side % kXcds != 0 ? 1.25 : 1.);
+    if (c > 1 && cost >= best) continue;
+    best = cost;
+    p.chunks = (int32_t)c;
+  }
+  return p;
+}
+
+hipError_t launch_lora(LoraArgs a, const LoraPlan &p, bool y_f32, hipStream_t s) {
   hipError_t e = hipSuccess;
   auto launch = [&](auto kern, const dim3 &grid, int threads, int lds) {
     if (lds > 64 * 1024) e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -487,79 +518,60 @@ hipError_t launch_lora(LoraArgs a, bool y_f32, hipStream_t s) {
     hipLaunchKernelGGL(kern, grid, dim3(threads), lds, s, a);
     e = hipGetLastError();
   };
-  if (!a.t) {
+  if (p.small) {
     const dim3 grid((unsigned)((a.n + 511) / 512), (unsigned)lora_items(a.m, a.adapters, 16));
     auto small = [&](auto blocks, auto stages) {
       constexpr int NB = decltype(blocks)::value, ST = decltype(stages)::value, LDS = 8 * ST * (1 + NB) * 2048;
       y_f32 ? launch(lora_small_kernel<NB, ST, true>, grid, 512, LDS) : launch(lora_small_kernel<NB, ST, false>, grid, 512, LDS);
     };
-    if (a.rank <= 16)
+    if (p.nb == 1)
       small(Int<1>(), Int<4>());
-    else if (a.rank <= 32)
+    else if (p.nb == 2)
       small(Int<2>(), Int<3>());
     else
       small(Int<4>(), Int<2>());
     return e;
   }
+  a.splits = p.splits;
+  a.chunks = p.chunks;
   auto down = [&](auto blocks, auto waves, auto stages) {
     constexpr int NB = decltype(blocks)::value, KW = decltype(waves)::value, ST = decltype(stages)::value;
     launch(lora_down_kernel<NB, KW, ST>, dim3((unsigned)lora_items(a.m, a.adapters, 16), a.splits), 64 * KW,
            KW * ST * (1 + NB) * 2048);
   };
   // (rings of 3 stages where two workgroups of them fit a CU)
-  if (a.rank <= 16)
+  if (p.nb == 1)
     down(Int<1>(), Int<4>(), Int<3>());
-  else if (a.rank <= 32)
+  else if (p.nb == 2)
     down(Int<2>(), Int<4>(), Int<3>());
-  else if (a.rank <= 64)
+  else if (p.nb == 4)
     down(Int<4>(), Int<4>(), Int<2>());
-  else if (a.rank <= 128)
+  else if (p.nb == 8)
     down(Int<8>(), Int<4>(), Int<2>());
   else
     down(Int<16>(), Int<2>(), Int<2>());
   if (e != hipSuccess) return e;
 
-  // Second product: rows of an item as many as the adapters have on average, as long
-  // as workgroups are left for the CUs.
   const int64_t columns = (a.n + 255) / 256;
-  int rb = 4;
-  while (rb > 1 && (a.m < 8ll * rb * a.adapters || lora_items(a.m, a.adapters, 16 * rb) * columns < 1024)) rb /= 2;
-  const int64_t rows = lora_items(a.m, a.adapters, 16 * rb);
-  // Chunks of a workgroup: rounds of the CUs times the chunks and what comes ahead
-  // of them (of the items that may be, half of the adapters' last ones are there).
-  // Many rows: workgroups side by side a multiple of the XCDs, each of which then
-  // reads its own columns of B (4096 rows, n 14336, rank 64: 8 side by side 54.9 us,
-  // 10 67.5, 19 62.3, 56 64.4; 44 rows of 35 adapters: 56 11.4, 28 8.3, 19 9.1).
-  const double expected = (double)a.m / (16 * rb) + 0.5 * (double)std::min<int64_t>(a.adapters, a.m);
-  const int places = 256 * (rb == 4 ? (y_f32 ? 2 : 3) : rb == 2 ? (y_f32 ? 3 : 4) : 5);
-  double best = 0;
-  for (int64_t c = 1; c <= std::min<int64_t>(columns, 32); ++c) {
-    const int64_t side = (columns + c - 1) / c;
-    const double cost = std::ceil(expected * side / places) * (c + 1) * (rb > 1 && side % kXcds != 0 ? 1.25 : 1.);
-    if (c > 1 && cost >= best) continue;
-    best = cost;
-    a.chunks = (int32_t)c;
-  }
   const int units = a.rank / 8, parts = y_f32 ? 3 : 2;
-  const int sd = units <= 4 ? 1 : units <= 8 ? 2 : 4;
-  const int lds_units = units <= 2 ? (parts * units + 3) / 4 * 4 : parts * ((units + 4 * sd - 1) / (4 * sd)) * 4 * sd;
-  const int lds = lds_units * (16 * rb + 1) * 16 + 4 * 16 * (64 * 4 + 16);
-  const dim3 grid((unsigned)((columns + a.chunks - 1) / a.chunks), (unsigned)rows);
+  const int lds_units = units <= 2 ? (parts * units + 3) / 4 * 4 : parts * ((units + 4 * p.sd - 1) / (4 * p.sd)) * 4 * p.sd;
+  const int lds = lds_units * (16 * p.rb + 1) * 16 + 4 * 16 * (64 * 4 + 16);
+  const dim3 grid((unsigned)((columns + a.chunks - 1) / a.chunks), (unsigned)lora_items(a.m, a.adapters, 16 * p.rb));
   auto up = [&](auto blocks, auto steps) {
     constexpr int RB = decltype(blocks)::value, SD = decltype(steps)::value;
     y_f32 ? launch(lora_up_kernel<RB, SD, true>, grid, 256, lds) : launch(lora_up_kernel<RB, SD, false>, grid, 256, lds);
   };
   auto with_rows = [&](auto blocks) {
-    if (sd == 1)
+    if (p.sd == 1)
       up(blocks, Int<1>());
-    else if (sd == 2)
+    else if (p.sd == 2)
       up(blocks, Int<2>());
     else
       up(blocks, Int<4>());
   };
-  if (rb == 4)
+  if (p.rb == 4)
     with_rows(Int<4>());
-  else if (rb == 2)
+  else if (p.rb == 2)
     with_rows(Int<2>());
   else
     with_rows(Int<1>());

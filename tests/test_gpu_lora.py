@@ -6,6 +6,7 @@ three (2^-23); y is rounded once."""
 import pytest
 import torch
 
+import lora_sizes
 import quantized_gemm_qg_amd as qg
 from gpu_harness import require_gpu
 
@@ -219,3 +220,34 @@ def test_a_workspace_for_more_rows():
         c.ws = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
         c.check(c.run())
         assert (c.ws[size:] == 255).all()
+
+
+@pytest.mark.parametrize("m,k,n,rank,adapters", lora_sizes.EVERY_KERNEL)
+@pytest.mark.parametrize("y_type", [qg.O_BF16, qg.O_F32])
+def test_every_kernel(m, k, n, rank, adapters, y_type):
+    prompts, shift = adapters > 8 and m > 500, n % 3 % 2   # (rows of every adapter side by side anyway; y on and off 16 bytes)
+    print(f"lora m={m} k={k} n={n} rank={rank} adapters={adapters} y={y_type} prompts={prompts} shift={shift}: "
+          f"{qg.describe_lora(m, k, n, adapters, rank, y_type)}", flush=True)
+    c = Case(m, k, n, rank, adapters, y_type, seed=m + n, prompts=prompts, pad=8 - n % 8, shift=shift, none=0.0 if m < 10 else 0.15)
+    c.call()
+    torch.cuda.synchronize()
+    assert (c.flat[:shift] == 7).all() and (c.flat[shift + m * c.ldy:] == 7).all() and (c.yd[:, n:] == 7).all()
+    # as Case.check, on the GPU
+    u, part = (U32, 2.0 ** -23) if y_type == qg.O_F32 else (U16, 2.0 ** -16)
+    got, before = c.yd[:, :n], c.before[shift:shift + m * c.ldy].view(m, c.ldy)[:, :n]
+    x, a, b, ids = c.x.cuda(), c.a.cuda(), c.b.cuda(), c.ids.cuda()
+    assert torch.equal(got[ids < 0], before[ids < 0])
+    for i in c.ids.unique().tolist():
+        if i < 0:
+            continue
+        at = (ids == i).nonzero()[:, 0]
+        xi, ai, bt = x[at].to(D), a[i].to(D).t().contiguous(), b[i].to(D).t().contiguous()
+        s = c.scales[i].item()
+        t, mag = s * torch.mm(xi, ai), s * torch.mm(xi.abs(), ai.abs())
+        e_t = mag * (2 * k + 2) * U32 + part * t.abs()
+        want = before[at].to(D) + torch.mm(t, bt)
+        bound = torch.mm(e_t + (t.abs() + e_t) * (6 * rank + 8) * U32, bt.abs())
+        bound = bound + (u + U32) * (want.abs() + bound) + 1e-37
+        off = (got[at].to(D) - want).abs() - bound
+        assert (off <= 0).all(), f"adapter {i}: {off.max().item():.3g} over the bound"
+    assert c.ids.max() >= 0

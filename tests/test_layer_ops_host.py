@@ -4,6 +4,7 @@ import ctypes
 
 import pytest
 
+import lora_sizes
 import quantized_gemm_qg_amd as qg
 
 DEV = 1 << 20   # a well-aligned address that is never read
@@ -193,3 +194,42 @@ def test_a_workspace_of_the_norm_serves_fewer_rows():
     for k in (64, 1024, 1032, 4096, 1 << 20):
         sizes = [qg.rmsnorm_backward_workspace_size(rows, k) for rows in [*range(700), 2047, 2048, 2049, 1 << 20]]
         assert sizes == sorted(sizes)
+
+
+def test_the_adapters_sizes_reach_every_kernel():
+    """The GPU tests run EVERY_KERNEL; a change of the rules must not turn them away from a kernel."""
+    for y_type in (qg.O_BF16, qg.O_F32):
+        small, down, parts, up, side, zeros, twice, tails = (set() for _ in range(8))
+        for m, k, n, rank, adapters in lora_sizes.EVERY_KERNEL:
+            t = lora_sizes.taken(m, k, n, rank, adapters, y_type)
+            if "splits" not in t:
+                small.add(t["NB"])
+                continue
+            s, stages = t["splits"], -(-k // 64)
+            down.add((t["NB"], 1 if s == 1 else 2 if s < 5 else 5))
+            parts |= {name for name, yes in (("all", s == 16), ("empty", (s - 1) * -(-stages // s) >= stages), ("group", s > 4 and s % 4))
+                      if yes}
+            up.add((t["RB"], t["SD"], min(t["chunks"], 2)))
+            if rank <= 16:
+                side.add((rank, t["RB"]))
+            elif rank // 8 % (4 * t["SD"]):
+                zeros.add((t["RB"], t["SD"]))
+            if rank > 128:
+                twice.add(t["RB"])   # two groups of the rank
+            tails.add((n % 8 != 0, t["RB"]))
+        assert small == {1, 2, 4}
+        assert down == {(nb, s) for nb in (1, 2, 4, 8, 16) for s in (1, 2, 5)} and parts == {"all", "empty", "group"}
+        assert up == {(rb, sd, chunks) for rb in (1, 2, 4) for sd in (1, 2, 4) for chunks in (1, 2)}
+        assert side == {(rank, rb) for rank in (8, 16) for rb in (1, 2, 4)}
+        assert zeros == {(rb, sd) for rb in (1, 2, 4) for sd in (1, 2, 4)}
+        assert twice == {1, 2, 4} and tails == {(odd, rb) for odd in (False, True) for rb in (1, 2, 4)}
+
+
+def test_describe_lora():
+    assert qg.describe_lora(0, 64, 100, 3, 16, qg.O_BF16) == "nothing"
+    assert qg.describe_lora(1, 4096, 4096, 8, 16, qg.O_BF16) == "lora_small NB=1"
+    out = ctypes.create_string_buffer(64)
+    call = lambda *a: qg._lib.qg_describe_lora(*a)  # noqa: E731
+    assert call(1, 64, 100, 3, 16, 2, out, 64) == INVALID and call(1, 64, 100, 3, 16, qg.O_F32, None, 64) == INVALID
+    assert call(1, 64, 100, 3, 16, qg.O_F32, out, 0) == INVALID and call(-1, 64, 100, 3, 16, qg.O_F32, out, 64) == INVALID
+    assert call(1, 60, 100, 3, 16, qg.O_F32, out, 64) == SHAPE and call(1, 64, 100, 3, 264, qg.O_F32, out, 64) == UNSUPPORTED
