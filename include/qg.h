@@ -753,6 +753,11 @@ qg_status qg_describe_moe_dispatch(const qg_weight *w, int64_t num_tokens, int32
 qg_status qg_describe_lora(int64_t m, int64_t k, int64_t n, int32_t num_adapters, int32_t rank, int32_t y_type, char *buf,
                            uint64_t buf_bytes);
 
+/* The shapes of the products that qg_linear_xent (the first) and
+ * qg_linear_xent_backward (the others, for the pieces of the vocabulary) take, as
+ * text: tile, stages in LDS and parts of the contraction. */
+qg_status qg_describe_linear_xent(int64_t m, int64_t k, int64_t vocab, char *buf, uint64_t buf_bytes);
+
 /* Static description of a status code (never NULL). */
 const char *qg_status_string(qg_status status);
 

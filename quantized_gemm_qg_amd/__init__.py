@@ -41,6 +41,7 @@ EXPORTS = (
     "qg_rmsnorm", "qg_rmsnorm_backward_workspace_size", "qg_rmsnorm_backward",
     "qg_lora_workspace_size", "qg_lora", "qg_describe_lora",
     "qg_linear_xent_workspace_size", "qg_linear_xent", "qg_linear_xent_backward_workspace_size", "qg_linear_xent_backward",
+    "qg_describe_linear_xent",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 GEMM_BATCH_INVARIANT, GEMM_QUANTIZE_X = 1, 2
@@ -138,6 +139,7 @@ def _load():
         "qg_linear_xent_backward_workspace_size": (I32, [I64, I64, I64, ctypes.POINTER(U64)]),
         "qg_linear_xent_backward": (I32, [P, I64, P, I64, I64, I64, I64, P, ctypes.c_float, P, P, P, I64, P, I32, I64, P, U64,
                                           P]),
+        "qg_describe_linear_xent": (I32, [I64, I64, I64, ctypes.c_char_p, U64]),
         "qg_autotune_reset": (None, []),
         "qg_set_override": (I32, [ctypes.c_char_p, ctypes.c_char_p]),
         "qg_clear_overrides": (None, []),
@@ -459,6 +461,12 @@ def linear_xent_backward(x, ldx: int, w, ldw: int, m: int, k: int, vocab: int, t
     _check(_lib.qg_linear_xent_backward(_ptr(x), ldx, _ptr(w), ldw, m, k, vocab, _ptr(targets), scale, _ptr(lse), _ptr(dloss),
                                         _ptr(dx), lddx, _ptr(dw), dw_type, lddw, _ptr(ws), ws_bytes, _stream(stream)),
            "qg_linear_xent_backward")
+
+
+def describe_linear_xent(m: int, k: int, vocab: int) -> str:
+    buf = ctypes.create_string_buffer(512)
+    _check(_lib.qg_describe_linear_xent(m, k, vocab, buf, 512), "qg_describe_linear_xent")
+    return buf.value.decode()
 
 
 def silu_mul(gu, gu_type: int, rows: int, inter: int, ldgu: int, h, h_type: int, ldh: int,

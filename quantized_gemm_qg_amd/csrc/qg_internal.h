@@ -369,7 +369,7 @@ hipError_t launch_moe_combine(const void *y, bool y_f32, int64_t ldy, const floa
 // kernel), parts of k, and the bytes of its partial tiles.
 struct MmInfo {
   uint64_t bytes = 0;
-  int bm = 0, bn = 0, splits = 1;
+  int bm = 0, bn = 0, splits = 1, stages = 0;  // stages: of the LDS ring
 };
 // int8 products (qg_int8.hip): quantized rows (x int8 [m][ldx], x_scales [m])
 // times the packed codes; gated: n outputs from 2 n weight columns; quantize:

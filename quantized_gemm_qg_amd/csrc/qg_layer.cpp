@@ -324,3 +324,33 @@ extern "C" qg_status qg_linear_xent_backward(const void *x, int64_t ldx, const v
   if (e == hipSuccess && dx) e = launch_xent_dx_sum(c, std::max(sp.splits, sp.last_splits), dx, lddx, stream);
   return hip_status(e);
 }
+
+extern "C" qg_status qg_describe_linear_xent(int64_t m, int64_t k, int64_t vocab, char *buf, uint64_t buf_bytes) {
+  if (!buf || buf_bytes == 0 || m < 0 || k < 0 || vocab < 0) return QG_ERR_INVALID_ARGUMENT;
+  if (k == 0 || k % 8 != 0 || vocab == 0) return QG_ERR_SHAPE;
+  if (!xent_in_range(m, k, vocab)) return QG_ERR_UNSUPPORTED;
+  char out[512] = "nothing";
+  int at = 0;
+  MmInfo i;
+  auto add = [&](const char *name, hipError_t) {  // (the choice is in i)
+    at += snprintf(out + at, sizeof out - at, "%s BM=%d BN=%d stages=%d splits=%d", name, i.bm, i.bn, i.stages, i.splits);
+  };
+  if (m > 0) {
+    const XentCall c = xent_call(nullptr, k, nullptr, k, m, k, vocab, nullptr, 1.f);
+    add("logits", launch_xent(c, nullptr, &i));
+    const int64_t piece = xent_piece(m, vocab), pieces = (vocab + piece - 1) / piece, last = vocab - (pieces - 1) * piece;
+    // pieces of full length, and a last one of another
+    const int64_t full = last == piece ? pieces : pieces - 1;
+    for (int64_t columns : {piece, last}) {
+      const int64_t count = columns == piece ? full : 1;
+      if (count == 0) continue;
+      at += snprintf(out + at, sizeof out - at, "; %lld x %lld:", (long long)count, (long long)columns);
+      add(" d", launch_xent_d(c, 0, columns, nullptr, &i));
+      add(", dx", launch_xent_dx(c, 0, columns, 0, nullptr, &i));
+      add(", dw", launch_xent_dw(c, 0, columns, nullptr, 0, 0, nullptr, &i));
+      if (last == piece) break;
+    }
+  }
+  snprintf(buf, buf_bytes, "%s", out);
+  return QG_OK;
+}

@@ -884,7 +884,7 @@ static hipError_t mm_dispatch(const typename C0::Args &a, uint64_t budget, hipSt
     using C = std::remove_pointer_t<decltype(cfg)>;
     if (i++ != best) return;
     if (info) {
-      *info = MmInfo{mm_partial_bytes<C>(a.m, a.n, plans[best]), C::BM, C::BN, plans[best].splits};
+      *info = MmInfo{mm_partial_bytes<C>(a.m, a.n, plans[best]), C::BM, C::BN, plans[best].splits, C::ST};
       e = hipSuccess;
     } else {
       e = launch_mm<C>(a, plans[best], s);

@@ -338,3 +338,11 @@ def test_a_workspace_for_more_tokens():
         within(got_dx, dx, b_dx * (1 + U16) + U16 * dx.abs() + 1e-37)
         within(got_dw, dw, b_dw + 2 * U32 * dw.abs() + 1e-37)
         assert (ws[max(n_f, n_b):] == 7).all()
+
+
+MORE_TILES = [(3589, 1280, 1574)]   # dw in parts of two stages
+
+
+@pytest.mark.parametrize("m,k,vocab", MORE_TILES)
+def test_more_tile_shapes(m, k, vocab):
+    test_forward_and_backward(m, k, vocab)

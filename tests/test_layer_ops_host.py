@@ -1,6 +1,7 @@
 """Refusals of the root-mean-square norm, the low-rank adapters and the cross
 entropy of a head (no GPU: every check comes before the first device call)."""
 import ctypes
+import re
 
 import pytest
 
@@ -233,3 +234,28 @@ def test_describe_lora():
     assert call(1, 64, 100, 3, 16, 2, out, 64) == INVALID and call(1, 64, 100, 3, 16, qg.O_F32, None, 64) == INVALID
     assert call(1, 64, 100, 3, 16, qg.O_F32, out, 0) == INVALID and call(-1, 64, 100, 3, 16, qg.O_F32, out, 64) == INVALID
     assert call(1, 60, 100, 3, 16, qg.O_F32, out, 64) == SHAPE and call(1, 64, 100, 3, 264, qg.O_F32, out, 64) == UNSUPPORTED
+
+
+def test_the_cross_entropys_sizes_reach_every_tile_shape():
+    """Every compiled shape of the four products, whole and, where it may, in parts of the contraction: a change of
+    the cost model must not turn the GPU tests away from one."""
+    import test_gpu_xent as gpu
+    reached = set()
+    for size in gpu.SIZES + gpu.TILES + gpu.MORE_TILES:
+        for name, bm, bn, stages, splits in re.findall(r"(logits|d|dx|dw) BM=(\d+) BN=(\d+) stages=(\d+) splits=(\d+)",
+                                                       qg.describe_linear_xent(*size)):
+            reached.add((name, int(bm), int(bn), int(stages), int(splits) > 1))
+    whole = {("dw", 256, 256, 2)} | {(name, bm, 256, 2) for name in ("logits", "d") for bm in (192, 256)}
+    both = {("dx", 256, 256, 2), ("dx", 128, 128, 4), ("dx", 64, 128, 4), ("dx", 32, 128, 4), ("dw", 128, 128, 2), ("dw", 128, 128, 4)}
+    both |= {(name, *t) for name in ("logits", "d") for t in ((128, 128, 2), (128, 128, 4), (64, 128, 3), (32, 128, 4))}
+    assert reached == {(*t, False) for t in whole | both} | {(*t, True) for t in both}
+
+
+def test_describe_linear_xent():
+    assert qg.describe_linear_xent(0, 64, 100) == "nothing"
+    assert qg.describe_linear_xent(20, 16, 1100001).count(" x ") == 2   # two pieces, the last one shorter
+    assert "; 8 x 16384: d " in qg.describe_linear_xent(4096, 4096, 131072)
+    out = ctypes.create_string_buffer(64)
+    call = lambda *a: qg._lib.qg_describe_linear_xent(*a)  # noqa: E731
+    assert call(1, 64, 100, None, 64) == INVALID and call(1, 64, 100, out, 0) == INVALID and call(-1, 64, 100, out, 64) == INVALID
+    assert call(1, 60, 100, out, 64) == SHAPE and call(1, 64, 0, out, 64) == SHAPE and call(1, 64, (1 << 24) + 1, out, 64) == UNSUPPORTED
