@@ -298,3 +298,48 @@ def test_another_stream_and_a_captured_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(every, want)), i
+
+
+# more rows than a launch has workgroups (4096 of one or of four rows): every workgroup
+# or wave takes several in turn, and not all of them the last time
+TURNS = [(12300, 1032), (16391, 512), (16401, 1000)]
+
+
+@pytest.mark.parametrize("rows,k", TURNS)
+@pytest.mark.parametrize("x_type,res_type", [(BF, BF), (F32, None)])
+def test_forward_of_rows_in_turn(rows, k, x_type, res_type):
+    test_forward(rows, k, x_type, res_type)
+
+
+@pytest.mark.parametrize("rows,k", TURNS + [(9000, 2080), (36870, 64), (4101, 16416)])
+@pytest.mark.parametrize("x_type,res_type", [(BF, BF), (F32, F32)])
+def test_rows_in_turn_are_as_rows_apart(rows, k, x_type, res_type):
+    """The same bits from one call and from calls of a thousand rows, each of which a workgroup of its own takes."""
+    print(f"rmsnorm in turn rows={rows} k={k} x={x_type} res={res_type}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, k, generator=gen, device="cuda").to(ref.types(x_type))
+    res = torch.randn(rows, k, generator=gen, device="cuda").to(ref.types(res_type))
+    w = (1 + 0.3 * torch.randn(k, generator=gen, device="cuda")).to(torch.bfloat16)
+    for q_type in QS:
+        if q_type == qg.A_MXFP8 and k % 32:
+            continue
+        per = {qg.A_MXFP8: k // 32, qg.A_FP8_BLOCK: -(-k // 128)}.get(q_type, 1)
+        outs = []
+        for step in (rows, 1000):
+            s, y, q = torch.zeros_like(res), torch.zeros_like(x, dtype=torch.bfloat16), torch.zeros_like(x, dtype=torch.uint8)
+            qs = torch.zeros(rows, per, dtype=torch.uint8 if q_type == qg.A_MXFP8 else torch.float32, device="cuda")
+            for r in range(0, rows, step):
+                n = min(step, rows - r)
+                qg.rmsnorm(x[r:], x_type, k, w, 1e-5, n, k, residual=res[r:], res_type=res_type, ldr=k, sum=s[r:], lds=k, y=y[r:], ldy=k,
+                           q_type=q_type, q=q[r:], ldq=k, q_scales=qs[r:])
+            outs.append((s, y, q, qs))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*outs)), q_type
+        assert outs[0][1].float().abs().amax(1).min() > 0
+
+
+@pytest.mark.parametrize("rows,k", [(6200, 520), (6203, 1024), (8197, 72), (1300, 1032)])
+@pytest.mark.parametrize("s_type", [BF, F32])
+def test_backward_of_rows_in_turn(rows, k, s_type):
+    """512 workgroups of one or of four rows."""
+    test_backward(rows, k, s_type, True)
