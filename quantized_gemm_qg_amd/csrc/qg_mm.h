@@ -241,8 +241,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(typename C::Args a) {
   const int rows = min(C::BM, a.m - m0);
   static_assert(C::EPI != kXentGrad || C::THREADS >= C::BM, "a thread per row");
   f32x4 my_row = {0.f, 0.f, 0.f, 0.f};  // kXentGrad: what the epilogue needs of this thread's row
-  __shared__ float most_of[C::EPI == kXentGrad ? C::WAVES : 1];
-  float dloss_most = 0.f;
+  float dloss_most = 0.f;  // the wave's, then the workgroup's
   if constexpr (C::EPI == kXentGrad) {
     // (every workgroup looks for the largest |dloss| of the rows that count: a launch
     // of its own for it took 5 us)
@@ -253,7 +252,7 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(typename C::Args a) {
       for (int r = threadIdx.x; r < a.m; r += C::THREADS) dloss_most = fmaxf(dloss_most, fabsf(dloss_of(r)));
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) dloss_most = fmaxf(dloss_most, __shfl_xor(dloss_most, off));
-    if (lane == 0) most_of[wave] = dloss_most;
+    dloss_most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(dloss_most)));
     const int row = min(m0 + (int)threadIdx.x, a.m - 1);
     my_row = f32x4{dloss_of(row), a.lse[row] * 1.4426950408889634f, __int_as_float(a.targets[row] - a.first_token), 0.f};
   }
@@ -476,14 +475,6 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(typename C::Args a) {
   multiply(f[0]);
   multiply(f[1]);
 
-  if constexpr (C::EPI == kXentGrad) {
-    // (the loop's barriers lie between most_of's writes and this)
-    for (int w = 0; w < C::WAVES; ++w) dloss_most = fmaxf(dloss_most, most_of[w]);
-    const float c = dloss_most >= 0x1p-126f && dloss_most < INFINITY ? dloss_most : 1.f;
-    my_row[0] /= c;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.alpha_out[0] = a.scale * c;
-  }
-
   if constexpr (C::SPLIT && C::EPI != kParts) {
     if (a.splits > 1) {
       // Publish this part of k (agent-scope stores, complete before the counter
@@ -623,6 +614,16 @@ __global__ __launch_bounds__(C::THREADS) void mm_kernel(typename C::Args a) {
   // kXentGrad: per row its weight, the logarithm (base 2) of its sum and its target
   float *row_info = (float *)(smem + C::WAVES * C::SLAB);  // [BM][4]
   if constexpr (C::EPI == kXentGrad) {
+    // (in the slabs' place, not in LDS of its own: 32 bytes more left one workgroup of
+    // 32 x 128 on a CU instead of two; backward pass of 16 tokens, 100003 x 2048: 263 us
+    // against 273)
+    float *most_of = (float *)smem;
+    if (lane == 0) most_of[wave] = dloss_most;
+    mm_barrier();
+    for (int w = 0; w < C::WAVES; ++w) dloss_most = fmaxf(dloss_most, most_of[w]);
+    const float c = dloss_most >= 0x1p-126f && dloss_most < INFINITY ? dloss_most : 1.f;
+    my_row[0] /= c;
+    if (tm == 0 && tn == 0 && threadIdx.x == 0) a.alpha_out[0] = a.scale * c;
     if (threadIdx.x < C::BM) *(f32x4 *)(row_info + 4 * threadIdx.x) = my_row;
     mm_barrier();
   }
@@ -774,7 +775,8 @@ struct MmPlan {
   int splits = 1, per = 0;
   double cost = 0;
 };
-// Workgroups of a shape that a CU holds.
+// Workgroups of a shape that a CU holds (the kernels have no LDS but what the launch
+// asks for).
 template <class C>
 constexpr int64_t kMmResident = 160 * 1024 / C::LDS;
 constexpr int64_t kMmMostSplits = 32;

@@ -37,3 +37,10 @@ def test_only_the_written_out_copies_use_m0(compiled):
 
 def test_the_device_code_compiles_without_warnings(compiled):
     assert compiled[1] == ""
+
+
+def test_the_products_have_no_lds_but_their_ring(compiled):
+    """How many workgroups of a shape a CU holds is counted from the LDS that the launch asks for."""
+    fixed = dict(re.findall(r"\.amdhsa_kernel (\S+)\n\s*\.amdhsa_group_segment_fixed_size (\d+)", compiled[0]))
+    assert fixed
+    assert {name: n for name, n in fixed.items() if "mm_kernel" in name and n != "0"} == {}
