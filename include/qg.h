@@ -694,8 +694,10 @@ qg_status qg_lora(const void *x, int64_t ldx, const void *a, int64_t lda, const 
  *           pass.
  *   ws      qg_linear_xent_workspace_size bytes (enough for every smaller m too),
  *           256-B aligned, zero-filled once (its first 64 KiB suffice).
- * NaN in a row of x, or an infinite logit, gives NaN in that row alone.  m == 0 is
- * a no-op.  Sums are in a fixed order.  Asynchronous on `stream`. */
+ * A logit of -inf is a token of probability 0 (loss +inf where it is the target).  NaN
+ * in a row of x or a logit of +inf gives NaN in that row alone, nothing but -inf an lse
+ * of -inf and a loss of NaN.  m == 0 is a no-op.  Sums are in a fixed order.
+ * Asynchronous on `stream`. */
 qg_status qg_linear_xent_workspace_size(int64_t m, int64_t k, int64_t vocab, uint64_t *bytes);
 qg_status qg_linear_xent(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t k, int64_t vocab,
                          const int32_t *targets, float scale, float *loss, float *lse, void *ws, uint64_t ws_bytes,

@@ -346,3 +346,52 @@ MORE_TILES = [(3589, 1280, 1574)]   # dw in parts of two stages
 @pytest.mark.parametrize("m,k,vocab", MORE_TILES)
 def test_more_tile_shapes(m, k, vocab):
     test_forward_and_backward(m, k, vocab)
+
+
+@pytest.mark.parametrize("m,vocab", [(5, 300), (150, 700), (700, 3001)])
+def test_infinite_logits(m, vocab):
+    """-inf: a token of probability 0.  +inf, or nothing but -inf: NaN losses, in those rows alone."""
+    big, k = 2.0 ** 100, 72
+
+    def edit(c):
+        c.w[:, :2] = (torch.randn(vocab, 2, device="cuda") / big).to(torch.bfloat16)
+        c.w[5, 0], c.w[9, 1], c.w[:, 2] = -big, big, -big
+        c.x[:, :3] = 0
+        c.x[:5] = 0
+        c.x[0, 0] = c.x[1, 0] = c.x[2, 1] = c.x[3, 2] = big   # one of -inf, the same, one of +inf, all of -inf
+        c.x[4, 3] = 1
+        c.targets[:5] = torch.tensor([7, 5, 7, 7, 7], dtype=torch.int32)
+
+    c = Case(m, k, vocab, seed=m, edit=edit)
+    c.solve()
+    loss, lse = c.forward()
+    ordinary = torch.arange(m, device="cuda") > 3
+    ordinary[0] = True
+    z = c.z.clone()
+    z[:2, 5] = -float("inf")
+    e_z = c.e_z.clone()
+    e_z[:2, 5] = 0
+    for row in (0, 1):
+        want = torch.logsumexp(z[row], 0)
+        e = e_z[row].max() + (200 + vocab / 2048 + 40) * U32 + 2 * U32 * want.abs()
+        assert abs(lse[row].item() - want) <= e
+    assert abs(loss[0].item() - (torch.logsumexp(z[0], 0) - z[0, 7])) <= 2 * e_z[0].max() + 300 * U32 + 8 * U32 * z[0].abs()[z[0] > -1e30].max()
+    assert loss[1] == float("inf")
+    assert loss[2].isnan() and lse[2].isnan() and loss[3].isnan() and lse[3] == -float("inf")
+    rest = ordinary.clone()
+    rest[0] = False
+    within(lse[rest], c.lse[rest], c.e_lse[rest])
+    within(loss[rest], c.loss[rest], c.e_loss[rest])
+    # gradients without the rows of NaN: d is that of the other tokens
+    c.targets[2], c.targets[3] = -1, -1
+    dx, dw = c.backward(lse)
+    p = torch.exp(z[:2] - torch.logsumexp(z[:2], 1, keepdim=True))
+    p[0, 7] -= 1
+    p[1, 5] -= 1
+    d = c.dloss[:2, None].to(D) * p
+    want = torch.mm(d, c.w.to(D))[:, 4:]
+    bound = (2 * U16) * torch.mm(d.abs() + 1e-6, c.w.to(D).abs())[:, 4:]
+    within(dx[:2, 4:], want, bound + U16 * want.abs())
+    assert (dx[2:4] == 0).all() and dx[rest.nonzero()[:, 0], 4:].isfinite().all() and dw[:, 4:].isfinite().all()
+    # the target of the second row, whose logit is -inf, has the whole of its gradient (the first column: rows 0 and 1 alone)
+    assert abs(dw[5, 0].item() / big + c.dloss[1].item()) <= 2 * U16 * c.dloss[1].item()
