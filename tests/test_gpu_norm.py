@@ -4,6 +4,7 @@ against the formulas in 64 bits and, for the gradients, against differences.
 Tolerances: fp32 sums of k terms are within k roundings (2^-24) of the sum of the
 terms' magnitudes, whatever their order; each output is rounded once (half a
 step: bf16 2^-8, e4m3 2^-4 of the value, int8 half a unit)."""
+import numpy as np
 import pytest
 import torch
 
@@ -343,3 +344,46 @@ def test_rows_in_turn_are_as_rows_apart(rows, k, x_type, res_type):
 def test_backward_of_rows_in_turn(rows, k, s_type):
     """512 workgroups of one or of four rows."""
     test_backward(rows, k, s_type, True)
+
+
+@pytest.mark.parametrize("q_type", [qg.A_INT8_TOKEN, qg.A_FP8_TOKEN, qg.A_FP8_BLOCK])
+def test_codes_by_the_reciprocal_and_by_division(q_type):
+    """The codes are the nearest to y times the scale's reciprocal, bit for bit; the quantizers divide.  Rows of
+    small whole numbers, whose sums are exact, so that y is known to the last bit.
+
+    y and the row's largest |y| are off by 2^-24 of themselves, so is the scale; the quotient adds one rounding
+    more, the reciprocal two: codes differ only where the quotient of the exact numbers is within 5 2^-24 of itself
+    from a tie of two codes, and then by one.  (Evenly spread quotients: 2 * 127 * 5 * 2^-24 = 8e-5 of them for
+    int8, 2 * 16 * 5 * 2^-24 = 1e-5 for e4m3; products of small numbers as here meet ties more often.)"""
+    rows, k, eps = 64, 4096, 1e-5
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randint(-32, 33, (rows, k), generator=gen).to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn(k, generator=gen)).to(torch.bfloat16)
+    q = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    per = k // 128 if q_type == qg.A_FP8_BLOCK else 1
+    qs = torch.zeros(rows, per, device="cuda")
+    qg.rmsnorm(x.cuda(), BF, k, w.cuda(), eps, rows, k, q_type=q_type, q=q, ldq=k, q_scales=qs, y=None)
+    torch.cuda.synchronize()
+    # (numpy, whose square root and quotients are correctly rounded, as the kernel's are)
+    one = np.float32(1)
+    s, wf = x.float().numpy(), w.float().numpy()
+    r = one / np.sqrt((s * s).sum(1, keepdims=True) / np.float32(k) + np.float32(eps))
+    y = ((s * wf) * r).reshape(rows, per, k // per)
+    most = np.abs((s * wf).reshape(rows, per, -1)).max(2, keepdims=True) * r[:, None]
+    scale = most / np.float32(127 if q_type == qg.A_INT8_TOKEN else 448)
+    assert np.array_equal(qs.cpu().numpy(), scale[:, :, 0])
+
+    def codes(t):
+        if q_type == qg.A_INT8_TOKEN:
+            return torch.from_numpy(t).round().to(torch.int8).view(torch.uint8).view(rows, k)
+        return torch.from_numpy(t).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).view(rows, k)
+
+    assert torch.equal(q.cpu(), codes(y * (one / scale)))
+    step = (q.cpu().view(torch.int8).int() - codes(y / scale).view(torch.int8).int()).abs()
+    assert step.max() <= 1
+    sw = (x.double() * w.double()).view(rows, per, -1)
+    exact = ((127 if q_type == qg.A_INT8_TOKEN else 448) * sw / sw.abs().amax(2, keepdim=True)).view(rows, k)
+    unit = torch.ones_like(exact) if q_type == qg.A_INT8_TOKEN else torch.exp2(torch.floor(torch.log2(exact.abs())).clamp_min(-6) - 3)
+    near = ((exact / unit - torch.floor(exact / unit) - 0.5).abs() * unit) <= 5 * 2.0 ** -24 * exact.abs()
+    print(f"codes that differ: {int((step > 0).sum())} of {step.numel()}, near a tie: {int(near.sum())}", flush=True)
+    assert not ((step > 0) & ~near).any()
