@@ -497,6 +497,10 @@ LoraPlan lora_plan(int64_t m, int64_t k, int64_t n, int adapters, int rank, bool
   // Many rows: workgroups side by side a multiple of the XCDs, each of which then
   // reads its own columns of B (4096 rows, n 14336, rank 64: 8 side by side 54.9 us,
   // 10 67.5, 19 62.3, 56 64.4; 44 rows of 35 adapters: 56 11.4, 28 8.3, 19 9.1).
+  // `places` are those of ranks up to 64.  Above, the parts of t take up to 117 KB and
+  // leave one workgroup of 64 rows to a CU; the same chunks were kept there without a
+  // measurement of others (4096 rows, n 14336, both launches, bf16 and fp32 y: rank 64 104
+  // and 138 us, 128 162 and 192, 256 273 and 318).
   const double expected = (double)m / (16 * p.rb) + 0.5 * (double)std::min<int64_t>(adapters, m);
   const int places = 256 * (p.rb == 4 ? (y_f32 ? 2 : 3) : p.rb == 2 ? (y_f32 ? 3 : 4) : 5);
   double best = 0;

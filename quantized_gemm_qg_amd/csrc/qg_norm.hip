@@ -11,7 +11,13 @@
 // is rounded once, to bf16 and from fp32 to the codes.
 // Bound by HBM from about 100 MB on: 16384 x 4096 with the residual, bf16 and MXFP8 out
 // 117 us (606 MB, 5.2 TB/s); 4096 x 4096 forward 26 and backward 25 us; below, by a
-// launch and two memory latencies (one row of 4096 3.5 us, 1001 x 2080 8.1 us).
+// launch and two memory latencies (one row of 4096 3.5 us, 1001 x 2080 8.1 us).  Rows of
+// other lengths, bf16 with the residual, 268 MB, TB/s forward and backward with dw (a
+// copy 5.2): 256 4.8 and 3.1, 512 and 1024 5.0 and 4.8, 2048 5.1 and 4.2, 4096 5.3 and
+// 4.7, 8192 5.4 and 4.4, 12288 5.2 and 4.1, 14336 4.5 and 3.8, 16384 4.3 and 3.8, 32768 and
+// 65536 3.8 and 2.2.  Above 12288 values a workgroup of 13 to 16 waves has a CU for
+// itself and asks for nothing of the next row while it stores one; longer rows are read
+// twice, and their backward kernels spill 17 (bf16) and 34 (fp32) registers.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -422,7 +428,9 @@ hipError_t launch_rmsnorm(const NormArgs &a, bool x_f32, int res, hipStream_t s)
   return hipGetLastError();
 }
 
-// Rows of `partial`: one per workgroup, at most 64 MB of them.
+// Rows of `partial`: one per workgroup, at most 512 and at most 64 MB of them.  (The
+// grid is the same without dw.  512 workgroups of one-wave rows leave too little in
+// flight below 512 values, see the rates above.)
 int64_t rmsnorm_back_parts(int64_t rows, int64_t k) {
   const int64_t most = std::max<int64_t>((64ll << 20) / (4 * k), 1), teams = k <= 1024 ? 4 : 1;
   return std::min<int64_t>(std::min<int64_t>((rows + teams - 1) / teams, 512), most);

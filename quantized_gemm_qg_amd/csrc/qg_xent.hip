@@ -6,7 +6,8 @@
 // of exponentials; a small kernel joins them.  Backward: pieces of the vocabulary
 // whose d (bf16) stays in the last-level cache, per piece the product again with d
 // as its epilogue, then one product for dx (summed over the pieces in fp32) and one
-// for the piece's rows of dW.
+// for the piece's rows of dW.  (W does not stay there: up to a few hundred tokens
+// have one piece, W is the larger operand and comes from HBM for d and again for dx.)
 // d is rounded to bf16 because the matrix cores take bf16.  So that the target's
 // entry, the largest of its row, is rounded as little as possible, d holds
 // dloss / c with c the largest |dloss|: under a mean over tokens these weights are
@@ -118,7 +119,7 @@ static int64_t xent_halves(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 0; 
 int64_t xent_d_rows(int64_t m) { return m + xent_halves(m); }
 
 // Columns of a piece: d takes up to 128 MB, half of the last-level cache, in which both
-// products find it, and at least 8192 columns (the products over a piece would be
+// products find it (W's rows are not counted), and at least 8192 columns (the products over a piece would be
 // short).
 int64_t xent_piece(int64_t m, int64_t vocab) {
   int64_t most = (64ll << 20) / std::max<int64_t>(m, 1);
